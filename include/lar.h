@@ -11,7 +11,10 @@
  * with variants for per-token pool slots (gdn_decode_tokens, kda_decode_tokens),
  * token-major spans of any length per sequence (gdn_decode_varlen,
  * kda_decode_varlen, la_decode_varlen) and the chunked form of the latter for
- * long spans (gdn_prefill, kda_prefill, la_prefill).  The chunked calls also set their
+ * long spans (gdn_prefill, kda_prefill, la_prefill).  Around them stand the short
+ * causal convolution in front of such a layer (conv_*), a further recurrent form,
+ * the selective state space scan (ssm_*), and the verification of drafted tokens
+ * that makes the accepted counts (spec_verify).  The chunked calls also set their
  * kernel's shared-memory limit (a function attribute) on every call; capturing
  * them into a CUDA graph has not been tested (the other calls' capture and
  * replay are).
@@ -132,6 +135,12 @@ enum {
     LAR_STATE_KV = 1u << 3   /* pool and inter hold S as [k][v] (v fastest), see below */
 };
 
+/* flags for conv_* and ssm_* */
+enum {
+    LAR_SILU = 1u << 4,       /* conv_*: out <- y / (1 + exp(-y)), in kernel */
+    LAR_DT_SOFTPLUS = 1u << 5 /* ssm_*: dt <- softplus(dt + dt_bias), in kernel */
+};
+
 /* bits OR-ed into *dev_err */
 enum {
     LAR_DEVERR_READ_SLOT = 1,  /* some read_idx[b] >= P (that entry started from zero) */
@@ -139,8 +148,12 @@ enum {
     LAR_DEVERR_ACCEPTED = 4,   /* some num_accepted[b] outside [1, T] (that entry started from zero) */
     LAR_DEVERR_SEQLEN = 8,     /* varlen: some span cu_seqlens[n]..[n+1] reversed or past the token
                                   arrays (treated as empty: the read state goes to the write slot) */
-    LAR_DEVERR_TIMEOUT = 16    /* chunked prefill: a bounded wait for the tensor cores gave up; that
+    LAR_DEVERR_TIMEOUT = 16,   /* chunked prefill: a bounded wait for the tensor cores gave up; that
                                   (sequence, head) skipped the rest of its span and its writeback */
+    LAR_DEVERR_DRAFT = 32,     /* spec_verify: some drafted token outside [0, V) (rejected), or some
+                                  num_draft[b] outside [0, T - 1] (taken as the nearer end) */
+    LAR_DEVERR_PROBS = 64      /* spec_verify: some row to draw from has no positive finite weight
+                                  (its token is -1) */
 };
 
 /*
@@ -330,6 +343,116 @@ lar_status la_prefill(const lar_tensor* q, const lar_tensor* k, const lar_tensor
                       const lar_tensor* cu_seqlens, const lar_tensor* read_idx,
                       const lar_tensor* write_idx, const lar_tensor* out, float scale,
                       int32_t* dev_err, void* stream);
+
+/*
+ * Short causal convolution over the tokens of a sequence, one filter a channel,
+ * as it stands in front of the recurrent layers' q, k and v:
+ *     y[t][c] = bias[c] + sum_{j < W} weight[c][j] x[t - (W - 1) + j][c]
+ * and out = y, or y / (1 + exp(-y)) with LAR_SILU.  A sequence's state is its last
+ * W - 1 inputs; inputs before its first token come from the state it starts from.
+ *   x, out   [B, T, C] (rank 2 [B, C] means T = 1), T from 1 to 16; fp32 or bf16,
+ *            any strides (out: no two elements at one address).  conv_prefill:
+ *            packed spans, [Ntok, C].
+ *   weight   [C, W], W from 2 to 4; bias [C] or NULL; fp32 or bf16, any strides.
+ *   pool     fp32 or bf16 [P, W - 1, C], channel stride 1, any slot and row
+ *            strides: row j of a slot is the input W - 1 - j tokens before the
+ *            next one.  Inputs enter the pool rounded to its type.
+ *   read_idx, write_idx, num_accepted, state_idx, cu_seqlens   as in gdn_decode,
+ *            gdn_decode_tokens and gdn_decode_varlen: negative read slots are a
+ *            zero state, negative write slots skip the store, slots >= P and bad
+ *            counts or spans are flagged in *dev_err; B and N <= 65535.
+ *            conv_prefill with an empty span copies the read state.
+ *   C        from 1 to 2^24.
+ * Channels that are contiguous, a multiple of 8, with 16-byte aligned rows move in
+ * 16-byte accesses; other layouts element by element.
+ * Ownership, streams, errors and aliasing as for the decode calls above: pool and
+ * out overlap nothing else of the call, entries name distinct write slots and read
+ * no slot that another entry writes; an entry may read a slot that it writes.
+ */
+lar_status conv_decode(const lar_tensor* x, const lar_tensor* weight, const lar_tensor* bias,
+                       const lar_tensor* pool, const lar_tensor* read_idx, const lar_tensor* write_idx,
+                       const lar_tensor* out, uint32_t flags, int32_t* dev_err, void* stream);
+
+lar_status conv_decode_tokens(const lar_tensor* x, const lar_tensor* weight, const lar_tensor* bias,
+                              const lar_tensor* pool, const lar_tensor* read_idx,
+                              const lar_tensor* num_accepted, const lar_tensor* state_idx,
+                              const lar_tensor* out, uint32_t flags, int32_t* dev_err, void* stream);
+
+lar_status conv_prefill(const lar_tensor* x, const lar_tensor* weight, const lar_tensor* bias,
+                        const lar_tensor* pool, const lar_tensor* cu_seqlens, const lar_tensor* read_idx,
+                        const lar_tensor* write_idx, const lar_tensor* out, uint32_t flags,
+                        int32_t* dev_err, void* stream);
+
+/*
+ * Selective state space scan: per channel d a state h of N numbers, with a decay
+ * and an input row that every token sets anew.  Per token
+ *     s      = softplus(dt[d] + dt_bias[d]) with LAR_DT_SOFTPLUS, else dt[d]
+ *     h[n]  <- exp(s A[d][n]) h[n] + s x[d] B[g][n]
+ *     y      = sum_n C[g][n] h[n] + D[d] x[d];   out = y z / (1 + exp(-z))
+ * without z: out = y; without D (NULL): no skip term.  g = d / (Dch / G), Dch
+ * channels in G groups (G divides Dch).
+ *   x, dt, z, out   [B, T, Dch] (rank 2 for T = 1), T from 1 to 16; ssm_prefill:
+ *            [Ntok, Dch].  fp32 or bf16, any strides (out: no two elements at one
+ *            address); z may be NULL.
+ *   A        fp32 [Dch, N], any strides (usually negative); N 16, 32, 64 or 128.
+ *   B, C     [B, T, G, N] (rank 3 [B, G, N] for T = 1; packed [Ntok, G, N]), fp32
+ *            or bf16, any strides.
+ *   D        fp32 [Dch] or NULL.
+ *   dt_bias  fp32 [Dch] or NULL; must be NULL without LAR_DT_SOFTPLUS.
+ *   pool     fp32 or bf16 [P, Dch, N], state stride 1, 16-byte aligned with slot
+ *            and channel strides that are multiples of 16 bytes.  The arithmetic
+ *            is fp32; a bf16 state is rounded to nearest even once per store.
+ *   read_idx, write_idx, num_accepted, state_idx, cu_seqlens   as for conv_*.
+ *   Dch      from 1 to 2^24.
+ */
+lar_status ssm_decode(const lar_tensor* x, const lar_tensor* dt, const lar_tensor* A, const lar_tensor* B,
+                      const lar_tensor* C, const lar_tensor* D, const lar_tensor* z,
+                      const lar_tensor* dt_bias, const lar_tensor* pool, const lar_tensor* read_idx,
+                      const lar_tensor* write_idx, const lar_tensor* out, uint32_t flags,
+                      int32_t* dev_err, void* stream);
+
+lar_status ssm_decode_tokens(const lar_tensor* x, const lar_tensor* dt, const lar_tensor* A,
+                             const lar_tensor* B, const lar_tensor* C, const lar_tensor* D,
+                             const lar_tensor* z, const lar_tensor* dt_bias, const lar_tensor* pool,
+                             const lar_tensor* read_idx, const lar_tensor* num_accepted,
+                             const lar_tensor* state_idx, const lar_tensor* out, uint32_t flags,
+                             int32_t* dev_err, void* stream);
+
+lar_status ssm_prefill(const lar_tensor* x, const lar_tensor* dt, const lar_tensor* A, const lar_tensor* B,
+                       const lar_tensor* C, const lar_tensor* D, const lar_tensor* z,
+                       const lar_tensor* dt_bias, const lar_tensor* pool, const lar_tensor* cu_seqlens,
+                       const lar_tensor* read_idx, const lar_tensor* write_idx, const lar_tensor* out,
+                       uint32_t flags, int32_t* dev_err, void* stream);
+
+/*
+ * Verification of drafted tokens against the target model's probabilities, from
+ * given random numbers.  A step of T tokens holds the last token known and k
+ * drafted ones d_0 .. d_{k-1}, drawn from q_0 .. q_{k-1}; p_t is the target's
+ * distribution at the place of d_t, p_k the one behind all of them.
+ *     d_t is accepted if every draft before it is and u_accept[t] q_t(d_t) < p_t(d_t)
+ *     n drafts accepted;  w = max(p_n - q_n, 0) if n < k, p_k if n = k
+ *     next token: the first i with w[0] + .. + w[i] > u_sample (w[0] + .. + w[V - 1])
+ * An empty residual (w all zero) is replaced by p_n.
+ *   draft_tokens  int32/int64 [B, T - 1]; a token outside [0, V) is rejected.
+ *   draft_probs   fp32 or bf16 [B, T - 1, V], or NULL: each draft was its model's
+ *                 choice (q_t is 1 at d_t, 0 elsewhere).
+ *   target_probs  fp32 or bf16 [B, T, V]; T from 1 to 16, V from 1 to 2^24.
+ *   u_accept, u_sample   fp32 [B, T - 1], [B], in [0, 1).
+ *   num_draft     int32/int64 [B] or NULL: k of each sequence, 0 to T - 1 (NULL:
+ *                 T - 1); drafts behind it are not looked at.
+ *   num_accepted  out, int32 or int64 [B]: n + 1, the tokens of the step that stand
+ *                 (what *_decode_tokens take as num_accepted in the next step).
+ *   tokens        out, int32 or int64 [B, T]: the accepted drafts, the next token,
+ *                 then -1.
+ * Any strides.  A weight that is not a positive finite number counts as 0; sums are
+ * held to about 2^-48 of their value (weights up to 2^64), so that the index is the
+ * one that exact sums give.
+ */
+lar_status spec_verify(const lar_tensor* draft_tokens, const lar_tensor* draft_probs,
+                       const lar_tensor* target_probs, const lar_tensor* u_accept,
+                       const lar_tensor* u_sample, const lar_tensor* num_draft,
+                       const lar_tensor* num_accepted, const lar_tensor* tokens, int32_t* dev_err,
+                       void* stream);
 
 /* Static, human-readable name of a status code. */
 const char* lar_status_string(lar_status status);

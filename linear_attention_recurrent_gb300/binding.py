@@ -1,4 +1,4 @@
-"""ctypes binding over liblar.so: the same three calls as include/lar.h, taking
+"""ctypes binding over liblar.so: the calls of include/lar.h, taking
 torch tensors.  Marshalling only -- every step of the decode runs in the CUDA
 kernels behind the C ABI; there is no Python or CPU fallback.  A missing
 library, a CPU tensor or a non-OK status raises.
@@ -16,8 +16,9 @@ _LIB_PATH = _build.LIB
 
 LAR_F32, LAR_BF16, LAR_I32, LAR_I64 = 0, 1, 2, 3
 LAR_QK_L2NORM, LAR_GATE_RAW, LAR_BETA_RAW, LAR_STATE_KV = 1, 2, 4, 8
+LAR_SILU, LAR_DT_SOFTPLUS = 16, 32
 LAR_DEVERR_READ_SLOT, LAR_DEVERR_WRITE_SLOT, LAR_DEVERR_ACCEPTED, LAR_DEVERR_SEQLEN = 1, 2, 4, 8
-LAR_DEVERR_TIMEOUT = 16
+LAR_DEVERR_TIMEOUT, LAR_DEVERR_DRAFT, LAR_DEVERR_PROBS = 16, 32, 64
 
 STATUS = {0: "LAR_OK", 1: "LAR_ERR_NULL", 2: "LAR_ERR_DTYPE", 3: "LAR_ERR_RANK",
           4: "LAR_ERR_SHAPE", 5: "LAR_ERR_STRIDE", 6: "LAR_ERR_ALIGN", 7: "LAR_ERR_ARG",
@@ -78,6 +79,13 @@ def load() -> ctypes.CDLL:
             fn.argtypes = [P] * 12 + tail
         lib.la_prefill.restype = ctypes.c_int
         lib.la_prefill.argtypes = [P] * 9 + [ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]
+        for name, n in (("conv_decode", 7), ("conv_decode_tokens", 8), ("conv_prefill", 8), ("ssm_decode", 12),
+                        ("ssm_decode_tokens", 13), ("ssm_prefill", 13)):
+            fn = getattr(lib, name)
+            fn.restype = ctypes.c_int
+            fn.argtypes = [P] * n + [ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]
+        lib.spec_verify.restype = ctypes.c_int
+        lib.spec_verify.argtypes = [P] * 8 + [ctypes.c_void_p, ctypes.c_void_p]
         lib.lar_status_string.restype = ctypes.c_char_p
         lib.lar_status_string.argtypes = [ctypes.c_int]
         _lib = lib
@@ -302,17 +310,136 @@ def _varlen(name, q, k, v, gates, pool, cu_seqlens, read_idx, write_idx, out, in
     return out
 
 
+# The tensors of the conv_* / ssm_* / spec_verify calls, in the library's order;
+# the slot arguments of a call stand between `pool` and `out`.
+_LAYER = {"conv": ("x", "weight", "bias", "pool"),
+          "ssm": ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "pool")}
+_SLOTS = {"decode": ("read_idx", "write_idx"), "decode_tokens": ("read_idx", "num_accepted", "state_idx"),
+          "prefill": ("cu_seqlens", "read_idx", "write_idx")}
+_VERIFY = ("draft_tokens", "draft_probs", "target_probs", "u_accept", "u_sample", "num_draft", "num_accepted",
+           "tokens")
+
+
+def _layer_flags(silu, dt_softplus):
+    return (LAR_SILU if silu else 0) | (LAR_DT_SOFTPLUS if dt_softplus else 0)
+
+
+def _layer(form, kind, tensors, flags, dev_err, out_dtype, stream):
+    """One conv_* or ssm_* call; `tensors` by name."""
+    lib = load()
+    name = f"{form}_{kind}"
+    if tensors["out"] is None:
+        x = tensors["x"]
+        tensors["out"] = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    ts = [tensors[n] for n in _LAYER[form] + _SLOTS[kind] + ("out",)]
+    dev = _device_of(ts, dev_err, stream)
+    ds = [describe(t) for t in ts]
+    err = dev_err.data_ptr() if dev_err is not None else None
+    with torch.cuda.device(dev):
+        st = getattr(lib, name)(*[_ref(d) for d in ds], flags, err, _stream(stream, dev))
+    _check(name, st)
+    return tensors["out"]
+
+
+def conv_decode(x, weight, pool, read_idx, write_idx=None, *, bias=None, out=None, silu=False, dev_err=None,
+                out_dtype=None, stream=None):
+    """Short causal convolution of x [B, T, C] (or [B, C]) with weight [C, W]
+    after the W - 1 inputs in slot read_idx[b] of pool [P, W - 1, C]; the last
+    W - 1 inputs go to slot write_idx[b].  silu: out = y / (1 + exp(-y))."""
+    return _layer("conv", "decode", dict(x=x, weight=weight, bias=bias, pool=pool, read_idx=read_idx,
+                                         write_idx=write_idx, out=out), _layer_flags(silu, False), dev_err, out_dtype,
+                  stream)
+
+
+def conv_decode_tokens(x, weight, pool, state_idx, *, read_idx=None, num_accepted=None, bias=None, out=None,
+                       silu=False, dev_err=None, out_dtype=None, stream=None):
+    """conv_decode with per-token pool slots (see gdn_decode_tokens)."""
+    return _layer("conv", "decode_tokens", dict(x=x, weight=weight, bias=bias, pool=pool, read_idx=read_idx,
+                                                num_accepted=num_accepted, state_idx=state_idx, out=out),
+                  _layer_flags(silu, False), dev_err, out_dtype, stream)
+
+
+def conv_prefill(x, weight, pool, cu_seqlens, read_idx, write_idx=None, *, bias=None, out=None, silu=False,
+                 dev_err=None, out_dtype=None, stream=None):
+    """conv_decode over packed spans: x [Ntok, C], sequence n owning tokens
+    cu_seqlens[n] .. cu_seqlens[n+1]-1 (other rows of out are left as allocated)."""
+    return _layer("conv", "prefill", dict(x=x, weight=weight, bias=bias, pool=pool, cu_seqlens=cu_seqlens,
+                                          read_idx=read_idx, write_idx=write_idx, out=out),
+                  _layer_flags(silu, False), dev_err, out_dtype, stream)
+
+
+def ssm_decode(x, dt, A, B, C, pool, read_idx, write_idx=None, *, D=None, z=None, dt_bias=None, out=None,
+               dt_softplus=False, dev_err=None, out_dtype=None, stream=None):
+    """Selective state space step: h <- exp(dt A) h + dt x B, out = (C h + D x)
+    silu(z), for x, dt, z [B, T, Dch] (or [B, Dch]), A [Dch, N], B and C
+    [B, T, G, N]; states in pool [P, Dch, N].  dt_softplus: dt is
+    softplus(dt + dt_bias)."""
+    return _layer("ssm", "decode", dict(x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, pool=pool,
+                                        read_idx=read_idx, write_idx=write_idx, out=out),
+                  _layer_flags(False, dt_softplus), dev_err, out_dtype, stream)
+
+
+def ssm_decode_tokens(x, dt, A, B, C, pool, state_idx, *, read_idx=None, num_accepted=None, D=None, z=None,
+                      dt_bias=None, out=None, dt_softplus=False, dev_err=None, out_dtype=None, stream=None):
+    """ssm_decode with per-token pool slots (see gdn_decode_tokens)."""
+    return _layer("ssm", "decode_tokens", dict(x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, pool=pool,
+                                               read_idx=read_idx, num_accepted=num_accepted, state_idx=state_idx,
+                                               out=out),
+                  _layer_flags(False, dt_softplus), dev_err, out_dtype, stream)
+
+
+def ssm_prefill(x, dt, A, B, C, pool, cu_seqlens, read_idx, write_idx=None, *, D=None, z=None, dt_bias=None,
+                out=None, dt_softplus=False, dev_err=None, out_dtype=None, stream=None):
+    """ssm_decode over packed spans: x, dt, z [Ntok, Dch], B and C [Ntok, G, N]
+    (rows of out outside every span are left as allocated)."""
+    return _layer("ssm", "prefill", dict(x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, pool=pool,
+                                         cu_seqlens=cu_seqlens, read_idx=read_idx, write_idx=write_idx, out=out),
+                  _layer_flags(False, dt_softplus), dev_err, out_dtype, stream)
+
+
+def spec_verify(draft_tokens, target_probs, u_accept, u_sample, *, draft_probs=None, num_draft=None,
+                num_accepted=None, tokens=None, dev_err=None, stream=None):
+    """Verify drafted tokens [B, T - 1] against target_probs [B, T, V] with the
+    random numbers u_accept [B, T - 1] and u_sample [B].  Returns (num_accepted
+    [B], tokens [B, T]): the tokens of the step that stand, as *_decode_tokens
+    take them next, and the accepted drafts, the next token, then -1.
+    draft_probs None: the drafts were their model's choices (probability 1)."""
+    lib = load()
+    if num_accepted is None:
+        num_accepted = torch.empty(target_probs.shape[0], dtype=torch.int32, device=target_probs.device)
+    if tokens is None:
+        tokens = torch.empty(target_probs.shape[:2], dtype=draft_tokens.dtype, device=target_probs.device)
+    ts = (draft_tokens, draft_probs, target_probs, u_accept, u_sample, num_draft, num_accepted, tokens)
+    dev = _device_of(ts, dev_err, stream)
+    ds = [describe(t) for t in ts]
+    err = dev_err.data_ptr() if dev_err is not None else None
+    with torch.cuda.device(dev):
+        st = lib.spec_verify(*[_ref(d) for d in ds], err, _stream(stream, dev))
+    _check("spec_verify", st)
+    return num_accepted, tokens
+
+
 class PreparedCall:
     """A decode call whose descriptors are built once, for tight launch loops.
     The tensors it was built from must stay alive and keep their storage.
     Passing ``state_idx`` (and ``num_accepted`` or ``read_idx``) selects the
     per-token-slot call (gdn_decode_tokens / kda_decode_tokens); passing
     ``cu_seqlens`` selects the variable-length call (*_decode_varlen), and with
-    ``prefill=True`` the chunked prefill call (gdn_prefill / la_prefill)."""
+    ``prefill=True`` the chunked prefill call (gdn_prefill / la_prefill).
+    Forms "conv" and "ssm" select conv_* / ssm_* the same way (``cu_seqlens``
+    with ``prefill=True``; flags ``silu`` and ``dt_softplus``), form "verify"
+    spec_verify; a name that the call does not take is refused."""
 
     def __init__(self, form, *, scale=1.0, qk_l2norm=False, gate_raw=False, beta_raw=False,
-                 state_kv=False, dev_err=None, stream=None, prefill=False, **tensors):
+                 state_kv=False, silu=False, dt_softplus=False, dev_err=None, stream=None, prefill=False, **tensors):
         lib = load()
+        if form in ("conv", "ssm", "verify"):
+            if scale != 1.0 or qk_l2norm or gate_raw or beta_raw or state_kv:
+                raise ValueError(f"form {form!r} takes neither a scale nor the decode flags")
+            self._prepare_layer(lib, form, tensors, prefill, _layer_flags(silu, dt_softplus), dev_err, stream)
+            return
+        if silu or dt_softplus:
+            raise ValueError("silu and dt_softplus are flags of the forms 'conv' and 'ssm'")
         tokens = tensors.get("state_idx") is not None
         varlen = tensors.get("cu_seqlens") is not None
         if prefill and (not varlen or tensors.get("inter") is not None):
@@ -348,6 +475,26 @@ class PreparedCall:
             self._descs = [describe(tensors.get(n)) for n in names]
             self._args = [_ref(d) for d in self._descs] + [
                 float(scale), _flags(qk_l2norm, gate_raw, beta_raw, state_kv), err, st]
+
+    def _prepare_layer(self, lib, form, tensors, prefill, flags, dev_err, stream):
+        if form == "verify":
+            if prefill or flags:
+                raise ValueError("the verify call takes no flags")
+            self._name, names, tail = "spec_verify", _VERIFY, []
+        else:
+            if prefill != (tensors.get("cu_seqlens") is not None):
+                raise ValueError("packed spans take cu_seqlens and prefill=True together")
+            kind = "prefill" if prefill else ("decode_tokens" if tensors.get("state_idx") is not None else "decode")
+            self._name, names, tail = f"{form}_{kind}", _LAYER[form] + _SLOTS[kind] + ("out",), [flags]
+        extra = [n for n, t in tensors.items() if t is not None and n not in names]
+        if extra:
+            raise ValueError(f"{self._name} takes no {', '.join(sorted(extra))}")
+        self._fn = getattr(lib, self._name)
+        self._keep = (tensors, dev_err)
+        self._dev = _device_of(tensors.values(), dev_err, stream)
+        err = dev_err.data_ptr() if dev_err is not None else None
+        self._descs = [describe(tensors.get(n)) for n in names]
+        self._args = [_ref(d) for d in self._descs] + tail + [err, _stream(stream, self._dev)]
 
     def __call__(self):
         if torch.cuda.current_device() == self._dev.index:

@@ -1,0 +1,144 @@
+// layer_common.cuh -- device helpers shared by the convolution, scan and
+// verification kernels: slot resolution, spans, 8-channel loads and stores.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "decode_kernel.cuh"
+#include "layer_params.h"
+
+namespace lar {
+
+// Order after the previous kernel on the stream (launched with programmatic
+// serialization); its successor may be scheduled from here on.
+__device__ __forceinline__ void stream_order() {
+#if LAR_PDL
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+#endif
+}
+
+template <typename... Kp, typename... Args>
+lar_status launch_ordered(void (*kern)(Kp...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                          const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+#if LAR_PDL
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+#endif
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? LAR_OK : LAR_ERR_LAUNCH;
+}
+
+__device__ __forceinline__ void flag_err(int32_t* word, int32_t bits) {
+    if (word && bits) atomicOr(word, bits);
+}
+
+// The slot that sequence b starts from; -1: a zero state.
+__device__ __forceinline__ int64_t read_slot(const SlotParams& s, int b, int32_t* bits) {
+    int64_t slot;
+    if (s.nacc) {
+        const int64_t n = ld_idx(s.nacc, b * s.na_s, s.na_dt);
+        if (n < 1 || n > s.T) {
+            *bits |= LAR_DEVERR_ACCEPTED;
+            return -1;
+        }
+        slot = ld_idx(s.tslot, b * s.tsl_s[0] + (n - 1) * s.tsl_s[1], s.tsl_dt);
+    } else {
+        slot = ld_idx(s.ridx, b * s.ri_s, s.ri_dt);
+    }
+    if (slot >= s.P) {
+        *bits |= LAR_DEVERR_READ_SLOT;
+        return -1;
+    }
+    return slot;
+}
+
+// The slot that takes the state of sequence b after its token t (per-token
+// slots) or after its last one; -1: none.
+__device__ __forceinline__ int64_t write_slot(const SlotParams& s, int b, int t, int32_t* bits) {
+    const int64_t slot = s.tslot ? ld_idx(s.tslot, b * s.tsl_s[0] + t * s.tsl_s[1], s.tsl_dt)
+                         : s.widx ? ld_idx(s.widx, b * s.wi_s, s.wi_dt)
+                                  : ld_idx(s.ridx, b * s.ri_s, s.ri_dt);
+    if (slot >= s.P) {
+        *bits |= LAR_DEVERR_WRITE_SLOT;
+        return -1;
+    }
+    return slot;
+}
+
+// Span n of a packed call.  A reversed span or one that leaves the token arrays
+// counts as empty.
+__device__ __forceinline__ void span_of(const SlotParams& s, int n, int* begin, int* len, int32_t* bits) {
+    const int64_t a = ld_idx(s.cu, n * s.cu_s, s.cu_dt), e = ld_idx(s.cu, (n + 1) * s.cu_s, s.cu_dt);
+    const bool ok = a >= 0 && a <= e && e <= s.ntok;
+    if (!ok) *bits |= LAR_DEVERR_SEQLEN;
+    *begin = ok ? static_cast<int>(a) : 0;
+    *len = ok ? static_cast<int>(e - a) : 0;
+}
+
+// 8 neighbouring channels as fp32, 16-byte loads; NC: through the read-only path
+// (never for the pool, which the same call writes).
+template <bool NC>
+__device__ __forceinline__ uint4 ld16(const void* p) {
+    return NC ? __ldg(static_cast<const uint4*>(p)) : *static_cast<const uint4*>(p);
+}
+
+__device__ __forceinline__ void unpack8(const uint4 u, float* f) {
+    const unsigned w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+template <bool NC>
+__device__ __forceinline__ void ld8(const void* base, int64_t off, int dt, float* f) {
+    if (dt == LAR_BF16) {
+        unpack8(ld16<NC>(static_cast<const unsigned short*>(base) + off), f);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 u = ld16<NC>(static_cast<const float*>(base) + off + 4 * h);
+            f[4 * h] = __uint_as_float(u.x);
+            f[4 * h + 1] = __uint_as_float(u.y);
+            f[4 * h + 2] = __uint_as_float(u.z);
+            f[4 * h + 3] = __uint_as_float(u.w);
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+__device__ __forceinline__ void st8(void* base, int64_t off, int dt, const float* f) {
+    if (dt == LAR_BF16) {
+        *reinterpret_cast<uint4*>(static_cast<unsigned short*>(base) + off) = pack8(f);
+    } else {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + off);
+        d[0] = make_float4(f[0], f[1], f[2], f[3]);
+        d[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+
+// One element of the pool (a plain load: see ld16).
+__device__ __forceinline__ float ld_pool(const void* base, int64_t off, int dt) {
+    return dt == LAR_F32 ? static_cast<const float*>(base)[off]
+                         : bf16_bits_to_float(static_cast<const unsigned short*>(base)[off]);
+}
+
+// y / (1 + e^-y).  Both SFU steps are good to 2 ulp; where e^-y overflows the
+// quotient is the limit, 0.
+__device__ __forceinline__ float silu_f(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+
+}  // namespace lar

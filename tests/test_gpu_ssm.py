@@ -1,0 +1,300 @@
+"""ssm_decode, ssm_decode_tokens and ssm_prefill against the 64-bit recurrence."""
+import numpy as np
+import pytest
+import torch
+
+import _layer_ref as R
+import linear_attention_recurrent_gb300 as lar
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def inputs(seed, lead, D, N, G, dtype, full=True):
+    """x, dt, A, B, C and the optional D, z, dt_bias on the CPU."""
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    a = dict(x=r(*lead, D).to(dtype), dt=(r(*lead, D) if full else torch.rand(*lead, D, generator=g) * 0.3).to(dtype),
+             A=-torch.exp(r(D, N)), B=r(*lead, G, N).to(dtype), C=r(*lead, G, N).to(dtype))
+    opt = dict(D=r(D), z=(2 * r(*lead, D)).to(dtype), dt_bias=r(D) - 2) if full else {}
+    return g, a, opt
+
+
+def on(d, dev):
+    return {k: v.to(dev) for k, v in d.items()}
+
+
+def ref_of(a, opt, pick, seed):
+    """The reference over the tokens a["x"][pick], from a seed state."""
+    f = lambda t: R.f64(t)[pick]  # noqa: E731
+    return R.ssm_tokens(f(a["x"]), f(a["dt"]), R.f64(a["A"]), f(a["B"]), f(a["C"]), seed,
+                        D=R.f64(opt["D"]) if opt else None, z=f(opt["z"]) if opt else None,
+                        dt_bias=R.f64(opt["dt_bias"]) if opt else None, soft=bool(opt))
+
+
+@pytest.mark.parametrize("B,T,D,N,G,dtype,pdt,full", [
+    (1, 1, 1, 16, 1, F32, F32, True),
+    (3, 1, 64, 16, 1, BF16, F32, True),
+    (2, 1, 257, 16, 1, BF16, BF16, False),
+    (4, 3, 96, 32, 2, F32, F32, True),
+    (2, 16, 40, 64, 4, BF16, F32, True),
+    (5, 2, 36, 128, 3, F32, BF16, False),
+    (2, 2, 128, 128, 128, BF16, F32, True),
+    (66, 1, 520, 16, 1, BF16, F32, True),
+    (67, 2, 24, 32, 1, F32, BF16, True),
+])
+def test_decode(B, T, D, N, G, dtype, pdt, full, cuda_device):
+    dev = cuda_device
+    g, a, opt = inputs(B + D + N, (B, T), D, N, G, dtype, full)
+    P = 2 * B + 2
+    pool = torch.randn(P, D, N, generator=g).to(pdt)
+    perm = torch.randperm(P, generator=g)
+    read, write = perm[:B].clone(), perm[:B].clone()
+    write[B // 2:] = perm[B:2 * B][B // 2:]
+    if B > 2:
+        read[1], write[2] = -1, -1
+    gp = pool.to(dev)
+    out = lar.ssm_decode(**on(a, dev), **on(opt, dev), pool=gp, read_idx=read.to(dev), write_idx=write.to(dev),
+                         dt_softplus=full)
+    got = gp.cpu()
+    touched = torch.zeros(P, dtype=torch.bool)
+    for i in range(B):
+        seed = R.f64(pool)[read[i]] if read[i] >= 0 else np.zeros((D, N))
+        ref, bound, hs, Es = ref_of(a, opt, i, seed)
+        R.assert_within(out[i], ref, bound, f"out {i}")
+        if write[i] >= 0:
+            R.assert_within(got[write[i]], hs[-1], Es[-1], f"state {i}")
+            touched[write[i]] = True
+    assert torch.equal(got[~touched], pool[~touched])
+
+
+@pytest.mark.parametrize("T,D,N,G,dtype,pdt", [(1, 33, 16, 1, F32, F32), (4, 64, 16, 2, BF16, BF16),
+                                               (16, 20, 32, 1, BF16, F32), (5, 130, 64, 1, F32, F32)])
+def test_tokens(T, D, N, G, dtype, pdt, cuda_device):
+    dev, B = cuda_device, 6
+    g, a, opt = inputs(T * D, (B, T), D, N, G, dtype)
+    P = B * T + 2
+    pool = torch.randn(P, D, N, generator=g).to(pdt)
+    rows = torch.randperm(P, generator=g)[:B * T].view(B, T).int()
+    acc = torch.randint(1, T + 1, (B,), generator=g).int()
+    acc[0], acc[1] = 0, T + 1
+    seeds = [R.f64(pool)[rows[i, acc[i] - 1]] if 1 <= acc[i] <= T else np.zeros((D, N)) for i in range(B)]
+    if T > 1:
+        rows[2, T - 1 if acc[2] != T else 0] = -1
+        rows[3, T - 1 if acc[3] != T else 0] = P
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    gp = pool.to(dev)
+    out = lar.ssm_decode_tokens(**on(a, dev), **on(opt, dev), pool=gp, state_idx=rows.to(dev),
+                                num_accepted=acc.to(dev), dt_softplus=True, dev_err=err)
+    got, touched = gp.cpu(), torch.zeros(P, dtype=torch.bool)
+    for i in range(B):
+        ref, bound, hs, Es = ref_of(a, opt, i, seeds[i])
+        R.assert_within(out[i], ref, bound, f"out {i}")
+        for t in range(T):
+            if 0 <= rows[i, t] < P:
+                R.assert_within(got[rows[i, t]], hs[t], Es[t], f"state {i} {t}")
+                touched[rows[i, t]] = True
+    assert torch.equal(got[~touched], pool[~touched])
+    assert int(err) == lar.LAR_DEVERR_ACCEPTED | (lar.LAR_DEVERR_WRITE_SLOT if T > 1 else 0)
+
+
+SPANS = [[1], [0, 1, 0], [31, 32, 33, 0, 64, 65], [700], [3] * 20, [0, 0, 129, 1, 257]]
+
+
+def check_prefill(dev, lens, D, N, G, dtype, pdt, full, seed=0):
+    n, lead, behind = len(lens), 3, 2
+    off = np.cumsum([lead] + list(lens))
+    tok = int(off[-1]) + behind
+    g, a, opt = inputs(sum(lens) + D + seed, (tok,), D, N, G, dtype, full)
+    P = 2 * n + 1
+    pool = torch.randn(P, D, N, generator=g).to(pdt)
+    perm = torch.randperm(P, generator=g)
+    read, write = perm[:n].clone(), perm[:n].clone()
+    write[n // 2:] = perm[n:2 * n][n // 2:]
+    if n > 3:
+        read[1], write[3] = -1, -1
+    gp = pool.to(dev)
+    out = torch.full((tok, D), 7.0, dtype=dtype, device=dev)
+    lar.ssm_prefill(**on(a, dev), **on(opt, dev), pool=gp, cu_seqlens=torch.tensor(off, device=dev),
+                    read_idx=read.to(dev), write_idx=write.to(dev), out=out, dt_softplus=full)
+    got, touched = gp.cpu(), torch.zeros(P, dtype=torch.bool)
+    for i in range(n):
+        s = R.f64(pool)[read[i]] if read[i] >= 0 else np.zeros((D, N))
+        hs, Es = s[None], np.zeros_like(s)[None]
+        if lens[i]:
+            ref, bound, hs, Es = ref_of(a, opt, slice(off[i], off[i + 1]), s)
+            R.assert_within(out[off[i]:off[i + 1]], ref, bound, f"span {i}")
+        if write[i] >= 0:
+            R.assert_within(got[write[i]], hs[-1], Es[-1], f"state {i}")
+            touched[write[i]] = True
+    assert torch.equal(got[~touched], pool[~touched])
+    assert bool((out[:lead] == 7).all()) and bool((out[off[-1]:] == 7).all())
+
+
+@pytest.mark.parametrize("lens", SPANS, ids=lambda v: "-".join(map(str, v[:6])))
+@pytest.mark.parametrize("D,N,G,dtype,pdt,full", [
+    (64, 16, 1, BF16, F32, True), (37, 16, 1, F32, F32, True), (136, 32, 2, BF16, BF16, True),
+    (24, 64, 2, F32, F32, False), (20, 128, 4, BF16, F32, True), (16, 16, 16, F32, F32, True)])
+def test_prefill(lens, D, N, G, dtype, pdt, full, cuda_device):
+    check_prefill(cuda_device, lens, D, N, G, dtype, pdt, full)
+
+
+@pytest.mark.parametrize("lens,D,N", [([1500], 64, 16), ([2100, 1, 900], 40, 16), ([1100, 0, 513], 24, 64),
+                                      ([4097], 8, 128)])
+def test_prefill_long(lens, D, N, cuda_device):
+    """Few channels and long spans: the tokens of a span are split over blocks."""
+    check_prefill(cuda_device, lens, D, N, 1, F32, F32, True)
+
+
+def test_prefill_many_channels(cuda_device):
+    """Enough blocks that no span is split, several channels a lane."""
+    check_prefill(cuda_device, [40] * 12 + [0, 300], 2056, 16, 1, BF16, F32, True)
+
+
+def test_prefill_equals_steps(cuda_device):
+    """A prompt in one call, in two calls and token by token."""
+    dev, L, D, N = cuda_device, 100, 72, 16
+    g, a, opt = inputs(3, (L,), D, N, 1, F32)
+    a, opt = on(a, dev), on(opt, dev)
+    pool = torch.zeros(4, D, N, device=dev)
+    rest = {k: opt[k] for k in ("D", "dt_bias")}
+    at = lambda lo, hi: dict(A=a["A"], **{k: a[k][lo:hi] for k in ("x", "dt", "B", "C")}, z=opt["z"][lo:hi], **rest)  # noqa: E731
+    idx = lambda i: torch.tensor([i], device=dev)  # noqa: E731
+    kw = dict(pool=pool, dt_softplus=True)
+    whole = lar.ssm_prefill(**at(0, L), cu_seqlens=torch.tensor([0, L], device=dev), read_idx=idx(-1), write_idx=idx(0), **kw)
+    lar.ssm_prefill(**at(0, 61), cu_seqlens=torch.tensor([0, 61], device=dev), read_idx=idx(-1), write_idx=idx(1), **kw)
+    lar.ssm_prefill(**at(61, L), cu_seqlens=torch.tensor([0, L - 61], device=dev), read_idx=idx(1), **kw)
+    steps = []
+    for t in range(L):
+        s = at(t, t + 1)
+        steps.append(lar.ssm_decode(**s, read_idx=idx(-1 if t == 0 else 2), write_idx=idx(2), **kw))
+    ref, bound, hs, Es = ref_of({k: v.cpu() for k, v in a.items()}, {k: v.cpu() for k, v in opt.items()}, slice(0, L),
+                                np.zeros((D, N)))
+    R.assert_within(whole, ref, bound)
+    R.assert_within(torch.cat(steps), ref, bound)
+    for i in range(3):
+        R.assert_within(pool[i], hs[-1], Es[-1], f"way {i}")
+
+
+@pytest.mark.parametrize("how", ["slices", "strides", "off 16 bytes", "A broadcast", "pool rows"])
+def test_layouts(how, cuda_device):
+    dev, B, T, D, N, G = cuda_device, 3, 4, 64, 16, 2
+    g, a, opt = inputs(9, (B, T), D, N, G, BF16)
+    a, opt = on(a, dev), on(opt, dev)
+    pool = torch.randn(9, D, N, generator=g).to(dev)
+    v, p2 = dict(a, **opt), pool.clone()
+
+    def view(t, lo, step):
+        back = torch.zeros(*t.shape[:-1], lo + step * t.shape[-1] + 3, dtype=t.dtype, device=dev)
+        w = back[..., lo:lo + step * t.shape[-1]:step]
+        w.copy_(t)
+        return w
+    if how == "slices":
+        fused = torch.cat([a["x"], opt["z"], a["dt"]], -1)
+        v.update(x=fused[..., :D], z=fused[..., D:2 * D], dt=fused[..., 2 * D:])
+        v.update(B=torch.cat([a["B"], a["C"]], -1)[..., :N], C=torch.cat([a["B"], a["C"]], -1)[..., N:])
+    elif how == "strides":
+        v = {k: view(t, 0, 2) for k, t in v.items()}
+    elif how == "off 16 bytes":
+        v = {k: view(t, 1, 1) for k, t in v.items()}
+    elif how == "A broadcast":
+        a["A"] = -torch.rand(D, 1, device=dev).expand(D, N)
+        v["A"], a["A"] = a["A"], a["A"].contiguous()
+        v["dt"], a["dt"] = a["dt"][..., :1].expand(B, T, D), a["dt"][..., :1].expand(B, T, D).contiguous()
+    else:
+        back = torch.zeros(9, 2 * D, N + 12, device=dev)
+        p2 = back[:, ::2, 4:4 + N]
+        p2.copy_(pool)
+    read, write = torch.tensor([4, 0, 7], device=dev), torch.tensor([4, 1, 2], device=dev)
+    ref_pool = pool.clone()
+    ref = lar.ssm_decode(**a, **opt, pool=ref_pool, read_idx=read, write_idx=write, dt_softplus=True)
+    out = lar.ssm_decode(**v, pool=p2, read_idx=read, write_idx=write, dt_softplus=True)
+    assert torch.equal(out, ref) and torch.equal(p2, ref_pool)
+    flat = lambda d: {k: (t.reshape(B * T, *t.shape[2:]) if t.dim() > 2 else t) for k, t in d.items()}  # noqa: E731
+    off = torch.tensor([0, 5, B * T], dtype=torch.int32, device=dev)
+    kw = dict(cu_seqlens=off, read_idx=read[:2], write_idx=write[:2], dt_softplus=True)
+    p3 = pool.clone()
+    one = lar.ssm_prefill(**flat({**a, **opt}), pool=p3, **kw)
+    p2.copy_(pool)
+    two = lar.ssm_prefill(**{k: (t.as_strided((B * T,) + tuple(t.shape[2:]), t.stride()[1:], t.storage_offset())
+                                 if t.dim() > 2 else t) for k, t in v.items()}, pool=p2, **kw)
+    assert torch.equal(one, two) and torch.equal(p2, p3)
+
+
+def test_values_at_the_edge(cuda_device):
+    """Steps of 0 keep the state; large ones forget it without NaN; a NaN stays in
+    its channel."""
+    dev, D, N = cuda_device, 32, 16
+    z = lambda *s: torch.zeros(*s, device=dev)  # noqa: E731
+    pool = torch.randn(2, D, N, device=dev)
+    before = pool.clone()
+    x, B, C = torch.ones(1, D, device=dev), torch.ones(1, 1, N, device=dev), torch.ones(1, 1, N, device=dev)
+    A = -torch.ones(D, N, device=dev)
+    r = torch.tensor([0], device=dev)
+    lar.ssm_decode(x, z(1, D), A, B, C, pool, r)
+    assert torch.equal(pool, before)
+    dt = torch.full((1, D), -200.0, device=dev)          # softplus underflows to 0
+    lar.ssm_decode(x, dt, A, B, C, pool, r, dt_softplus=True)
+    assert torch.equal(pool, before)
+    out = lar.ssm_decode(z(1, D), torch.full((1, D), 1e6, device=dev), A, B, C, pool, r)
+    assert bool((out == 0).all()) and bool((pool[0] == 0).all())
+    x[0, 5] = float("nan")
+    zz = torch.full((1, D), -200.0, device=dev)
+    out = lar.ssm_decode(x, torch.ones(1, D, device=dev), A, B, C, pool, r, z=zz)
+    assert bool(torch.isnan(out[0, 5])) and int(torch.isnan(out).sum()) == 1
+    assert int(torch.isnan(pool).sum()) == N
+    pool[:] = before
+    off = torch.tensor([0, 1], device=dev)
+    out = lar.ssm_prefill(x, torch.ones(1, D, device=dev), A, B, C, pool, off, r, z=zz)
+    assert bool(torch.isnan(out[0, 5])) and int(torch.isnan(out).sum()) == 1 and int(torch.isnan(pool).sum()) == N
+
+
+@pytest.mark.parametrize("soft", [-30.0, -8.0, -1.0, 0.0, 1.0, 8.0, 25.0, 100.0])
+def test_softplus_range(soft, cuda_device):
+    """The step over softplus's whole range, as x dt on a cleared state."""
+    dev, D, N = cuda_device, 256, 16
+    dt = soft + torch.linspace(-1, 1, D)
+    x, one = torch.ones(1, D), torch.ones(1, 1, N)
+    for packed in (False, True):
+        pool = torch.zeros(1, D, N, device=dev)
+        args = [t.to(dev) for t in (x, dt[None], -torch.ones(D, N), one, one)]
+        if packed:
+            lar.ssm_prefill(*args, pool, torch.tensor([0, 1], device=dev), torch.tensor([0], device=dev), dt_softplus=True)
+        else:
+            lar.ssm_decode(*args, pool, torch.tensor([0], device=dev), dt_softplus=True)
+        ref, bound, hs, Es = R.ssm_tokens(R.f64(x), R.f64(dt[None]), -np.ones((D, N)), np.ones((1, 1, N)),
+                                          np.ones((1, 1, N)), np.zeros((D, N)), soft=True)
+        R.assert_within(pool[0], hs[0], Es[0])
+
+
+def test_bad_spans_and_no_tokens(cuda_device):
+    dev, D, N = cuda_device, 24, 16
+    g, a, opt = inputs(1, (50,), D, N, 1, F32)
+    pool = torch.randn(8, D, N, generator=g).to(dev)
+    before = pool.clone()
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    off = torch.tensor([0, 40, 20, 50, 60], device=dev)
+    lar.ssm_prefill(**on(a, dev), **on(opt, dev), pool=pool, cu_seqlens=off, read_idx=torch.arange(4, device=dev),
+                    write_idx=torch.arange(4, 8, device=dev), dt_softplus=True, dev_err=err)
+    assert int(err) == lar.LAR_DEVERR_SEQLEN
+    assert torch.equal(pool[5], before[1]) and torch.equal(pool[7], before[3])
+    _, _, hs, Es = ref_of(a, opt, slice(0, 40), R.f64(before[0]))
+    R.assert_within(pool[4], hs[-1], Es[-1])
+    none = {k: (t[:0] if k != "A" else t) for k, t in on(a, dev).items()}
+    lar.ssm_prefill(**none, pool=pool, cu_seqlens=torch.zeros(2, dtype=torch.int32, device=dev),
+                    read_idx=torch.tensor([2], device=dev), write_idx=torch.tensor([0], device=dev))
+    assert torch.equal(pool[0], before[2])
+
+
+def test_far_offsets(cuda_device):
+    """A slot whose element offset passes 32 bits."""
+    dev, D, N, P = cuda_device, 32, 16, 70000
+    pool = torch.empty(P, 4 * 512, N, device=dev)[:, :D]       # 2.29e9 elements
+    seed = torch.randn(D, N)
+    pool[P - 1] = seed.to(dev)
+    g, a, opt = inputs(2, (1, 2), D, N, 1, F32)
+    out = lar.ssm_decode(**on(a, dev), **on(opt, dev), pool=pool, read_idx=torch.tensor([P - 1], device=dev),
+                         write_idx=torch.tensor([P - 2], device=dev), dt_softplus=True)
+    ref, bound, hs, Es = ref_of(a, opt, 0, R.f64(seed))
+    R.assert_within(out[0], ref, bound)
+    R.assert_within(pool[P - 2], hs[-1], Es[-1])
