@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) conv_prefill_kernel(const ConvParams
 template <int W, int VEC>
 lar_status step(const ConvParams& p, cudaStream_t st) {
     const unsigned cb = (p.C + kThreads * VEC - 1) / (kThreads * VEC);
-    return launch_ordered(conv_step_kernel<W, VEC>, dim3(cb, p.s.n), kThreads, 0, st, p);
+    return launch_ordered(conv_step_kernel<W, VEC>, dim3(cb, p.s.n), kThreads, 0, 1, st, p);
 }
 
 template <int W, int VEC>
@@ -218,7 +218,7 @@ lar_status prefill(const ConvParams& p, cudaStream_t st) {
     // disjoint spans make at most this many tiles; a block goes on to others where they are not
     const int64_t tiles = p.s.ntok / kTile + p.s.n;
     return launch_ordered(conv_prefill_kernel<W, VEC>, dim3(cb, static_cast<unsigned>(tiles < 65535 ? tiles : 65535)),
-                          kThreads, 0, st, p);
+                          kThreads, 0, 1, st, p);
 }
 
 }  // namespace

@@ -302,8 +302,9 @@ lar_status ssm(const Where& where, const SsmIn& in, const lar_tensor* pool, cons
     const lar_tensor* ins[] = {in.x, in.dt, in.A, in.B, in.C, in.D, in.z, in.dt_bias, where.read_idx, where.write_idx,
                                where.num_accepted, where.state_idx, where.cu_seqlens};
     LAR_TRY(check_aliasing(outs, 2, ins, 13, dev_err));
-    p.vec = D % 8 == 0 && vec8(p.x, p.x_dt, p.xs, 2, p.xs[2]) && vec8(p.dt, p.dt_dt, p.ds, 2, p.ds[2]) &&
+    p.vec = p.per_group % 8 == 0 && vec8(p.x, p.x_dt, p.xs, 2, p.xs[2]) && vec8(p.dt, p.dt_dt, p.ds, 2, p.ds[2]) &&
             vec8(p.out, p.out_dt, p.os, 2, p.os[2]) && (!in.z || vec8(p.z, p.z_dt, p.zs, 2, p.zs[2]));
+    p.vec_bc = vec8(p.B, p.B_dt, p.bs, 3, p.bs[3]) && vec8(p.C, p.C_dt, p.cs, 3, p.cs[3]);
     if (p.s.n == 0) return LAR_OK;
     return where.packed ? lar::launch_ssm_prefill(p, stream) : lar::launch_ssm_step(p, stream);
 }

@@ -19,21 +19,29 @@ __device__ __forceinline__ void stream_order() {
 #endif
 }
 
+// `cluster`: blocks of a cluster along x (1: none).
 template <typename... Kp, typename... Args>
-lar_status launch_ordered(void (*kern)(Kp...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+lar_status launch_ordered(void (*kern)(Kp...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
                           const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
 #if LAR_PDL
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na++].val.programmaticStreamSerializationAllowed = 1;
 #endif
+    if (cluster > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[na].val.clusterDim.y = 1;
+        attr[na++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? LAR_OK : LAR_ERR_LAUNCH;
 }
 
@@ -82,6 +90,45 @@ __device__ __forceinline__ void span_of(const SlotParams& s, int n, int* begin, 
     if (!ok) *bits |= LAR_DEVERR_SEQLEN;
     *begin = ok ? static_cast<int>(a) : 0;
     *len = ok ? static_cast<int>(e - a) : 0;
+}
+
+// Cluster of blocks: this block's place in it, its size, a barrier over it, and
+// the address that `p` of this block's shared memory has in block `rank`.
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ unsigned cluster_size() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ unsigned peer_addr(const void* p, unsigned rank) {
+    const unsigned local = static_cast<unsigned>(__cvta_generic_to_shared(p));
+    unsigned remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    return remote;
+}
+
+__device__ __forceinline__ float ld_peer_f32(const float* p, unsigned rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(p, rank)));
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_peer_f32x4(const float* p, unsigned rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(peer_addr(p, rank)));
+    return v;
 }
 
 // 8 neighbouring channels as fp32, 16-byte loads; NC: through the read-only path
@@ -137,8 +184,14 @@ __device__ __forceinline__ float ld_pool(const void* base, int64_t off, int dt) 
                          : bf16_bits_to_float(static_cast<const unsigned short*>(base)[off]);
 }
 
-// y / (1 + e^-y).  Both SFU steps are good to 2 ulp; where e^-y overflows the
-// quotient is the limit, 0.
-__device__ __forceinline__ float silu_f(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+__device__ __forceinline__ float rcp_f(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// y / (1 + e^-y).  Both SFU steps are good to 2 ulp; where e^-y overflows, the
+// reciprocal is 0 and so is the limit.
+__device__ __forceinline__ float silu_f(float y) { return y * rcp_f(1.f + __expf(-y)); }
 
 }  // namespace lar

@@ -53,6 +53,7 @@ struct SsmParams {
     void* out;  int64_t os[3]; int out_dt;
     int softplus;
     int vec;                                        // 16-byte accesses of 8 channels fit x, dt, z and out
+    int vec_bc;                                     // 16-byte accesses of rows of states fit B and C
 };
 
 struct VerifyParams {

@@ -13,6 +13,67 @@ __device__ __forceinline__ float exp2_f(float x) {
     return y;
 }
 
+// Two fp32 numbers in a register pair: one instruction issued for two products.
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 ex2_2(f32x2 a) {
+    float lo, hi;
+    unpack2(a, lo, hi);
+    return pack2(exp2_f(lo), exp2_f(hi));
+}
+
+// log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v| in (0, 1].  log1p(u) / u is
+// a polynomial of degree 8, fitted to the relative error (Chebyshev nodes,
+// Lawson's weights): off by 2e-7 at most in fp32 arithmetic, for small u too,
+// where 1 + u would lose it.  Small steps matter: most are near 0.001.
+__device__ __forceinline__ float2 softplus2(float2 v) {
+    const f32x2 u = pack2(exp2_f(-fabsf(v.x) * kLog2e), exp2_f(-fabsf(v.y) * kLog2e));
+    const auto both = [](float c) { return pack2(c, c); };
+    f32x2 q = both(0.005232624243944883f);
+    q = fma2(q, u, both(-0.029504956677556038f));
+    q = fma2(q, u, both(0.07822549343109131f));
+    q = fma2(q, u, both(-0.1366320699453354f));
+    q = fma2(q, u, both(0.1910598874092102f));
+    q = fma2(q, u, both(-0.2484297752380371f));
+    q = fma2(q, u, both(0.3331909477710724f));
+    q = fma2(q, u, both(-0.4999949336051941f));
+    q = fma2(q, u, both(0.9999999403953552f));
+    q = fma2(q, u, pack2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+    float2 r;
+    unpack2(q, r.x, r.y);
+    return r;
+}
+
+__device__ __forceinline__ float softplus_fast(float v) { return softplus2(make_float2(v, v)).x; }
+
 // SPL (4 or 8) elements st apart, fp32 or bf16, vector loads where they fit.
 template <int SPL>
 __device__ __forceinline__ void load_row(const void* base, int64_t off, int64_t st, int dt, float* f) {

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmParams p) {
     for (int t = 0; t < p.s.T; ++t) {
         const float x = ld_in(p.x, b * p.xs[0] + t * p.xs[1] + dc * p.xs[2], p.x_dt);
         float s = ld_in(p.dt, b * p.ds[0] + t * p.ds[1] + dc * p.ds[2], p.dt_dt);
-        if (p.softplus) s = softplus_f(s + bias);
+        if (p.softplus) s = softplus_fast(s + bias);
         float Bv[SPL], Cv[SPL];
         load_row<SPL>(p.B, b * p.bs[0] + t * p.bs[1] + g * p.bs[2] + n0 * p.bs[3], p.bs[3], p.B_dt, Bv);
         load_row<SPL>(p.C, b * p.cs[0] + t * p.cs[1] + g * p.cs[2] + n0 * p.cs[3], p.cs[3], p.C_dt, Cv);
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmParams p) {
 template <int N, int SPL>
 lar_status go(const SsmParams& p, cudaStream_t st) {
     constexpr int CPB = kThreads / (N / SPL);
-    return launch_ordered(ssm_step_kernel<N, SPL>, dim3((p.D + CPB - 1) / CPB, p.s.n), kThreads, 0, st, p);
+    return launch_ordered(ssm_step_kernel<N, SPL>, dim3((p.D + CPB - 1) / CPB, p.s.n), kThreads, 0, 1, st, p);
 }
 
 }  // namespace

@@ -25,29 +25,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ unsigned cluster_size() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// a double of this block's shared memory, as block `rank` of the cluster holds it
-__device__ __forceinline__ double ld_peer(const double* p, unsigned rank) {
-    const unsigned local = static_cast<unsigned>(__cvta_generic_to_shared(p));
-    unsigned remote;
+__device__ __forceinline__ double ld_peer_f64(const double* p, unsigned rank) {
     double v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(remote));
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(peer_addr(p, rank)));
     return v;
 }
 
@@ -167,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
         total = before = 0.;
         for (unsigned r = 0; r < size; ++r) {
             if (r == rank) before = total;
-            total += ld_peer(&block_tot, r);
+            total += ld_peer_f64(&block_tot, r);
             if (r == rank) after = total;
         }
         cluster_sync();   // every block has read the sums: they may be written again
@@ -246,20 +226,7 @@ lar_status launch_verify(const VerifyParams& p, void* stream) {
     // a block a few thousand tokens, at most 8 (the portable cluster)
     int size = 1;
     while (size < kMaxCluster && static_cast<int64_t>(size) * 2048 < p.V) size *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(size, p.B);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = size;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_kernel, p) == cudaSuccess ? LAR_OK : LAR_ERR_LAUNCH;
+    return launch_ordered(verify_kernel, dim3(size, p.B), kThreads, 0, size, static_cast<cudaStream_t>(stream), p);
 }
 
 }  // namespace lar
