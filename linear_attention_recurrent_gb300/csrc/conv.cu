@@ -13,7 +13,15 @@ namespace lar {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTile = 32;    // tokens of a prefill tile
+constexpr int kTile = 64;    // tokens of a prefill tile
+#ifndef LAR_CG
+#define LAR_CG 4
+#define LAR_CA 3
+#define LAR_CMB 4
+#endif
+constexpr int kGroup = LAR_CG;    // tokens of a group of copies,
+constexpr int kAhead = LAR_CA;    // groups asked for ahead of the one in work,
+constexpr int kRing = kGroup * (kAhead + 1);   // and the tokens that the ring holds
 
 // VEC channels from channel c0: one 16-byte access (8) or one element (1).
 template <int VEC, bool NC>
@@ -28,16 +36,30 @@ __device__ __forceinline__ void st_ch(void* base, int64_t off, int64_t cs, int c
     else st_out(base, off + c0 * cs, dt, f[0]);
 }
 
-// The taps and bias of VEC channels.
+// The taps and bias of VEC channels, any layout.
 template <int W, int VEC>
 struct Taps {
     float w[VEC][W], b[VEC];
     __device__ __forceinline__ void load(const ConvParams& p, int c0) {
+        if (VEC == 8 && p.vec_w) {   // [C, W] in one piece: 8 W numbers from c0 W on
+            float* f = &w[0][0];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
+            for (int k = 0; k < VEC * W; k += 8) ld8<true>(p.w, static_cast<int64_t>(c0) * W + k, p.w_dt, f + k);
+        } else {
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[i][j] = ld_in(p.w, (c0 + i) * p.ws[0] + j * p.ws[1], p.w_dt);
-            b[i] = p.bias ? ld_in(p.bias, (c0 + i) * p.b_s, p.bias_dt) : 0.f;
+            for (int i = 0; i < VEC; ++i)
+#pragma unroll
+                for (int j = 0; j < W; ++j) w[i][j] = ld_in(p.w, (c0 + i) * p.ws[0] + j * p.ws[1], p.w_dt);
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) b[i] = 0.f;
+        if (p.bias) {
+            if (VEC == 8 && p.vec_b) {
+                ld8<true>(p.bias, c0, p.bias_dt, b);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) b[i] = ld_in(p.bias, (c0 + i) * p.b_s, p.bias_dt);
+            }
         }
     }
     // y of the newest input u after the W - 1 in h, which it joins
@@ -55,6 +77,47 @@ struct Taps {
         }
     }
 };
+
+// The same for 8 channels in pairs: one instruction issued for two channels.  The
+// prefill is bound by issue before it is by memory otherwise.
+template <int W>
+struct Taps8 {
+    f32x2 w[W][4], b[4];
+    __device__ __forceinline__ void load(const ConvParams& p, int c0) {
+        Taps<W, 8> t;
+        t.load(p, c0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = pack2(t.w[2 * i][j], t.w[2 * i + 1][j]);
+            b[i] = pack2(t.b[2 * i], t.b[2 * i + 1]);
+        }
+    }
+    // y of the newest of the W inputs in a window
+    __device__ __forceinline__ void at(const f32x2 (*win)[4], float* y, bool silu) const {
+        f32x2 a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = b[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) a[i] = fma2(w[j][i], win[j][i], a[i]);
+        }
+        if (silu) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = silu2(a[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack2(a[i], y[2 * i], y[2 * i + 1]);
+    }
+};
+
+template <typename T, bool NC>
+__device__ __forceinline__ void widen2(const Eight<T, NC>& e, f32x2* v) {
+    float f[8];
+    e.widen(f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
 
 template <int W, int VEC>
 __device__ __forceinline__ void load_state(const ConvParams& p, int64_t slot, int c0, float (*h)[VEC]) {
@@ -102,6 +165,58 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p)
     if (blockIdx.x == 0 && threadIdx.x == 0) flag_err(p.s.dev_err, bits);
 }
 
+// One token of NB sequences, 8 channels a thread: the states and inputs of all of
+// them are asked for at once, and the filters are read once.  X: type of x; S: of
+// the pool.
+template <int W, typename X, typename S, int NB>
+__global__ void __launch_bounds__(kThreads, NB == 1 ? 6 : 4) conv_token_kernel(const ConvParams p) {
+    const int c0 = (blockIdx.x * kThreads + threadIdx.x) * 8, b0 = blockIdx.y * NB;
+    stream_order();
+    int32_t bits = 0;
+    int64_t from[NB], to[NB];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+        from[k] = to[k] = -1;
+        if (b0 + k < p.s.n) {
+            from[k] = read_slot(p.s, b0 + k, &bits);
+            to[k] = write_slot(p.s, b0 + k, 0, &bits);
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) flag_err(p.s.dev_err, bits);
+    if (c0 >= p.C) return;
+    Eight<X> x[NB];
+    Eight<S, false> st[NB][W - 1];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+        x[k].load(p.x, min(b0 + k, p.s.n - 1) * p.xs[0] + c0);
+#pragma unroll
+        for (int j = 0; j + 1 < W; ++j) {
+            st[k][j].zero();
+            if (from[k] >= 0) st[k][j].load(p.pool, from[k] * p.ps[0] + j * p.ps[1] + c0);
+        }
+    }
+    Taps8<W> taps;
+    taps.load(p, c0);
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+        if (b0 + k >= p.s.n) break;
+        f32x2 win[W][4];
+#pragma unroll
+        for (int j = 0; j + 1 < W; ++j) widen2(st[k][j], win[j]);
+        widen2(x[k], win[W - 1]);
+        float y[8];
+        taps.at(win, y, p.silu);
+        st8(p.out, (b0 + k) * p.os[0] + c0, p.out_dt, y);
+        if (to[k] >= 0) {   // rows move up as they are; the input joins, rounded to the pool's type
+#pragma unroll
+            for (int j = 0; j + 2 < W; ++j) st[k][j + 1].store(p.pool, to[k] * p.ps[0] + j * p.ps[1] + c0);
+            float f[8];
+            x[k].widen(f);
+            st8(p.pool, to[k] * p.ps[0] + (W - 2) * p.ps[1] + c0, p.pool_dt, f);
+        }
+    }
+}
+
 // Which span and tokens tile `tile` covers: span n takes max(1, ceil(len / kTile))
 // tiles, in order.  False past the last one.  Every thread of the block calls it.
 struct TileOf {
@@ -146,48 +261,54 @@ __device__ __forceinline__ bool find_tile(const SlotParams& s, int64_t tile, Til
     return true;
 }
 
-// One tile of tokens of one span a block and step; the tile before supplies the
-// W - 1 inputs ahead of it by reading them again.  The block of a span's first
-// tile alone touches its slots: it reads the seed before it writes the final
-// state, which may go to the same slot.
-template <int W, int VEC>
-__global__ void __launch_bounds__(kThreads) conv_prefill_kernel(const ConvParams p) {
+// The final state of span f.seq: its last W - 1 inputs, the seed's (h) where it is
+// shorter.  The thread of the span's first tile does this for its channels: it has
+// read the seed, and the final state may go to the same slot.
+template <int W, int VEC, typename Input>
+__device__ __forceinline__ void close_span(const ConvParams& p, const TileOf& f, int c0, const float (*h)[VEC],
+                                           int64_t slot, const Input& input) {
+    float e[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j) {
+        const int t = f.len - (W - 1) + j;   // may lie before the span
+        if (t >= 0) {
+            input(t, e[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                e[j][i] = h[0][i];
+#pragma unroll
+                for (int k = 1; k + 1 < W; ++k)
+                    if (t + W - 1 == k) e[j][i] = h[k][i];
+            }
+        }
+    }
+    store_state<W, VEC>(p, slot, c0, e);
+}
+
+// One tile of tokens of one span a block and step; the W - 1 inputs ahead of it are
+// read again.  Any layout, element by element.
+template <int W>
+__global__ void __launch_bounds__(kThreads) conv_prefill_any_kernel(const ConvParams p) {
     __shared__ TileOf tile_s;
     __shared__ int64_t sums[kThreads / 32];
-    const int c0 = (blockIdx.x * kThreads + threadIdx.x) * VEC;
+    const int c0 = blockIdx.x * kThreads + threadIdx.x;
     stream_order();
     for (int64_t tile = blockIdx.y; find_tile(p.s, tile, &tile_s, sums); tile += gridDim.y) {
         const TileOf f = tile_s;
         int32_t bits = 0;
         if (c0 < p.C) {
-            Taps<W, VEC> taps;
+            Taps<W, 1> taps;
             taps.load(p, c0);
-            float h[W - 1][VEC];
+            float h[W - 1][1];
             const auto input = [&](int t, float* u) {
-                ld_ch<VEC, true>(p.x, static_cast<int64_t>(f.begin + t) * p.xs[1], p.xs[2], c0, p.x_dt, u);
+                u[0] = ld_in(p.x, static_cast<int64_t>(f.begin + t) * p.xs[1] + c0 * p.xs[2], p.x_dt);
             };
             if (f.first == 0) {
                 int begin, len;
                 span_of(p.s, f.seq, &begin, &len, &bits);
-                load_state<W, VEC>(p, read_slot(p.s, f.seq, &bits), c0, h);
-                // the last W - 1 inputs, the seed's where the span is shorter
-                float e[W - 1][VEC];
-#pragma unroll
-                for (int j = 0; j + 1 < W; ++j) {
-                    const int t = f.len - (W - 1) + j;   // may lie before the span
-                    if (t >= 0) {
-                        input(t, e[j]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) {
-                            e[j][i] = h[0][i];
-#pragma unroll
-                            for (int k = 1; k + 1 < W; ++k)
-                                if (t + W - 1 == k) e[j][i] = h[k][i];
-                        }
-                    }
-                }
-                store_state<W, VEC>(p, write_slot(p.s, f.seq, 0, &bits), c0, e);
+                load_state<W, 1>(p, read_slot(p.s, f.seq, &bits), c0, h);
+                close_span<W, 1>(p, f, c0, h, write_slot(p.s, f.seq, 0, &bits), input);
             } else {
 #pragma unroll
                 for (int j = 0; j + 1 < W; ++j) input(f.first - (W - 1) + j, h[j]);
@@ -195,10 +316,10 @@ __global__ void __launch_bounds__(kThreads) conv_prefill_kernel(const ConvParams
             const int end = min(f.first + kTile, f.len);
 #pragma unroll 4
             for (int t = f.first; t < end; ++t) {
-                float u[VEC], y[VEC];
+                float u[1], y[1];
                 input(t, u);
                 taps.step(h, u, y, p.silu);
-                st_ch<VEC>(p.out, static_cast<int64_t>(f.begin + t) * p.os[1], p.os[2], c0, p.out_dt, y);
+                st_out(p.out, static_cast<int64_t>(f.begin + t) * p.os[1] + c0 * p.os[2], p.out_dt, y[0]);
             }
         }
         if (blockIdx.x == 0 && threadIdx.x == 0) flag_err(p.s.dev_err, bits);
@@ -206,39 +327,146 @@ __global__ void __launch_bounds__(kThreads) conv_prefill_kernel(const ConvParams
     }
 }
 
-template <int W, int VEC>
-lar_status step(const ConvParams& p, cudaStream_t st) {
-    const unsigned cb = (p.C + kThreads * VEC - 1) / (kThreads * VEC);
-    return launch_ordered(conv_step_kernel<W, VEC>, dim3(cb, p.s.n), kThreads, 0, 1, st, p);
+// The same, 8 channels a thread, inputs on their way through a ring of cp.async
+// copies.  A thread reads back only what it copied: the ring needs no barrier.
+template <int W, typename X>
+__global__ void __launch_bounds__(kThreads, LAR_CMB) conv_prefill_kernel(const ConvParams p) {
+    constexpr int NCH = sizeof(X) / 2;   // 16-byte pieces of 8 channels
+    extern __shared__ __align__(16) unsigned char ring[];   // [kRing][NCH][kThreads] pieces
+    __shared__ TileOf tile_s;
+    __shared__ int64_t sums[kThreads / 32];
+    const int c0 = (blockIdx.x * kThreads + threadIdx.x) * 8;
+    unsigned char* mine = ring + threadIdx.x * 16;
+    stream_order();
+    for (int64_t tile = blockIdx.y; find_tile(p.s, tile, &tile_s, sums); tile += gridDim.y) {
+        const TileOf f = tile_s;
+        int32_t bits = 0;
+        if (c0 < p.C) {
+            const int nt = min(kTile, f.len - f.first);
+            const X* src = static_cast<const X*>(p.x) + static_cast<int64_t>(f.begin + f.first) * p.xs[1] + c0;
+            const auto ask = [&](int g) {   // tokens of group g of the tile
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) {
+                    const int t = g * kGroup + u;
+                    if (t < nt) {
+                        const X* from = src + t * p.xs[1];
+                        unsigned char* dst = mine + ((g % (kAhead + 1)) * kGroup + u) * NCH * kThreads * 16;
+#pragma unroll
+                        for (int k = 0; k < NCH; ++k) cp_async16(dst + k * kThreads * 16, from + k * (16 / sizeof(X)));
+                    }
+                }
+                cp_async_commit();
+            };
+#pragma unroll
+            for (int g = 0; g < kAhead; ++g) ask(g);
+            Taps8<W> taps;
+            taps.load(p, c0);
+            f32x2 win[W - 1 + kGroup][4];   // the inputs before a group, and the group's
+            {
+                float h1[W - 1][8];
+                const auto input = [&](int t, float* u) {
+                    ld8<true>(p.x, static_cast<int64_t>(f.begin + t) * p.xs[1] + c0, p.x_dt, u);
+                };
+                if (f.first == 0) {
+                    int begin, len;
+                    span_of(p.s, f.seq, &begin, &len, &bits);
+                    load_state<W, 8>(p, read_slot(p.s, f.seq, &bits), c0, h1);
+                    close_span<W, 8>(p, f, c0, h1, write_slot(p.s, f.seq, 0, &bits), input);
+                } else {
+#pragma unroll
+                    for (int j = 0; j + 1 < W; ++j) input(f.first - (W - 1) + j, h1[j]);
+                }
+#pragma unroll
+                for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) win[j][i] = pack2(h1[j][2 * i], h1[j][2 * i + 1]);
+            }
+            int64_t o = static_cast<int64_t>(f.begin + f.first) * p.os[1] + c0;
+            for (int g = 0; g * kGroup < nt; ++g) {
+                ask(g + kAhead);
+                cp_async_wait<kAhead>();
+                const unsigned char* at = mine + (g % (kAhead + 1)) * kGroup * NCH * kThreads * 16;
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) {   // past the last token: what the ring holds, not used
+                    Eight<X, false> e;
+#pragma unroll
+                    for (int k = 0; k < NCH; ++k)
+                        e.u[k] = *reinterpret_cast<const uint4*>(at + (u * NCH + k) * kThreads * 16);
+                    widen2(e, win[W - 1 + u]);
+                }
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) {
+                    if (g * kGroup + u < nt) {
+                        float y[8];
+                        taps.at(win + u, y, p.silu);
+                        st8(p.out, o + u * p.os[1], p.out_dt, y);
+                    }
+                }
+                o += kGroup * p.os[1];
+#pragma unroll
+                for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) win[j][i] = win[kGroup + j][i];
+            }
+        }
+        if (blockIdx.x == 0 && threadIdx.x == 0) flag_err(p.s.dev_err, bits);
+        cp_async_wait<0>();
+        __syncthreads();   // tile_s and sums are used again
+    }
 }
 
-template <int W, int VEC>
+template <int W, typename X, typename S, int NB>
+lar_status token(const ConvParams& p, cudaStream_t st) {
+    const unsigned cb = (p.C + kThreads * 8 - 1) / (kThreads * 8);
+    return launch_ordered(conv_token_kernel<W, X, S, NB>, dim3(cb, (p.s.n + NB - 1) / NB), kThreads, 0, 1, st, p);
+}
+
+template <int W>
+lar_status step(const ConvParams& p, cudaStream_t st) {
+    using F = float;
+    using H = unsigned short;
+    const unsigned per = kThreads * (p.vec ? 8 : 1), cb = (p.C + per - 1) / per;
+    if (!p.vec) return launch_ordered(conv_step_kernel<W, 1>, dim3(cb, p.s.n), kThreads, 0, 1, st, p);
+    if (p.s.T > 1) return launch_ordered(conv_step_kernel<W, 8>, dim3(cb, p.s.n), kThreads, 0, 1, st, p);
+    const bool many = static_cast<int64_t>(cb) * p.s.n >= 4 * 152;
+    if (p.x_dt == LAR_BF16) {
+        if (p.pool_dt == LAR_BF16) return many ? token<W, H, H, 4>(p, st) : token<W, H, H, 1>(p, st);
+        return many ? token<W, H, F, 2>(p, st) : token<W, H, F, 1>(p, st);
+    }
+    if (p.pool_dt == LAR_BF16) return many ? token<W, F, H, 2>(p, st) : token<W, F, H, 1>(p, st);
+    return many ? token<W, F, F, 2>(p, st) : token<W, F, F, 1>(p, st);
+}
+
+template <int W, typename X>
+lar_status prefill_vec(const ConvParams& p, dim3 grid, cudaStream_t st) {
+    const auto kern = conv_prefill_kernel<W, X>;
+    const size_t smem = static_cast<size_t>(kRing) * kThreads * 8 * sizeof(X);
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+        return LAR_ERR_LAUNCH;
+    return launch_ordered(kern, grid, kThreads, smem, 1, st, p);
+}
+
+template <int W>
 lar_status prefill(const ConvParams& p, cudaStream_t st) {
-    const unsigned cb = (p.C + kThreads * VEC - 1) / (kThreads * VEC);
+    const unsigned per = kThreads * (p.vec ? 8 : 1), cb = (p.C + per - 1) / per;
     // disjoint spans make at most this many tiles; a block goes on to others where they are not
     const int64_t tiles = p.s.ntok / kTile + p.s.n;
-    return launch_ordered(conv_prefill_kernel<W, VEC>, dim3(cb, static_cast<unsigned>(tiles < 65535 ? tiles : 65535)),
-                          kThreads, 0, 1, st, p);
+    const dim3 grid(cb, static_cast<unsigned>(tiles < 65535 ? tiles : 65535));
+    if (!p.vec) return launch_ordered(conv_prefill_any_kernel<W>, grid, kThreads, 0, 1, st, p);
+    return p.x_dt == LAR_BF16 ? prefill_vec<W, unsigned short>(p, grid, st) : prefill_vec<W, float>(p, grid, st);
 }
 
 }  // namespace
 
 lar_status launch_conv_step(const ConvParams& p, void* stream) {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    switch (p.W) {
-        case 2: return p.vec ? step<2, 8>(p, st) : step<2, 1>(p, st);
-        case 3: return p.vec ? step<3, 8>(p, st) : step<3, 1>(p, st);
-        default: return p.vec ? step<4, 8>(p, st) : step<4, 1>(p, st);
-    }
+    return p.W == 2 ? step<2>(p, st) : p.W == 3 ? step<3>(p, st) : step<4>(p, st);
 }
 
 lar_status launch_conv_prefill(const ConvParams& p, void* stream) {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    switch (p.W) {
-        case 2: return p.vec ? prefill<2, 8>(p, st) : prefill<2, 1>(p, st);
-        case 3: return p.vec ? prefill<3, 8>(p, st) : prefill<3, 1>(p, st);
-        default: return p.vec ? prefill<4, 8>(p, st) : prefill<4, 1>(p, st);
-    }
+    return p.W == 2 ? prefill<2>(p, st) : p.W == 3 ? prefill<3>(p, st) : prefill<4>(p, st);
 }
 
 }  // namespace lar

@@ -243,6 +243,8 @@ lar_status conv(const Where& where, const lar_tensor* x, const lar_tensor* weigh
     LAR_TRY(check_aliasing(outs, 2, ins, 8, dev_err));
     p.vec = C % 8 == 0 && vec8(p.x, p.x_dt, p.xs, 2, p.xs[2]) && vec8(p.out, p.out_dt, p.os, 2, p.os[2]) &&
             vec8(p.pool, p.pool_dt, p.ps, 2, 1);
+    p.vec_w = p.ws[0] == W && vec8(p.w, p.w_dt, nullptr, 0, p.ws[1]);
+    p.vec_b = bias && vec8(p.bias, p.bias_dt, nullptr, 0, p.b_s);
     if (p.s.n == 0) return LAR_OK;
     return where.packed ? lar::launch_conv_prefill(p, stream) : lar::launch_conv_step(p, stream);
 }

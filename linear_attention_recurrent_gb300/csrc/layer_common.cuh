@@ -131,6 +131,51 @@ __device__ __forceinline__ float4 ld_peer_f32x4(const float* p, unsigned rank) {
     return v;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two fp32 numbers in a register pair: one instruction issued for two products.
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 ex2_2(f32x2 a) {
+    float lo, hi;
+    unpack2(a, lo, hi);
+    return pack2(exp2_f(lo), exp2_f(hi));
+}
+
 // 8 neighbouring channels as fp32, 16-byte loads; NC: through the read-only path
 // (never for the pool, which the same call writes).
 template <bool NC>
@@ -184,6 +229,40 @@ __device__ __forceinline__ float ld_pool(const void* base, int64_t off, int dt) 
                          : bf16_bits_to_float(static_cast<const unsigned short*>(base)[off]);
 }
 
+// 8 neighbouring values, asked for (raw) and widened: two steps, so that many are
+// on their way at once
+template <typename T, bool NC = true>
+struct Eight {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const void* base, int64_t i) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
+#pragma unroll
+        for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) u[h] = NC ? __ldg(src + h) : src[h];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) u[h] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void store(void* base, int64_t i) const {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(base) + i);
+#pragma unroll
+        for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) dst[h] = u[h];
+    }
+    __device__ __forceinline__ void widen(float* f) const {
+        if constexpr (sizeof(T) == 2) {
+            unpack8(u[0], f);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f[4 * h] = __uint_as_float(u[h].x);
+                f[4 * h + 1] = __uint_as_float(u[h].y);
+                f[4 * h + 2] = __uint_as_float(u[h].z);
+                f[4 * h + 3] = __uint_as_float(u[h].w);
+            }
+        }
+    }
+};
+
 __device__ __forceinline__ float rcp_f(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -192,6 +271,12 @@ __device__ __forceinline__ float rcp_f(float x) {
 
 // y / (1 + e^-y).  Both SFU steps are good to 2 ulp; where e^-y overflows, the
 // reciprocal is 0 and so is the limit.
-__device__ __forceinline__ float silu_f(float y) { return y * rcp_f(1.f + __expf(-y)); }
+__device__ __forceinline__ float silu_f(float y) { return y * rcp_f(1.f + exp2_f(-kLog2e * y)); }
+
+__device__ __forceinline__ f32x2 silu2(f32x2 y) {
+    float lo, hi;
+    unpack2(add2(ex2_2(mul2(y, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f)), lo, hi);
+    return mul2(y, pack2(rcp_f(lo), rcp_f(hi)));
+}
 
 }  // namespace lar

@@ -34,7 +34,8 @@ struct ConvParams {
     void* pool;       int64_t ps[2]; int pool_dt;   // slot, row (channel stride 1)
     void* out;        int64_t os[3]; int out_dt;
     int silu;
-    int vec;                                        // 16-byte loads and stores of 8 channels fit everywhere
+    int vec;                                        // 16-byte accesses of 8 channels fit x, out and the pool
+    int vec_w, vec_b;                               // and the weights of 8 channels lie in one piece, and the bias
 };
 
 // h[d, n] <- exp(dt[d] A[d, n]) h[d, n] + dt[d] x[d] B[g, n];  y[d] = sum_n C[g, n] h[d, n] + D[d] x[d]

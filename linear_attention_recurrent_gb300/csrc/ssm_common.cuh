@@ -5,51 +5,6 @@
 
 namespace lar {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float exp2_f(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Two fp32 numbers in a register pair: one instruction issued for two products.
-using f32x2 = unsigned long long;
-
-__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-
-__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ f32x2 ex2_2(f32x2 a) {
-    float lo, hi;
-    unpack2(a, lo, hi);
-    return pack2(exp2_f(lo), exp2_f(hi));
-}
-
 // log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v| in (0, 1].  log1p(u) / u is
 // a polynomial of degree 8, fitted to the relative error (Chebyshev nodes,
 // Lawson's weights): off by 2e-7 at most in fp32 arithmetic, for small u too,
@@ -72,7 +27,20 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
     return r;
 }
 
-__device__ __forceinline__ float softplus_fast(float v) { return softplus2(make_float2(v, v)).x; }
+// The same for one, with the coefficients as immediates: where few are wanted at a
+// time, pairs of them would first have to be built in registers.
+__device__ __forceinline__ float softplus1(float v) {
+    const float u = exp2_f(-fabsf(v) * kLog2e);
+    float q = fmaf(0.005232624243944883f, u, -0.029504956677556038f);
+    q = fmaf(q, u, 0.07822549343109131f);
+    q = fmaf(q, u, -0.1366320699453354f);
+    q = fmaf(q, u, 0.1910598874092102f);
+    q = fmaf(q, u, -0.2484297752380371f);
+    q = fmaf(q, u, 0.3331909477710724f);
+    q = fmaf(q, u, -0.4999949336051941f);
+    q = fmaf(q, u, 0.9999999403953552f);
+    return fmaf(q, u, fmaxf(v, 0.f));
+}
 
 // SPL (4 or 8) elements st apart, fp32 or bf16, vector loads where they fit.
 template <int SPL>
@@ -87,6 +55,27 @@ __device__ __forceinline__ void load_a2(const SsmParams& p, int d, int n0, float
     load_row<SPL>(p.A, d * p.as[0] + n0 * p.as[1], p.as[1], LAR_F32, a2);
 #pragma unroll
     for (int i = 0; i < SPL; ++i) a2[i] *= kLog2e;
+}
+
+// 16 bytes of channel d's states from n0 on, as they lie in the pool; zero
+// without a slot.
+__device__ __forceinline__ uint4 load_raw(const SsmParams& p, int64_t slot, int d, int n0) {
+    if (slot < 0) return make_uint4(0u, 0u, 0u, 0u);
+    const int64_t off = slot * p.ps[0] + d * p.ps[1] + n0;
+    return *reinterpret_cast<const uint4*>(static_cast<const char*>(p.pool) + off * (p.pool_dt == LAR_F32 ? 4 : 2));
+}
+
+// 4 fp32 or 8 bf16 of them
+template <int SPL>
+__device__ __forceinline__ void raw_states(const uint4 u, float* h) {
+    if constexpr (SPL == 8) {
+        unpack8(u, h);
+    } else {
+        h[0] = __uint_as_float(u.x);
+        h[1] = __uint_as_float(u.y);
+        h[2] = __uint_as_float(u.z);
+        h[3] = __uint_as_float(u.w);
+    }
 }
 
 // SPL states of channel d from n0 on; the pool's rows are 16-byte aligned.

@@ -12,9 +12,10 @@
 //
 // A chosen index has to be the one that exact sums give, and a flat row has
 // neighbours 1e-5 apart of which a sum in 32 bits gets the last digits wrong.
-// So a weight is kept as the unevaluated sum of two floats (the rounding error
-// of p - q is itself a float), a lane adds pairs, and lanes, warps and blocks
-// are joined in 64 bits.
+// So weights and sums are kept as unevaluated sums of two floats (the rounding
+// error of p - q is itself a float), good to about 2^-48.  Doubles would do as
+// well, but this device adds two or so of them a clock on an SM: with doubles from
+// the lanes' sums on, one sequence took 15.6 us.
 #include "layer_common.cuh"
 
 namespace lar {
@@ -24,12 +25,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-
-__device__ __forceinline__ double ld_peer_f64(const double* p, unsigned rank) {
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(peer_addr(p, rank)));
-    return v;
-}
+constexpr int kStep = 256;      // tokens of a warp's step
 
 // (hi, lo) + x, the error of the sum kept: two-sum (Knuth)
 __device__ __forceinline__ void add_exact(float& hi, float& lo, float x) {
@@ -39,38 +35,147 @@ __device__ __forceinline__ void add_exact(float& hi, float& lo, float x) {
     hi = s;
 }
 
+// hi + lo, |lo| at most half a unit in the last place of hi
+struct Sum {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Sum renormal(float hi, float lo) {
+    const float s = hi + lo;
+    return {s, lo - (s - hi)};
+}
+
+__device__ __forceinline__ Sum plus(Sum a, Sum b) {
+    float hi = a.hi, lo = a.lo + b.lo;
+    add_exact(hi, lo, b.hi);
+    return renormal(hi, lo);
+}
+
+__device__ __forceinline__ bool below(Sum a, Sum b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+__device__ __forceinline__ bool same(Sum a, Sum b) { return a.hi == b.hi && a.lo == b.lo; }
+__device__ __forceinline__ Sum least(Sum a, Sum b) { return below(b, a) ? b : a; }
+
+__device__ __forceinline__ Sum shfl(Sum a, int lane) {
+    return {__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
+}
+
+__device__ __forceinline__ Sum warp_sum(Sum a) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        a = plus(a, {__shfl_xor_sync(0xffffffffu, a.hi, off), __shfl_xor_sync(0xffffffffu, a.lo, off)});
+    return a;
+}
+
+// sums of lanes 0 .. this one
+__device__ __forceinline__ Sum warp_scan(Sum a, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const Sum y = {__shfl_up_sync(0xffffffffu, a.hi, off), __shfl_up_sync(0xffffffffu, a.lo, off)};
+        if (lane >= off) a = plus(y, a);
+    }
+    return a;
+}
+
+// The weight of a token with target probability a and draft probability b, as hi +
+// lo; 0 unless positive and finite.  The error of a float difference is a float.
+__device__ __forceinline__ void weight_of(float a, float b, float& hi, float& lo) {
+    hi = a - b;
+    const float t = hi - a;
+    lo = (a - (hi - t)) + (-b - t);
+    if (!(hi > 0.f && hi < INFINITY)) hi = lo = 0.f;
+}
+
+// The same where nothing is infinite: fmaxf takes NaN and negative numbers to 0.
+__device__ __forceinline__ void weight_finite(float a, float b, float& hi, float& lo) {
+    const float d = a - b, t = d - a;
+    lo = (a - (d - t)) + (-b - t);
+    hi = fmaxf(d, 0.f);
+    lo = d > 0.f ? lo : 0.f;
+}
+
 struct Row {
     const void *p, *q;      // q NULL: nothing to subtract
     int64_t ps, qs;         // element strides
     int p_dt, q_dt;
     int64_t hot;            // one-hot q: the drafted token, else -1
+    int64_t V;
+    bool vec;               // 16-byte loads fit both
 
-    // the weight of token i as hi + lo; 0 unless positive and finite
     __device__ __forceinline__ void weight(int64_t i, float& hi, float& lo) const {
-        const float a = ld_in(p, i * ps, p_dt);
-        hi = a;
-        lo = 0.f;
-        if (q) {
-            const float b = ld_in(q, i * qs, q_dt);
-            hi = a - b;
-            const float t = hi - a;
-            lo = (a - (hi - t)) + (-b - t);
-        } else if (i == hot) {
-            hi = 0.f;
+        const float a = i == hot ? 0.f : ld_in(p, i * ps, p_dt);
+        weight_of(a, q ? ld_in(q, i * qs, q_dt) : 0.f, hi, lo);
+    }
+
+    // tokens [i, i + 8), in order; past the end they weigh nothing
+    __device__ __forceinline__ void weights8(int64_t i, float* hi, float* lo) const {
+        if (vec && i + 8 <= V) {
+            float a[8], b[8];
+            ld8<true>(p, i, p_dt, a);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b[k] = 0.f;
+            if (q) ld8<true>(q, i, q_dt, b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) weight_of(i + k == hot ? 0.f : a[k], b[k], hi[k], lo[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                hi[k] = lo[k] = 0.f;
+                if (i + k < V) weight(i + k, hi[k], lo[k]);
+            }
         }
-        if (!(hi > 0.f && hi < INFINITY)) hi = lo = 0.f;
     }
 };
 
-__device__ __forceinline__ double warp_sum(double x) {
+// Adds the weights of whole steps [s0, s1) of a row that 16-byte loads fit.  A sum
+// that is not finite says that some weight was not: the caller adds them again, with
+// each looked at.
+template <typename P, typename Q, bool HAS_Q>
+__device__ __forceinline__ void add_steps(const Row& row, int64_t s0, int64_t s1, int lane, float& hi, float& lo) {
+    constexpr int U = 2;
+    for (int64_t s = s0; s < s1; s += U) {
+        Eight<P> a[U];
+        Eight<Q> b[U];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    return x;
+        for (int u = 0; u < U; ++u) {   // the last one may ask for a step again, to no effect
+            const int64_t i = min(s + u, s1 - 1) * kStep + lane * 8;
+            a[u].load(row.p, i);
+            if (HAS_Q) b[u].load(row.q, i);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s + u >= s1) break;
+            const int64_t i = (s + u) * kStep + lane * 8;
+            float fa[8], fb[8];
+            a[u].widen(fa);
+            if (HAS_Q) b[u].widen(fb);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float w, e;
+                if (HAS_Q) {
+                    weight_finite(fa[k], fb[k], w, e);
+                    add_exact(hi, lo, w);
+                    lo += e;
+                } else {
+                    w = fmaxf(fa[k], 0.f);
+                    add_exact(hi, lo, i + k == row.hot ? 0.f : w);
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void put_token(const VerifyParams& p, int64_t b, int t, int64_t v) {
+    const int64_t o = b * p.os[0] + t * p.os[1];
+    if (p.out_dt == LAR_I32) static_cast<int32_t*>(p.out)[o] = static_cast<int32_t>(v);
+    else static_cast<int64_t*>(p.out)[o] = v;
 }
 
 __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) {
-    __shared__ double warp_tot[kWarps];
-    __shared__ double block_tot;
+    __shared__ Sum warp_tot[kWarps];
+    __shared__ Sum block_tot, before_s, after_s, total_s, start_s;
+    __shared__ int owner_s;
+    __shared__ int found[2];
+    __shared__ int64_t last_seen;
     const unsigned rank = cluster_rank(), size = cluster_size();
     const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     stream_order();
@@ -93,9 +198,9 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
         } else {
             const float pt = ld_in(p.p, b * p.ps[0] + lane * p.ps[1] + tok * p.ps[2], p.p_dt);
             const float qt = p.q ? ld_in(p.q, b * p.qs[0] + lane * p.qs[1] + tok * p.qs[2], p.q_dt) : 1.f;
-            // the product of two floats is exact in 64 bits
-            good = static_cast<double>(p.ua[b * p.ua_s[0] + lane * p.ua_s[1]]) * static_cast<double>(qt) <
-                   static_cast<double>(pt);
+            // u q < p for the product itself: where it rounds to p, its error decides
+            const float u = __ldg(p.ua + b * p.ua_s[0] + lane * p.ua_s[1]), uq = u * qt;
+            good = uq < pt || (uq == pt && fmaf(u, qt, -uq) < 0.f);
         }
     }
     const unsigned bad = ~__ballot_sync(0xffffffffu, good);
@@ -110,6 +215,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
     row.qs = 0;
     row.q_dt = p.q_dt;
     row.hot = -1;
+    row.V = p.V;
     if (n < k) {
         if (p.q) {
             row.q = static_cast<const char*>(p.q) + (b * p.qs[0] + n * p.qs[1]) * (p.q_dt == LAR_F32 ? 4 : 2);
@@ -119,105 +225,164 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
         }
     }
 
-    // this warp's stretch of the vocabulary, in steps of 32 tokens
-    const int64_t steps = (p.V + 31) / 32;
+    row.vec = row.ps == 1 && reinterpret_cast<uintptr_t>(row.p) % 16 == 0 &&
+              (!row.q || (row.qs == 1 && reinterpret_cast<uintptr_t>(row.q) % 16 == 0));
+
+    // this warp's stretch of the vocabulary, in steps of 256 tokens, 8 a lane
+    const int64_t steps = (p.V + kStep - 1) / kStep;
     const int64_t w_all = static_cast<int64_t>(size) * kWarps, w_me = static_cast<int64_t>(rank) * kWarps + warp;
     const int64_t s0 = steps * w_me / w_all, s1 = steps * (w_me + 1) / w_all;
 
-    double total = 0., before = 0., after = 0., mine = 0.;
+    Sum total = {0.f, 0.f};
     for (int pass = 0; pass < 2; ++pass) {
         float hi = 0.f, lo = 0.f;
-        for (int64_t s = s0; s < s1; ++s) {
-            const int64_t i = s * 32 + lane;
-            if (i >= p.V) continue;
-            float a, e;
-            row.weight(i, a, e);
-            add_exact(hi, lo, a);
-            lo += e;
+        int64_t done = s0;
+        if (row.vec) {
+            done = max(s0, min(s1, p.V / kStep));   // whole steps
+            const bool pb = row.p_dt == LAR_BF16, qb = row.q_dt == LAR_BF16;
+            using F = float;
+            using H = unsigned short;
+            if (!row.q) pb ? add_steps<H, H, false>(row, s0, done, lane, hi, lo) : add_steps<F, F, false>(row, s0, done, lane, hi, lo);
+            else if (qb) pb ? add_steps<H, H, true>(row, s0, done, lane, hi, lo) : add_steps<F, H, true>(row, s0, done, lane, hi, lo);
+            else pb ? add_steps<H, F, true>(row, s0, done, lane, hi, lo) : add_steps<F, F, true>(row, s0, done, lane, hi, lo);
+            if (__any_sync(0xffffffffu, !(hi < INFINITY && lo < INFINITY))) {
+                done = s0;
+                hi = lo = 0.f;
+            }
         }
-        mine = warp_sum(static_cast<double>(hi) + static_cast<double>(lo));
+        for (int64_t s = done; s < s1; ++s) {   // neighbours on neighbouring lanes: the order is free here
+            float a[8], e[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                a[k] = e[k] = 0.f;
+                const int64_t i = s * kStep + k * 32 + lane;
+                if (i < p.V) row.weight(i, a[k], e[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                add_exact(hi, lo, a[k]);
+                lo += e[k];
+            }
+        }
+        const Sum mine = warp_sum(renormal(hi, lo));
         if (lane == 0) warp_tot[warp] = mine;
         __syncthreads();
-        if (tid == 0) {
-            double t = 0.;
-            for (int w = 0; w < kWarps; ++w) t += warp_tot[w];
-            block_tot = t;
+        if (warp == 0) {
+            const Sum own = warp_sum(lane < kWarps ? warp_tot[lane] : Sum{0.f, 0.f});
+            if (lane == 0) block_tot = own;
         }
         cluster_sync();
-        total = before = 0.;
-        for (unsigned r = 0; r < size; ++r) {
-            if (r == rank) before = total;
-            total += ld_peer_f64(&block_tot, r);
-            if (r == rank) after = total;
+        if (warp == 0) {
+            Sum all = {0.f, 0.f};
+            if (lane < size) all = {ld_peer_f32(&block_tot.hi, lane), ld_peer_f32(&block_tot.lo, lane)};
+            Sum run = {0.f, 0.f};   // one after another: alike in every block, and never falling
+            for (unsigned r = 0; r < size; ++r) {
+                if (r == rank && lane == 0) before_s = run;
+                run = plus(run, shfl(all, r));
+                if (r == rank && lane == 0) after_s = run;
+            }
+            if (lane == 0) total_s = run;
         }
         cluster_sync();   // every block has read the sums: they may be written again
-        if (total > 0. || (row.q == nullptr && row.hot < 0)) break;
+        total = total_s;
+        if (total.hi > 0.f || (row.q == nullptr && row.hot < 0)) break;
         // the residual is empty: draw from the target itself
         row.q = nullptr;
         row.hot = -1;
+        __syncthreads();   // total_s is written again
     }
-    // This warp's stretch of the whole sum, [lo_sum, hi_sum).  `after` is where the
-    // next block's begins; the last warp with any weight ends there, so that the
-    // stretches of all warps cover [0, total) once, whatever the sums round to.
-    double lo_sum = before, hi_sum;
-    int last_warp = -1;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) lo_sum += warp_tot[w];
-        if (warp_tot[w] > 0.) last_warp = w;
-    }
-    hi_sum = warp == last_warp ? after : fmin(lo_sum + mine, after);
-    lo_sum = fmin(lo_sum, after);
-
     if (rank == 0 && warp == 0) {
-        if (lane < p.T && lane != n) {
-            const int64_t o = b * p.os[0] + lane * p.os[1], v = lane < n ? tok : -1;
-            if (p.out_dt == LAR_I32) static_cast<int32_t*>(p.out)[o] = static_cast<int32_t>(v);
-            else static_cast<int64_t*>(p.out)[o] = v;
-        }
+        if (lane < p.T && lane != n) put_token(p, b, lane, lane < n ? tok : -1);
         if (lane == 0) {
             if (p.acc_dt == LAR_I32) static_cast<int32_t*>(p.acc)[b * p.acc_s] = n + 1;
             else static_cast<int64_t*>(p.acc)[b * p.acc_s] = n + 1;
         }
-        if (!(total > 0.)) bits |= LAR_DEVERR_PROBS;
+        if (!(total.hi > 0.f)) bits |= LAR_DEVERR_PROBS;
         bits = static_cast<int32_t>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bits)));
         if (lane == 0) flag_err(p.dev_err, bits);
     }
 
-    // The warp whose stretch holds the threshold finds the token.  A number outside
-    // [0, 1) draws the first or the last token with any weight.
-    double thr = static_cast<double>(p.us[b * p.us_s]) * total;
-    if (!(thr >= 0.)) thr = 0.;
-    int64_t chosen = -1;
-    const bool here = total > 0. ? mine > 0. && lo_sum < hi_sum &&
-                                       ((lo_sum <= thr && thr < hi_sum) || (thr >= total && hi_sum == total))
-                                 : rank == 0 && warp == 0;   // no weight anywhere: token -1
-    if (here && total > 0.) {
-        double run = lo_sum;
-        int64_t last = -1;
-        for (int64_t s = s0; s < s1 && chosen < 0; ++s) {
-            const int64_t i = s * 32 + lane;
-            float a = 0.f, e = 0.f;
-            if (i < p.V) row.weight(i, a, e);
-            const double w = static_cast<double>(a) + static_cast<double>(e);
-            double incl = w;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += y;
-            }
-            const unsigned over = __ballot_sync(0xffffffffu, w > 0. && run + incl > thr);
-            const unsigned any = __ballot_sync(0xffffffffu, w > 0.);
-            if (over) chosen = s * 32 + __ffs(over) - 1;
-            if (any) last = s * 32 + 31 - __clz(any);
-            run += __shfl_sync(0xffffffffu, incl, 31);
+    if (!(total.hi > 0.f)) {   // no weight anywhere
+        if (rank == 0 && tid == 0) put_token(p, b, n, -1);
+        return;
+    }
+    // A number outside [0, 1) draws the first or the last token with any weight.
+    const float us = __ldg(p.us + b * p.us_s), up = us * total.hi;
+    const Sum zero = {0.f, 0.f}, thr = us >= 0.f ? renormal(up, fmaf(us, total.hi, -up) + us * total.lo) : zero;
+    // Warp w's stretch of the whole sum is [lo, hi).  `after` is where the next block's
+    // begins; the last warp with any weight ends there, so that the stretches of all
+    // warps cover [0, total) once, whatever the sums round to.
+    if (warp == 0) {
+        const Sum own = lane < kWarps ? warp_tot[lane] : zero;
+        const unsigned some = __ballot_sync(0xffffffffu, own.hi > 0.f);
+        Sum run = before_s, lo = run, hi = run;
+        for (int w = 0; w < kWarps; ++w) {
+            if (lane == w) lo = run;
+            run = least(plus(run, shfl(own, w)), after_s);
+            if (lane == w) hi = some >> w == 1u ? after_s : run;
         }
-        if (chosen < 0) chosen = last;
+        const bool mine = own.hi > 0.f && below(lo, hi) &&
+                          ((!below(thr, lo) && below(thr, hi)) || (!below(thr, total) && same(hi, total)));
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        if (lane == 0) owner_s = who ? __ffs(who) - 1 : -1;
+        if (who && lane == __ffs(who) - 1) start_s = lo;
     }
-    if (here && lane == 0) {
-        const int64_t o = b * p.os[0] + n * p.os[1];
-        if (p.out_dt == LAR_I32) static_cast<int32_t*>(p.out)[o] = static_cast<int32_t>(chosen);
-        else static_cast<int64_t*>(p.out)[o] = chosen;
+    __syncthreads();
+    const int owner = owner_s;
+    if (owner < 0) return;   // another block's: one alone finds an owner
+    Sum start = start_s;
+
+    // The block goes through the owner's stretch, 8 neighbours a thread.
+    const int64_t o_me = static_cast<int64_t>(rank) * kWarps + owner;
+    const int64_t first = steps * o_me / w_all * kStep, end = min(steps * (o_me + 1) / w_all * kStep, p.V);
+    for (int64_t base = first; base < end; base += kThreads * 8) {
+        const int64_t i = base + tid * 8;
+        float a[8], e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = e[k] = 0.f;
+        if (i < end) row.weights8(i, a, e);
+        float hi = 0.f, er = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            add_exact(hi, er, a[k]);
+            er += e[k];
+        }
+        const Sum own = renormal(hi, er), incl = warp_scan(own, lane);
+        __syncthreads();   // warp_tot and found are read no more
+        if (lane == 31) warp_tot[warp] = incl;
+        if (tid == 0) found[0] = found[1] = -1;
+        __syncthreads();
+        Sum run = start, block = start;   // up to this thread's tokens, and past the block's
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) run = block;
+            block = plus(block, warp_tot[w]);
+        }
+        const Sum left = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+        const Sum upto = plus(run, incl);
+        if (lane > 0) run = plus(run, left);
+        // the first thread that ends above the threshold holds the token
+        if (own.hi > 0.f && below(thr, upto))
+            atomicMin(reinterpret_cast<unsigned*>(&found[0]), static_cast<unsigned>(tid));
+        if (own.hi > 0.f) atomicMax(&found[1], tid);
+        __syncthreads();
+        if (tid == found[0] || tid == found[1]) {
+            int64_t chosen = -1, last = -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (!(a[k] > 0.f)) continue;
+                run = plus(run, {a[k], e[k]});
+                last = i + k;
+                if (chosen < 0 && below(thr, run)) chosen = i + k;
+            }
+            if (tid == found[0]) put_token(p, b, n, chosen >= 0 ? chosen : last);
+            else last_seen = last;
+        }
+        if (found[0] >= 0) return;
+        start = block;
     }
+    // rounding left none above: the last token of the stretch with any weight
+    __syncthreads();
+    if (tid == 0) put_token(p, b, n, last_seen);
 }
 
 }  // namespace
