@@ -14,13 +14,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 64;    // tokens of a prefill tile
-#ifndef LAR_CG
-#define LAR_CG 4
-#define LAR_CA 3
-#define LAR_CMB 4
-#endif
-constexpr int kGroup = LAR_CG;    // tokens of a group of copies,
-constexpr int kAhead = LAR_CA;    // groups asked for ahead of the one in work,
+constexpr int kGroup = 4;    // tokens of a group of copies,
+constexpr int kAhead = 3;    // groups asked for ahead of the one in work,
 constexpr int kRing = kGroup * (kAhead + 1);   // and the tokens that the ring holds
 
 // VEC channels from channel c0: one 16-byte access (8) or one element (1).
@@ -78,46 +73,23 @@ struct Taps {
     }
 };
 
-// The same for 8 channels in pairs: one instruction issued for two channels.  The
-// prefill is bound by issue before it is by memory otherwise.
+// 8 channels of a window of W inputs.
 template <int W>
-struct Taps8 {
-    f32x2 w[W][4], b[4];
-    __device__ __forceinline__ void load(const ConvParams& p, int c0) {
-        Taps<W, 8> t;
-        t.load(p, c0);
+struct Taps8 : Taps<W, 8> {
+    // y of the newest input of the window
+    __device__ __forceinline__ void at(const float (*win)[8], float* y, bool silu) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
+            y[i] = this->b[i];
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[j][i] = pack2(t.w[2 * i][j], t.w[2 * i + 1][j]);
-            b[i] = pack2(t.b[2 * i], t.b[2 * i + 1]);
-        }
-    }
-    // y of the newest of the W inputs in a window
-    __device__ __forceinline__ void at(const f32x2 (*win)[4], float* y, bool silu) const {
-        f32x2 a[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = b[i];
-#pragma unroll
-            for (int j = 0; j < W; ++j) a[i] = fma2(w[j][i], win[j][i], a[i]);
+            for (int j = 0; j < W; ++j) y[i] = fmaf(this->w[i][j], win[j][i], y[i]);
         }
         if (silu) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = silu2(a[i]);
+            for (int i = 0; i < 8; ++i) y[i] = silu_f(y[i]);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpack2(a[i], y[2 * i], y[2 * i + 1]);
     }
 };
-
-template <typename T, bool NC>
-__device__ __forceinline__ void widen2(const Eight<T, NC>& e, f32x2* v) {
-    float f[8];
-    e.widen(f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
-}
 
 template <int W, int VEC>
 __device__ __forceinline__ void load_state(const ConvParams& p, int64_t slot, int c0, float (*h)[VEC]) {
@@ -200,10 +172,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 6 : 4) conv_token_kernel(c
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
         if (b0 + k >= p.s.n) break;
-        f32x2 win[W][4];
+        float win[W][8];
 #pragma unroll
-        for (int j = 0; j + 1 < W; ++j) widen2(st[k][j], win[j]);
-        widen2(x[k], win[W - 1]);
+        for (int j = 0; j + 1 < W; ++j) st[k][j].widen(win[j]);
+        x[k].widen(win[W - 1]);
         float y[8];
         taps.at(win, y, p.silu);
         st8(p.out, (b0 + k) * p.os[0] + c0, p.out_dt, y);
@@ -330,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) conv_prefill_any_kernel(const ConvPa
 // The same, 8 channels a thread, inputs on their way through a ring of cp.async
 // copies.  A thread reads back only what it copied: the ring needs no barrier.
 template <int W, typename X>
-__global__ void __launch_bounds__(kThreads, LAR_CMB) conv_prefill_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kThreads, 4) conv_prefill_kernel(const ConvParams p) {
     constexpr int NCH = sizeof(X) / 2;   // 16-byte pieces of 8 channels
     extern __shared__ __align__(16) unsigned char ring[];   // [kRing][NCH][kThreads] pieces
     __shared__ TileOf tile_s;
@@ -361,25 +333,18 @@ __global__ void __launch_bounds__(kThreads, LAR_CMB) conv_prefill_kernel(const C
             for (int g = 0; g < kAhead; ++g) ask(g);
             Taps8<W> taps;
             taps.load(p, c0);
-            f32x2 win[W - 1 + kGroup][4];   // the inputs before a group, and the group's
-            {
-                float h1[W - 1][8];
-                const auto input = [&](int t, float* u) {
-                    ld8<true>(p.x, static_cast<int64_t>(f.begin + t) * p.xs[1] + c0, p.x_dt, u);
-                };
-                if (f.first == 0) {
-                    int begin, len;
-                    span_of(p.s, f.seq, &begin, &len, &bits);
-                    load_state<W, 8>(p, read_slot(p.s, f.seq, &bits), c0, h1);
-                    close_span<W, 8>(p, f, c0, h1, write_slot(p.s, f.seq, 0, &bits), input);
-                } else {
+            float win[W - 1 + kGroup][8];   // the inputs before a group, and the group's
+            const auto input = [&](int t, float* u) {
+                ld8<true>(p.x, static_cast<int64_t>(f.begin + t) * p.xs[1] + c0, p.x_dt, u);
+            };
+            if (f.first == 0) {
+                int begin, len;
+                span_of(p.s, f.seq, &begin, &len, &bits);
+                load_state<W, 8>(p, read_slot(p.s, f.seq, &bits), c0, win);
+                close_span<W, 8>(p, f, c0, win, write_slot(p.s, f.seq, 0, &bits), input);
+            } else {
 #pragma unroll
-                    for (int j = 0; j + 1 < W; ++j) input(f.first - (W - 1) + j, h1[j]);
-                }
-#pragma unroll
-                for (int j = 0; j + 1 < W; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) win[j][i] = pack2(h1[j][2 * i], h1[j][2 * i + 1]);
+                for (int j = 0; j + 1 < W; ++j) input(f.first - (W - 1) + j, win[j]);
             }
             int64_t o = static_cast<int64_t>(f.begin + f.first) * p.os[1] + c0;
             for (int g = 0; g * kGroup < nt; ++g) {
@@ -392,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, LAR_CMB) conv_prefill_kernel(const C
 #pragma unroll
                     for (int k = 0; k < NCH; ++k)
                         e.u[k] = *reinterpret_cast<const uint4*>(at + (u * NCH + k) * kThreads * 16);
-                    widen2(e, win[W - 1 + u]);
+                    e.widen(win[W - 1 + u]);
                 }
 #pragma unroll
                 for (int u = 0; u < kGroup; ++u) {
@@ -406,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, LAR_CMB) conv_prefill_kernel(const C
 #pragma unroll
                 for (int j = 0; j + 1 < W; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) win[j][i] = win[kGroup + j][i];
+                    for (int i = 0; i < 8; ++i) win[j][i] = win[kGroup + j][i];
             }
         }
         if (blockIdx.x == 0 && threadIdx.x == 0) flag_err(p.s.dev_err, bits);

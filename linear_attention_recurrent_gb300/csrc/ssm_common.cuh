@@ -42,7 +42,7 @@ __device__ __forceinline__ float softplus1(float v) {
     return fmaf(q, u, fmaxf(v, 0.f));
 }
 
-// SPL (4 or 8) elements st apart, fp32 or bf16, vector loads where they fit.
+// SPL (a multiple of 4) elements st apart, fp32 or bf16, vector loads where they fit.
 template <int SPL>
 __device__ __forceinline__ void load_row(const void* base, int64_t off, int64_t st, int dt, float* f) {
 #pragma unroll
@@ -78,7 +78,7 @@ __device__ __forceinline__ void raw_states(const uint4 u, float* h) {
     }
 }
 
-// SPL states of channel d from n0 on; the pool's rows are 16-byte aligned.
+// SPL (a multiple of 4) states of channel d from n0 on; the pool's rows are 16-byte aligned.
 template <int SPL>
 __device__ __forceinline__ void load_states(const SsmParams& p, int64_t slot, int d, int n0, float* h) {
     if (slot < 0) {
@@ -115,11 +115,15 @@ __device__ __forceinline__ void store_states(const SsmParams& p, int64_t slot, i
         for (int i = 0; i < SPL; i += 4)
             st_state(reinterpret_cast<float4*>(static_cast<float*>(p.pool) + off + i),
                      make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]));
-    } else if constexpr (SPL == 8) {
-        st_state(reinterpret_cast<uint4*>(static_cast<unsigned short*>(p.pool) + off), pack8(h));
+    } else if constexpr (SPL % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < SPL; i += 8)
+            st_state(reinterpret_cast<uint4*>(static_cast<unsigned short*>(p.pool) + off + i), pack8(h + i));
     } else {
-        st_state(reinterpret_cast<uint2*>(static_cast<unsigned short*>(p.pool) + off),
-                 make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])));
+#pragma unroll
+        for (int i = 0; i < SPL; i += 4)
+            st_state(reinterpret_cast<uint2*>(static_cast<unsigned short*>(p.pool) + off + i),
+                     make_uint2(pack_bf16x2(h[i], h[i + 1]), pack_bf16x2(h[i + 2], h[i + 3])));
     }
 }
 

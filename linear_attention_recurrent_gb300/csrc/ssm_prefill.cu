@@ -1,542 +1,551 @@
 // ssm_prefill.cu -- the selective scan over packed spans (ssm_prefill).
 //
-// A block of 128 threads walks the tokens of one span for CH channels, tile by
-// tile, with the states in registers: a lane holds SPL states of each of CPL
-// channels, LPC = N / SPL neighbouring lanes hold a channel.  Per tile
-//   1. dt and x of every (token, channel) become the step s and s x in shared
-//      memory, B and C lie beside them in fp32;
-//   2. the recurrence runs, its sums y go where s was;
-//   3. the skip and the gate are applied and the tile is stored.
-// The next tile's inputs come in by cp.async meanwhile.
+// A warp walks the tokens of (a part of) one span for CW channels with the states
+// in registers, by itself: a lane holds 16 states, N / 16 neighbouring lanes hold a
+// channel.  Inputs come in by cp.async, eight tokens a stage and some stages ahead,
+// into shared memory of the warp's own; B and C are widened there once for all
+// channels.  A lane works out the step, the gate and the output of its channel
+// itself, so warps never wait for one another.
 //
-// What bounds it: for N = 16 a (token, channel) costs 16 SFU exponentials (32 a
-// clock on an SM: 0.5 clocks), 64 fp32 multiplies and adds (0.5 clocks; issued
-// in pairs), and what a lane reads of shared memory (128 bytes a clock).  A lane
-// with one channel would read 2 N words of B and C for every channel, a clock's
-// worth; four channels a lane share them.
+// What bounds it, at N = 16 for a (token, channel): 19 SFU operations (32 a clock on
+// an SM, 0.6 clocks), 64 fp32 multiplies and adds (128 a clock, 0.5 clocks), and
+// their issue beside everything else (4 instructions of 32 lanes a clock).  Products
+// are taken in pairs, one instruction for two: operands that lie in neighbouring
+// registers anyway (states, A, B, C).  An earlier form, in which blocks of threads
+// prepared s and s x in shared memory for all lanes of a channel and met at three
+// barriers a tile, needed 154 instructions for a (token, channel).
 //
-// Few rows, long spans: the tokens of a span are split over the blocks of a
-// cluster.  Every block but the last first runs its tokens from a zero state and
-// keeps the end state and the sum of its steps (the decay over the block is
-// exp(A sum)); all read the ones before them through distributed shared memory,
-// join them to the state they start from, and run their tokens again with
-// outputs.  That costs 1.7 times the work, so a span is split only where blocks
-// are too few (see launch).
+// Few rows, long spans: the tokens of a span are split over the warps of a cluster
+// of blocks.  Every warp but the last first runs its tokens from a zero state and
+// keeps the end state and the sum of its steps (the decay over its part is exp(A
+// sum)); they are joined within a block, then over the blocks through distributed
+// shared memory, and every warp runs its tokens again from the state it starts
+// with, now with outputs.
+#include <algorithm>
+#include <type_traits>
+
 #include "ssm_common.cuh"
 
 namespace lar {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSPL = 8;        // states of a channel on a lane,
+constexpr int kH = kSPL / 2;   // and pairs of them
+constexpr int kTok = 8;        // tokens of a stage
+constexpr int kStages = 3;
+// Tokens whose steps and gates are worked out together, and blocks an SM: a whole
+// stage with the registers of three blocks, or half of one with four, which spans
+// over clusters want (8192 x 2048 x 16: 162 us, with three 181 us; 24 ragged spans of
+// 16384 x 4096 x 16 within blocks: 401 us with three, 450 us with four).
+__host__ __device__ constexpr int tokens_of(bool cluster) { return cluster ? 4 : kTok; }
+__host__ __device__ constexpr int blocks_of(bool cluster) { return cluster ? 4 : 3; }
 constexpr int kSms = 152;      // of a GB300
-constexpr int kMinSeg = 64;    // least tokens of a block where a span is split
+constexpr int kFill = 4096;    // warps that keep it busy
 
-#ifndef LAR_TU
-#define LAR_TU 4
-#endif
-constexpr int kTU = LAR_TU;   // tokens taken together: their loads and exponentials do not wait for one another
+// The types of x, dt, z, B, C and out: all bf16 or all fp32, staged as they are, or
+// mixed, staged as fp32.
+enum Mode { MIXED, BF16, F32 };
 
-template <int N, int SPL, int CPL>
+template <int MODE>
+using Elem = typename std::conditional<MODE == BF16, unsigned short, float>::type;
+
+template <int N, int MODE>
 struct Geo {
-    static constexpr int LPC = N / SPL;                     // lanes of a channel
-    static constexpr int CPW = 32 / LPC * CPL;              // channels of a warp
-    static constexpr int CH = kThreads / 32 * CPW;          // channels of a block
-    static constexpr int TT = 2048 / CH < 32 ? 2048 / CH : 32;   // tokens of a tile
-    static constexpr int E = TT * CH;
-    static constexpr int PAIRS = CH / 2;                    // channel pairs: a thread prepares one, for
-    static constexpr int TSTEP = kThreads / PAIRS;          // every TSTEP-th token,
-    static constexpr int PT = TT / TSTEP;                   // PT of a tile
-    static_assert(TT % kTU == 0 && TT % TSTEP == 0, "whole groups of tokens");
-    static_assert(CH % 8 == 0 && kThreads % (CH / 2) == 0, "whole 16-byte groups; pairs of channels tile the block");
+    using E = Elem<MODE>;
+    static constexpr int LPC = N / kSPL;      // lanes of a pair of channels
+    static constexpr int CW = 64 / LPC;       // channels of a warp
+    // a stage: x, dt, z [kTok][CW], B, C [kTok][N] as they come
+    static constexpr int X = kTok * CW, R = kTok * N;
+    static constexpr int stage = (3 * X + 2 * R) * static_cast<int>(sizeof(E));
+    static constexpr int wide = MODE == BF16 ? 2 * R * 4 : 0;   // B, C of the stage in work, in fp32
+    static constexpr int warp_bytes = kStages * stage + wide;
+    static_assert(stage % 16 == 0, "stages start on 16 bytes");
 };
 
-// Where the parts of a block's shared memory lie (bytes).
-struct Parts {
-    int bs, raw, x, dt, z, b, c, stage, total;
-};
-
-template <int N, int SPL, int CPL>
-__host__ __device__ inline Parts parts_of(const SsmParams& p) {
-    using G = Geo<N, SPL, CPL>;
-    Parts q;
-    q.bs = G::E * 8;                                        // after s, s x
-    q.raw = q.bs + G::TT * N * 8;                           // after B, C
-    const auto size = [](int dt, int n) { return n * (dt == LAR_F32 ? 4 : 2); };
-    q.x = 0;
-    q.dt = q.x + size(p.x_dt, G::E);
-    q.z = q.dt + size(p.dt_dt, G::E);
-    q.b = q.z + (p.z ? size(p.z_dt, G::E) : 0);
-    q.c = q.b + size(p.B_dt, G::TT * N);
-    q.stage = q.c + size(p.C_dt, G::TT * N);
-    q.total = q.raw + 2 * q.stage;
-    return q;
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+    const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(dst));
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
 }
 
-// Rows [0, nt) of the first `cols` of COLS elements, `row` elements apart in
-// memory and COLS in shared memory, by 16-byte copies.
-template <int COLS, int ES>
-__device__ __forceinline__ void copy_rows_of(unsigned char* dst, const unsigned char* src, int64_t row, int nt, int cols) {
-    constexpr int PER = COLS * ES / 16;   // a power of two
-    constexpr int STEP = kThreads / PER > 0 ? kThreads / PER : 1;
-    static_assert(PER <= kThreads, "a thread keeps its column");
-    const int k = threadIdx.x % PER;
-    if (k * 16 >= cols * ES) return;
-    int t = threadIdx.x / PER;
-    const unsigned char* s = src + t * row * ES + k * 16;
-#pragma unroll 4
-    for (; t < nt; t += STEP, s += STEP * row * ES) cp_async16(dst + t * COLS * ES + k * 16, s);
-}
-
-template <int COLS>
-__device__ __forceinline__ void copy_rows(unsigned char* dst, const void* src, int64_t off, int64_t row, int dt, int nt,
-                                          int cols) {
-    if (dt == LAR_BF16)
-        copy_rows_of<COLS, 2>(dst, static_cast<const unsigned char*>(src) + off * 2, row, nt, cols);
-    else
-        copy_rows_of<COLS, 4>(dst, static_cast<const unsigned char*>(src) + off * 4, row, nt, cols);
-}
-
-__device__ __forceinline__ float2 bf2(unsigned u) {
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-
-// PT pairs, `step` elements apart, from a stage
-template <int PT>
-__device__ __forceinline__ void raw_pairs(const unsigned char* base, int dt, int i, int step, float2* v) {
-    if (dt == LAR_BF16) {
+// nt rows of the first `cols` of COLS elements, by the lanes of a warp
+template <int COLS, typename E>
+__device__ __forceinline__ void copy_rows(E* dst, const E* src, int64_t row, int nt, int cols, int lane) {
+    constexpr int B = COLS * sizeof(E) >= 16 ? 16 : static_cast<int>(COLS * sizeof(E));
+    constexpr int PER = COLS * static_cast<int>(sizeof(E)) / B, EPC = B / static_cast<int>(sizeof(E));
+    constexpr int ALL = PER * kTok;
 #pragma unroll
-        for (int k = 0; k < PT; ++k) v[k] = bf2(*reinterpret_cast<const unsigned*>(base + (i + k * step) * 2));
-    } else {
-#pragma unroll
-        for (int k = 0; k < PT; ++k) v[k] = *reinterpret_cast<const float2*>(base + (i + k * step) * 4);
+    for (int i0 = 0; i0 < ALL; i0 += 32) {
+        const int i = i0 + lane, t = i / PER, k = i % PER * EPC;
+        if (i < ALL && t < nt && k < cols) cp_async<B>(dst + t * COLS + k, src + t * row + k);
     }
 }
 
-// the same from memory, any layout: pair k at off + k row, its second element st on
-template <int PT, typename T>
-__device__ __forceinline__ void mem_pairs_of(const T* src, int64_t row, int64_t st, int n_tok, int tstep, bool one,
-                                             bool two, float2* v) {
+// the same by single elements: fp32 neighbours by 4-byte copies, others by loads and
+// stores, which the warp waits for
+template <int COLS, typename E>
+__device__ __forceinline__ void read_rows(E* dst, const void* src, int64_t off, int64_t row, int64_t st, int dt, int nt,
+                                          int cols, int lane) {
+    constexpr int ALL = COLS * kTok, PER = (ALL + 31) / 32;
+    if (sizeof(E) == 4 && dt == LAR_F32 && st == 1) {
 #pragma unroll
-    for (int k = 0; k < PT; ++k) {
-        v[k] = make_float2(0.f, 0.f);
-        const T* a = src + k * row;
-        if constexpr (sizeof(T) == 2) {
-            if (one && k * tstep < n_tok) v[k].x = bf16_bits_to_float(__ldg(a));
-            if (two && k * tstep < n_tok) v[k].y = bf16_bits_to_float(__ldg(a + st));
-        } else {
-            if (one && k * tstep < n_tok) v[k].x = __ldg(a);
-            if (two && k * tstep < n_tok) v[k].y = __ldg(a + st);
+        for (int k = 0; k < PER; ++k) {
+            const int i = k * 32 + lane, t = i / COLS, c = i % COLS;
+            if (i < ALL && t < nt && c < cols) cp_async<4>(dst + i, static_cast<const float*>(src) + off + t * row + c);
         }
+        return;
     }
-}
-
-template <int PT>
-__device__ __forceinline__ void mem_pairs(const void* base, int dt, int64_t off, int64_t row, int64_t st, int n_tok,
-                                          int tstep, bool one, bool two, float2* v) {
-    if (dt == LAR_BF16)
-        mem_pairs_of<PT>(static_cast<const unsigned short*>(base) + off, row, st, n_tok, tstep, one, two, v);
-    else
-        mem_pairs_of<PT>(static_cast<const float*>(base) + off, row, st, n_tok, tstep, one, two, v);
-}
-
-// Sums of y[token][channel] over the LPC lanes of a channel, scattered over them.
-// Steps that halve the channels need no selection: channel j of lane l is channel
-// j ^ perm(l) of its group, so that a lane always keeps its first values and sends
-// its last ones.  Steps past that halve the tokens, which lanes take in order.
-template <int LPC, int CPL>
-struct Scatter {
-    static constexpr int CK = CPL / (LPC < CPL ? LPC : CPL);                 // channels kept
-    static constexpr int LEFT = LPC < CPL ? 1 : LPC / CPL;                   // lanes that share them
-    static constexpr int TK = kTU / (LEFT < kTU ? LEFT : kTU);               // tokens kept
-
-    static __device__ __forceinline__ int perm_of(int lane) {
-        int m = 0;
+    constexpr int AT = PER < 8 ? PER : 8;   // on their way at once
 #pragma unroll
-        for (int bit = 1, half = CPL / 2; bit < LPC && half > 0; bit <<= 1, half >>= 1)
-            if (lane & bit) m |= half;
-        return m;
-    }
-    // the first of the TK tokens that a lane ends with
-    static __device__ __forceinline__ int first_token(int lane) {
-        int t = 0;
+    for (int k0 = 0; k0 < PER; k0 += AT) {
+        E v[AT];
 #pragma unroll
-        for (int bit = CPL, half = kTU / 2; bit < LPC && half > 0; bit <<= 1, half >>= 1)
-            if (lane & bit) t += half;
-        return t;
-    }
-    static __device__ __forceinline__ void sum(float (*y)[CPL], int lane) {
-        int nt = kTU;
-#pragma unroll
-        for (int bit = 1, half = CPL / 2; bit < LPC; bit <<= 1, half >>= 1) {
-            if (half > 0) {
-#pragma unroll
-                for (int u = 0; u < kTU; ++u)
-#pragma unroll
-                    for (int j = 0; j < half; ++j) y[u][j] += __shfl_xor_sync(0xffffffffu, y[u][j + half], bit);
-            } else if (nt > 1) {
-                nt /= 2;
-                const bool up = lane & bit;
-#pragma unroll
-                for (int u = 0; u < kTU / 2; ++u) {
-                    if (u >= nt) continue;
-                    const float keep = up ? y[u + nt][0] : y[u][0], send = up ? y[u][0] : y[u + nt][0];
-                    y[u][0] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
-                }
-            } else {
-                y[0][0] += __shfl_xor_sync(0xffffffffu, y[0][0], bit);
+        for (int k = 0; k < AT; ++k) {
+            const int i = (k0 + k) * 32 + lane, t = i / COLS, c = i % COLS;
+            v[k] = E(0);
+            if (i < ALL && t < nt && c < cols) {
+                if constexpr (sizeof(E) == 2) v[k] = __ldg(static_cast<const unsigned short*>(src) + off + t * row + c * st);
+                else v[k] = ld_in(src, off + t * row + c * st, dt);
             }
         }
+#pragma unroll
+        for (int k = 0; k < AT; ++k) {
+            const int i = (k0 + k) * 32 + lane;
+            if (i < ALL) dst[i] = v[k];
+        }
     }
-};
+}
 
-template <int N, int SPL, int CPL>
+template <int N, int MODE, bool VEC>
 struct Scan {
-    using G = Geo<N, SPL, CPL>;
-    using S = Scatter<G::LPC, CPL>;
-    static constexpr int LPC = G::LPC, CH = G::CH, TT = G::TT, H = SPL / 2;
+    using G = Geo<N, MODE>;
+    using E = typename G::E;
+    static constexpr int LPC = G::LPC, CW = G::CW, H = kH;
 
     const SsmParams& p;
-    const Parts q;
-    unsigned char* smem;
-    float2* step;              // [TT][CH]: s, s x; the sum y takes the place of s
-    float *Bs, *Cs;            // [TT][N]
+    unsigned char* mem;        // this warp's shared memory
+    int lane, sub, ch, n0;     // lane; its place among the pair's lanes; its own channel; its first state
     int g, d0, nch;            // group, first channel, channels
-    int ch0, n0, perm, t_own;  // this lane's channels (in the block) and states; the token of a group it ends with
-    f32x2 h[CPL][H], a2[CPL][H];
-    float ssum[CPL];           // pass 1: the steps' sum
+    float bias, skip;          // of its own channel
+    f32x2 h[2][kH], a2[2][kH]; // of its own channel and of the pair's other
+    float ssum;                // pass without outputs: the sum of the own channel's steps
 
-    __device__ __forceinline__ Scan(const SsmParams& params, unsigned char* sm, int column)
-        : p(params), q(parts_of<N, SPL, CPL>(params)), smem(sm) {
-        step = reinterpret_cast<float2*>(smem);
-        Bs = reinterpret_cast<float*>(smem + q.bs);
-        Cs = Bs + TT * N;
-        const int per_g = (p.per_group + CH - 1) / CH;   // blocks do not straddle groups
+    __device__ __forceinline__ Scan(const SsmParams& params, unsigned char* m, int column) : p(params), mem(m) {
+        lane = threadIdx.x & 31;
+        sub = lane % LPC;
+        ch = lane / LPC * 2 + (sub & 1);
+        n0 = sub * kSPL;
+        const int per_g = (p.per_group + CW - 1) / CW;   // warps do not straddle groups
         g = column / per_g;
-        d0 = g * p.per_group + (column % per_g) * CH;
-        nch = min(CH, (g + 1) * p.per_group - d0);
-        const int lane = threadIdx.x % LPC;
-        ch0 = threadIdx.x / LPC * CPL;
-        n0 = lane * SPL;
-        perm = S::perm_of(lane);
-        t_own = S::first_token(lane);
+        d0 = g * p.per_group + (column % per_g) * CW;
+        nch = min(CW, (g + 1) * p.per_group - d0);
     }
 
-    __device__ __forceinline__ int channel(int j) const { return ch0 + (j ^ perm); }
+    // The lane's own channel (j = 0) and the other one; past the last, the last.
+    __device__ __forceinline__ int d(int j) const { return d0 + min(ch ^ j, nch - 1); }
 
-    __device__ __forceinline__ void load_decay() {
+    __device__ __forceinline__ void load_weights() {
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            float a[SPL];
-            load_a2<SPL>(p, d0 + min(channel(j), nch - 1), n0, a);
+        for (int j = 0; j < 2; ++j) {
+            float a[kSPL];
+            load_a2<kSPL>(p, d(j), n0, a);
 #pragma unroll
-            for (int i = 0; i < H; ++i) a2[j][i] = pack2(a[2 * i], a[2 * i + 1]);
+            for (int i = 0; i < kH; ++i) a2[j][i] = pack2(a[2 * i], a[2 * i + 1]);
         }
+        bias = p.dt_bias ? p.dt_bias[d(0) * p.dtb_s] : 0.f;
+        skip = p.skip ? p.skip[d(0) * p.skip_s] : 0.f;
     }
 
     __device__ __forceinline__ void load_seed(int64_t slot) {
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            float v[SPL];
-            load_states<SPL>(p, slot, d0 + min(channel(j), nch - 1), n0, v);
+        for (int j = 0; j < 2; ++j) {
+            float v[kSPL];
+            load_states<kSPL>(p, slot, d(j), n0, v);
 #pragma unroll
-            for (int i = 0; i < H; ++i) h[j][i] = pack2(v[2 * i], v[2 * i + 1]);
+            for (int i = 0; i < kH; ++i) h[j][i] = pack2(v[2 * i], v[2 * i + 1]);
         }
     }
 
     __device__ __forceinline__ void store_end(int64_t slot) const {
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            float v[SPL];
+        for (int j = 0; j < 2; ++j) {
+            float v[kSPL];
 #pragma unroll
-            for (int i = 0; i < H; ++i) unpack2(h[j][i], v[2 * i], v[2 * i + 1]);
-            if (channel(j) < nch) store_states<SPL>(p, slot, d0 + channel(j), n0, v);
+            for (int i = 0; i < kH; ++i) unpack2(h[j][i], v[2 * i], v[2 * i + 1]);
+            if ((ch ^ j) < nch) store_states<kSPL>(p, slot, d(j), n0, v);
         }
     }
 
-    // Start the copies of tokens [tok, tok + nt) into a stage.
+    __device__ __forceinline__ E* stage(int s) const { return reinterpret_cast<E*>(mem + s * G::stage); }
+
+    // Ask for tokens [tok, tok + nt).
     template <bool OUT>
-    __device__ __forceinline__ void fetch(int64_t tok, int nt, int stage) const {
-        unsigned char* r = smem + q.raw + stage * q.stage;
-        if (p.vec) {
-            copy_rows<CH>(r + q.x, p.x, tok * p.xs[1] + d0, p.xs[1], p.x_dt, nt, nch);
-            copy_rows<CH>(r + q.dt, p.dt, tok * p.ds[1] + d0, p.ds[1], p.dt_dt, nt, nch);
-            if (OUT && p.z) copy_rows<CH>(r + q.z, p.z, tok * p.zs[1] + d0, p.zs[1], p.z_dt, nt, nch);
-        }
-        if (p.vec_bc) {
-            copy_rows<N>(r + q.b, p.B, tok * p.bs[1] + g * p.bs[2], p.bs[1], p.B_dt, nt, N);
-            if (OUT) copy_rows<N>(r + q.c, p.C, tok * p.cs[1] + g * p.cs[2], p.cs[1], p.C_dt, nt, N);
-        }
-        cp_async_commit();
-    }
-
-    // This thread's pairs of x, dt or z: channels c, c + 1 of every TSTEP-th token
-    // of the tile from t on.
-    __device__ __forceinline__ void pairs(const void* base, int part, const unsigned char* r, int dt, int64_t tok,
-                                          const int64_t* st, int t, int c, int nt, float2* v) const {
-        if (p.vec)
-            raw_pairs<G::PT>(r + part, dt, t * CH + c, G::TSTEP * CH, v);
-        else
-            mem_pairs<G::PT>(base, dt, (tok + t) * st[1] + (d0 + c) * st[2], G::TSTEP * st[1], st[2], nt - t, G::TSTEP,
-                             c < nch, c + 1 < nch, v);
-    }
-
-    // Rows of B or C, zero past the tile's last token.
-    __device__ __forceinline__ void rows(float* dst, const void* base, int part, const unsigned char* r, int dt,
-                                         int64_t off, const int64_t* st, int nt) const {
-        constexpr int PT = (TT * N / 2 + kThreads - 1) / kThreads;
-        float2 v[PT];
-        const int i = 2 * threadIdx.x;
-        if (i >= TT * N) return;   // a tile of few values; else they divide evenly
-        if (p.vec_bc) {
-            raw_pairs<PT>(r + part, dt, i, 2 * kThreads, v);
+    __device__ __forceinline__ void fetch(int64_t tok, int nt, int s) const {
+        E* r = stage(s);
+        if constexpr (VEC) {
+            copy_rows<CW>(r, static_cast<const E*>(p.x) + tok * p.xs[1] + d0, p.xs[1], nt, nch, lane);
+            copy_rows<CW>(r + G::X, static_cast<const E*>(p.dt) + tok * p.ds[1] + d0, p.ds[1], nt, nch, lane);
+            if (OUT && p.z) copy_rows<CW>(r + 2 * G::X, static_cast<const E*>(p.z) + tok * p.zs[1] + d0, p.zs[1], nt, nch, lane);
         } else {
-#pragma unroll
-            for (int k = 0; k < PT; ++k) {
-                const int t = (i + k * 2 * kThreads) / N, n = (i + k * 2 * kThreads) % N;
-                if (t < nt)
-                    v[k] = make_float2(ld_in(base, off + t * st[1] + n * st[3], dt),
-                                       ld_in(base, off + t * st[1] + (n + 1) * st[3], dt));
-            }
+            read_rows<CW>(r, p.x, tok * p.xs[1] + d0 * p.xs[2], p.xs[1], p.xs[2], p.x_dt, nt, nch, lane);
+            read_rows<CW>(r + G::X, p.dt, tok * p.ds[1] + d0 * p.ds[2], p.ds[1], p.ds[2], p.dt_dt, nt, nch, lane);
+            if (OUT && p.z)
+                read_rows<CW>(r + 2 * G::X, p.z, tok * p.zs[1] + d0 * p.zs[2], p.zs[1], p.zs[2], p.z_dt, nt, nch, lane);
         }
-#pragma unroll
-        for (int k = 0; k < PT; ++k) {
-            const int e = i + k * 2 * kThreads;
-            *reinterpret_cast<float2*>(dst + e) = e < nt * N ? v[k] : make_float2(0.f, 0.f);
+        if (MODE != MIXED && (VEC || p.vec_bc)) {
+            copy_rows<N>(r + 3 * G::X, static_cast<const E*>(p.B) + tok * p.bs[1] + g * p.bs[2], p.bs[1], nt, N, lane);
+            if (OUT) copy_rows<N>(r + 3 * G::X + G::R, static_cast<const E*>(p.C) + tok * p.cs[1] + g * p.cs[2], p.cs[1], nt, N, lane);
+        } else {
+            read_rows<N>(r + 3 * G::X, p.B, tok * p.bs[1] + g * p.bs[2], p.bs[1], p.bs[3], p.B_dt, nt, N, lane);
+            if (OUT) read_rows<N>(r + 3 * G::X + G::R, p.C, tok * p.cs[1] + g * p.cs[2], p.cs[1], p.cs[3], p.C_dt, nt, N, lane);
         }
+    }
+
+    static __device__ __forceinline__ float value(E v) {
+        if constexpr (MODE == BF16) return bf16_bits_to_float(v);
+        else return v;
     }
 
     // Tokens [begin, end) of the packed arrays; OUT: with outputs, else the end
     // state and the steps' sum alone.
-    template <bool OUT>
+    template <bool OUT, int U>
     __device__ __forceinline__ void run(int64_t begin, int64_t end) {
-        constexpr int PT = G::PT, TSTEP = G::TSTEP;
-        const int c = threadIdx.x % G::PAIRS * 2, t0 = threadIdx.x / G::PAIRS;
-        const bool one = c < nch, two = c + 1 < nch;
-        const float2 bias = make_float2(one && p.dt_bias ? p.dt_bias[(d0 + c) * p.dtb_s] : 0.f,
-                                        two && p.dt_bias ? p.dt_bias[(d0 + c + 1) * p.dtb_s] : 0.f);
-        const float2 skip = make_float2(one && p.skip ? p.skip[(d0 + c) * p.skip_s] : 0.f,
-                                        two && p.skip ? p.skip[(d0 + c + 1) * p.skip_s] : 0.f);
-        int stage = 0;
-        fetch<OUT>(begin, static_cast<int>(min(static_cast<int64_t>(TT), end - begin)), 0);
-        for (int64_t tok = begin; tok < end; tok += TT, stage ^= 1) {
-            const int nt = static_cast<int>(min(static_cast<int64_t>(TT), end - tok));
-            cp_async_wait<0>();
-            __syncthreads();   // the stage is in; the last tile's step and stage are free
-            if (tok + TT < end)
-                fetch<OUT>(tok + TT, static_cast<int>(min(static_cast<int64_t>(TT), end - tok - TT)), stage ^ 1);
-            const unsigned char* r = smem + q.raw + stage * q.stage;
-            {
-                float2 x[PT], s[PT];
-                pairs(p.x, q.x, r, p.x_dt, tok, p.xs, t0, c, nt, x);
-                pairs(p.dt, q.dt, r, p.dt_dt, tok, p.ds, t0, c, nt, s);
-                if (p.softplus) {
+        const int64_t n = end - begin;
+        const auto left = [&](int64_t i) { return static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(kTok), n - i * kTok))); };
 #pragma unroll
-                    for (int k = 0; k < PT; ++k)
-                        s[k] = softplus2(make_float2(s[k].x + bias.x, s[k].y + bias.y));
-                }
-#pragma unroll
-                for (int k = 0; k < PT; ++k) {   // a step of 0 past the last token and the last channel
-                    const bool a = one && t0 + k * TSTEP < nt, b = two && t0 + k * TSTEP < nt;
-                    *reinterpret_cast<float4*>(step + (t0 + k * TSTEP) * CH + c) =
-                        make_float4(a ? s[k].x : 0.f, a ? s[k].x * x[k].x : 0.f, b ? s[k].y : 0.f,
-                                    b ? s[k].y * x[k].y : 0.f);
-                }
-            }
-            rows(Bs, p.B, q.b, r, p.B_dt, tok * p.bs[1] + g * p.bs[2], p.bs, nt);
-            if (OUT) rows(Cs, p.C, q.c, r, p.C_dt, tok * p.cs[1] + g * p.cs[2], p.cs, nt);
-            __syncthreads();
-            for (int t = 0; t < nt; t += kTU) tokens<OUT>(t);
-            if (!OUT) continue;
-            __syncthreads();
-            float2 y[PT];
-#pragma unroll
-            for (int k = 0; k < PT; ++k) {
-                const float4 v = *reinterpret_cast<const float4*>(step + (t0 + k * TSTEP) * CH + c);
-                y[k] = make_float2(v.x, v.z);
-            }
-            if (p.skip) {
-                float2 x[PT];
-                pairs(p.x, q.x, r, p.x_dt, tok, p.xs, t0, c, nt, x);
-#pragma unroll
-                for (int k = 0; k < PT; ++k) y[k] = make_float2(fmaf(skip.x, x[k].x, y[k].x), fmaf(skip.y, x[k].y, y[k].y));
-            }
-            if (p.z) {
-                float2 z[PT];
-                pairs(p.z, q.z, r, p.z_dt, tok, p.zs, t0, c, nt, z);
-#pragma unroll
-                for (int k = 0; k < PT; ++k) y[k] = make_float2(y[k].x * silu_f(z[k].x), y[k].y * silu_f(z[k].y));
-            }
-            const int64_t o = (tok + t0) * p.os[1] + (d0 + c) * p.os[2], row = TSTEP * p.os[1];
-            if (p.vec && p.out_dt == LAR_BF16) {
-#pragma unroll
-                for (int k = 0; k < PT; ++k)
-                    if (one && t0 + k * TSTEP < nt)   // channels come by eights
-                        *reinterpret_cast<unsigned*>(static_cast<unsigned short*>(p.out) + o + k * row) =
-                            pack_bf16x2(y[k].x, y[k].y);
-            } else {
-#pragma unroll
-                for (int k = 0; k < PT; ++k) {
-                    if (t0 + k * TSTEP >= nt) continue;
-                    if (one) st_out(p.out, o + k * row, p.out_dt, y[k].x);
-                    if (two) st_out(p.out, o + k * row + p.os[2], p.out_dt, y[k].y);
-                }
-            }
+        for (int s = 0; s + 1 < kStages; ++s) {
+            if (left(s) > 0) fetch<OUT>(begin + s * kTok, left(s), s);
+            cp_async_commit();
         }
-        __syncthreads();   // before anything else uses the shared memory
+        int s = 0, sn = kStages - 1;   // stage in work, stage to fill
+        for (int64_t i = 0; i * kTok < n; ++i) {
+            const int nt = left(i);
+            const int64_t tok = begin + i * kTok, ahead = i + kStages - 1;
+            if (left(ahead) > 0) fetch<OUT>(begin + ahead * kTok, left(ahead), sn);
+            cp_async_commit();
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            const E* r = stage(s);
+            const float *Bs, *Cs;
+            if constexpr (MODE == BF16) {
+                float* w = reinterpret_cast<float*>(mem + kStages * G::stage);
+                // 8 numbers a lane and turn; C lies behind B in both
+#pragma unroll
+                for (int k = lane * 8; k < (OUT ? 2 : 1) * G::R; k += 256) {
+                    float f[8];
+                    unpack8(*reinterpret_cast<const uint4*>(r + 3 * G::X + k), f);
+                    *reinterpret_cast<float4*>(w + k) = make_float4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<float4*>(w + k + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                }
+                __syncwarp();
+                Bs = w + n0;
+                Cs = w + G::R + n0;
+            } else {
+                Bs = reinterpret_cast<const float*>(r) + 3 * G::X + n0;
+                Cs = Bs + G::R;
+            }
+            if (nt == kTok) {
+#pragma unroll
+                for (int t = 0; t < kTok; t += U) tokens<OUT, U>(r, Bs, Cs, tok, t);
+            } else {
+                for (int t = 0; t < nt; ++t) tokens<OUT, 1>(r, Bs, Cs, tok, t);
+            }
+            __syncwarp();   // the stage, and B and C, are free
+            s = s + 1 == kStages ? 0 : s + 1;
+            sn = sn + 1 == kStages ? 0 : sn + 1;
+        }
+        cp_async_wait<0>();
+        __syncwarp();
     }
 
-    // kTU tokens of the tile, from t on
-    template <bool OUT>
-    __device__ __forceinline__ void tokens(int t) {
-        float y[kTU][CPL];
+    // U tokens of the stage from t on
+    template <bool OUT, int U>
+    __device__ __forceinline__ void tokens(const E* r, const float* Bs, const float* Cs, int64_t tok, int t) {
+        float st[U], x[U], y[U];
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            // every decay of the group before the recurrence needs the first
-            f32x2 e[kTU][H];
-            float sx[kTU];
+        for (int u = 0; u < U; ++u) {
+            x[u] = value(r[(t + u) * CW + ch]);
+            st[u] = value(r[G::X + (t + u) * CW + ch]);
+        }
+        if (p.softplus) {
 #pragma unroll
-            for (int u = 0; u < kTU; ++u) {
-                const float2 v = step[(t + u) * CH + channel(j)];
-                sx[u] = v.y;
-                if (!OUT) ssum[j] += v.x;
+            for (int u = 0; u < U; ++u) st[u] = softplus1(st[u] + bias);
+        }
 #pragma unroll
-                for (int i = 0; i < H; ++i) e[u][i] = ex2_2(mul2(pack2(v.x, v.x), a2[j][i]));
-            }
+        for (int u = 0; u < U; ++u) {
+            // s and s x of the own channel; the other's come from the neighbour that owns it
+            const float s0 = st[u], x0 = st[u] * x[u];
+            const float s1 = __shfl_xor_sync(0xffffffffu, s0, 1), x1 = __shfl_xor_sync(0xffffffffu, x0, 1);
+            const f32x2 ss[2] = {pack2(s0, s0), pack2(s1, s1)}, xx[2] = {pack2(x0, x0), pack2(x1, x1)};
+            f32x2 acc[2] = {0ull, 0ull};
 #pragma unroll
-            for (int u = 0; u < kTU; ++u) {
-                f32x2 acc = 0ull;
+            for (int i = 0; i < kH; i += 2) {
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(Bs + (t + u) * N + 2 * i);
+                ulonglong2 c = b;
+                if (OUT) c = *reinterpret_cast<const ulonglong2*>(Cs + (t + u) * N + 2 * i);
 #pragma unroll
-                for (int i = 0; i < H; i += 2) {
-                    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(Bs + (t + u) * N + n0 + 2 * i);
-                    h[j][i] = fma2(e[u][i], h[j][i], mul2(pack2(sx[u], sx[u]), b.x));
-                    h[j][i + 1] = fma2(e[u][i + 1], h[j][i + 1], mul2(pack2(sx[u], sx[u]), b.y));
+                for (int j = 0; j < 2; ++j) {
+                    h[j][i] = fma2(ex2_2(mul2(ss[j], a2[j][i])), h[j][i], mul2(xx[j], b.x));
+                    h[j][i + 1] = fma2(ex2_2(mul2(ss[j], a2[j][i + 1])), h[j][i + 1], mul2(xx[j], b.y));
                     if (OUT) {
-                        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(Cs + (t + u) * N + n0 + 2 * i);
-                        acc = i == 0 ? mul2(c.x, h[j][i]) : fma2(c.x, h[j][i], acc);
-                        acc = fma2(c.y, h[j][i + 1], acc);
+                        acc[j] = i == 0 ? mul2(c.x, h[j][i]) : fma2(c.x, h[j][i], acc[j]);
+                        acc[j] = fma2(c.y, h[j][i + 1], acc[j]);
                     }
                 }
-                if (OUT) {
-                    float lo, hi;
-                    unpack2(acc, lo, hi);
-                    y[u][j] = lo + hi;
-                }
+            }
+            if (OUT) {
+                float lo, hi, lo1, hi1;
+                unpack2(acc[0], lo, hi);
+                unpack2(acc[1], lo1, hi1);
+                y[u] = lo + hi + __shfl_xor_sync(0xffffffffu, lo1 + hi1, 1);
+            } else {
+                ssum += st[u];
             }
         }
-        if (OUT) {
-            S::sum(y, threadIdx.x % LPC);
-            // y goes where s was: the lanes of a channel have read it, they met in the sums
+        if (!OUT) return;
 #pragma unroll
-            for (int u = 0; u < S::TK; ++u)
+        for (int off = 2; off < LPC; off <<= 1) {
 #pragma unroll
-                for (int j = 0; j < S::CK; ++j) step[(t + t_own + u) * CH + channel(j)].x = y[u][j];
+            for (int u = 0; u < U; ++u) y[u] += __shfl_xor_sync(0xffffffffu, y[u], off);
+        }
+        if (sub > 1 || ch >= nch) return;
+        if (p.skip) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) y[u] = fmaf(skip, x[u], y[u]);
+        }
+        if (p.z) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) y[u] *= silu_f(value(r[2 * G::X + (t + u) * CW + ch]));
+        }
+        const int64_t o = (tok + t) * p.os[1] + (d0 + ch) * p.os[2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if constexpr (MODE == BF16) static_cast<__nv_bfloat16*>(p.out)[o + u * p.os[1]] = __float2bfloat16_rn(y[u]);
+            else st_out(p.out, o + u * p.os[1], MODE == F32 ? LAR_F32 : p.out_dt, y[u]);
         }
     }
 };
 
-// blockIdx.x: (column of channels, rank in the cluster), blockIdx.y: the span.
-// min_seg: the least tokens worth a block of their own where a span is split.
-template <int N, int SPL, int CPL>
-__global__ void __launch_bounds__(kThreads) ssm_prefill_kernel(const SsmParams p, int ranks, int min_seg) {
-    using G = Geo<N, SPL, CPL>;
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int seq = blockIdx.y, rank = static_cast<int>(blockIdx.x) % ranks;
-    Scan<N, SPL, CPL> sc(p, smem, static_cast<int>(blockIdx.x) / ranks);
-    stream_order();
+// h <- 2^(s a2) h + e for both channels of a lane, s0 and s1 the sums of their steps
+__device__ __forceinline__ void decay_join(f32x2 (*h)[kH], const f32x2 (*a2)[kH], float s0, float s1,
+                                           const f32x2 (*e)[kH]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const f32x2 ss = j ? pack2(s1, s1) : pack2(s0, s0);
+#pragma unroll
+        for (int i = 0; i < kH; ++i) h[j][i] = fma2(ex2_2(mul2(ss, a2[j][i])), h[j][i], e[j][i]);
+    }
+}
+
+// The y-th longest span (equal ones in order); y itself past kSorted spans.  Blocks
+// start in this order: the last ones to start are short.
+constexpr int kSorted = 64;
+
+__device__ __forceinline__ int longest(const SlotParams& s, int y, int* lens, int* found) {
+    if (s.n > kSorted) return y;
     int32_t bits = 0;
+    int begin;
+    for (int i = threadIdx.x; i < s.n; i += kThreads) span_of(s, i, &begin, &lens[i], &bits);
+    __syncthreads();
+    for (int i = threadIdx.x; i < s.n; i += kThreads) {
+        const int li = lens[i];
+        int rank = 0;
+        for (int j = 0; j < s.n; ++j) rank += lens[j] > li || (lens[j] == li && j < i);
+        if (rank == y) *found = i;
+    }
+    __syncthreads();
+    return *found;
+}
+
+// How a launch spreads its work.
+struct Spread {
+    int columns;    // columns of channels
+    int ranks;      // blocks of a cluster that share a column of a span, or 1
+    int min_part;   // ranks > 1: least tokens of a part
+    int long_len;   // ranks 1: spans of more tokens are split over the warps of a block,
+    int long_max;   // and there are at most so many of them
+};
+
+// ranks 1: a block takes four columns of a span, a warp each, or, of a long span, one
+// column whose tokens its warps share.  ranks > 1: the warps of a whole cluster share
+// the tokens of one column.
+template <int N, int MODE, bool VEC, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kernel(const SsmParams p, const Spread w) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    // what a warp (and, behind them, the block) leaves: its lanes' states, four by
+    // four, and the sums of the steps of the channels that its lanes own
+    struct Left {
+        float4 h[kSPL / 2][32];
+        float s[32];
+    };
+    __shared__ int lens[kSorted], found;
+    Left* left = reinterpret_cast<Left*>(smem + kWarps * Geo<N, MODE>::warp_bytes);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int rank = CLUSTER ? static_cast<int>(blockIdx.x) % w.ranks : 0;
+    stream_order();
+    int seq, column, parts, part;   // the span, this warp's column and part of the span's tokens
     int begin, len;
-    span_of(p.s, seq, &begin, &len, &bits);
+    int32_t bits = 0;
+    if (CLUSTER) {
+        seq = blockIdx.y;
+        span_of(p.s, seq, &begin, &len, &bits);
+        column = static_cast<int>(blockIdx.x) / w.ranks;
+        parts = min(w.ranks * kWarps, max(1, len / w.min_part));
+        part = rank * kWarps + warp;
+    } else {
+        // blocks: a column each of the spans that may be long, four of the others
+        const int quads = (w.columns + kWarps - 1) / kWarps;
+        const int64_t b = blockIdx.x, longs = static_cast<int64_t>(w.long_max) * w.columns;
+        const int y = static_cast<int>(b < longs ? b / w.columns : w.long_max + (b - longs) / quads);
+        const int at = static_cast<int>(b < longs ? b % w.columns : (b - longs) % quads);
+        seq = longest(p.s, y, lens, &found);
+        span_of(p.s, seq, &begin, &len, &bits);
+        const bool split = b < longs && len > w.long_len;
+        if (!split && at >= quads) return;   // not long after all: others have its columns
+        column = split ? at : at * kWarps + warp;
+        parts = split ? kWarps : 1;
+        part = split ? warp : 0;
+        if (column >= w.columns) return;     // split blocks are whole: no barrier misses this warp
+    }
+    Scan<N, MODE, VEC> sc(p, smem + warp * Geo<N, MODE>::warp_bytes, column);
     const int64_t slot = read_slot(p.s, seq, &bits), dest = write_slot(p.s, seq, 0, &bits);
-    if (blockIdx.x == 0 && threadIdx.x == 0) flag_err(p.s.dev_err, bits);
-    const int parts = min(ranks, max(1, len / min_seg));
-    if (parts == 1) {
-        if (rank > 0) return;   // the whole cluster agrees
-        sc.load_decay();
-        sc.load_seed(slot);
-        sc.template run<true>(begin, begin + len);
-        sc.store_end(dest);
-        return;
-    }
-    // whole tiles a block; the last ones may have none
-    const int seg = ((len + parts - 1) / parts + G::TT - 1) / G::TT * G::TT;
-    const int lo = min(rank * seg, len), hi = min(lo + seg, len);
-    float* hend = reinterpret_cast<float*>(smem);              // [CPL][SPL / 4][threads] of 4: a lane's own order
-    float* send = hend + kThreads * CPL * SPL;                 // [CPL][threads]
-    sc.load_decay();
+    if (column == 0 && part == 0 && lane == 0) flag_err(p.s.dev_err, bits);
+    // whole stages a part; the last ones may have none
+    const int each = ((len + parts - 1) / parts + kTok - 1) / kTok * kTok;
+    const int lo = static_cast<int>(min(static_cast<int64_t>(part) * each, static_cast<int64_t>(len)));
+    const int hi = min(lo + each, len);
+    sc.load_weights();
+    if (parts > 1) {   // all warps of the block, of the cluster, agree
+        const auto put = [&](Left& to) {
 #pragma unroll
-    for (int j = 0; j < CPL; ++j) {
-        sc.ssum[j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < SPL / 2; ++i) sc.h[j][i] = 0ull;
-    }
-    const bool tail = hi < len;   // somebody comes after this block
-    if (tail) {
-        sc.template run<false>(begin + lo, begin + hi);
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-#pragma unroll
-            for (int i = 0; i < SPL / 4; ++i) {
-                ulonglong2 v;
-                v.x = sc.h[j][2 * i];
-                v.y = sc.h[j][2 * i + 1];
-                *reinterpret_cast<ulonglong2*>(hend + ((j * (SPL / 4) + i) * kThreads + threadIdx.x) * 4) = v;
+            for (int i = 0; i < kSPL / 2; ++i) {
+                const f32x2* h = &sc.h[0][0] + 2 * i;
+                float4 v;
+                unpack2(h[0], v.x, v.y);
+                unpack2(h[1], v.z, v.w);
+                to.h[i][lane] = v;
             }
-            send[j * kThreads + threadIdx.x] = sc.ssum[j];
+            to.s[lane] = sc.ssum;
+        };
+        const auto take = [&](const float4* v, f32x2* e) {
+#pragma unroll
+            for (int i = 0; i < kSPL / 2; ++i) {
+                e[2 * i] = pack2(v[i].x, v[i].y);
+                e[2 * i + 1] = pack2(v[i].z, v[i].w);
+            }
+        };
+        const auto clear = [](f32x2 (*h)[kH]) {
+#pragma unroll
+            for (int i = 0; i < 2 * kH; ++i) h[i / kH][i % kH] = 0ull;
+        };
+        clear(sc.h);
+        sc.ssum = 0.f;
+        if (hi < len) sc.template run<false, tokens_of(CLUSTER)>(begin + lo, begin + hi);   // somebody comes after this warp
+        put(left[warp]);
+        __syncthreads();
+        // what the warps before this one in the block come to; the last one, with its
+        // own part, what the block does
+        f32x2 pre[2][kH];
+        float pre_s = 0.f, pre_t = 0.f;   // sums of steps: the own channel's, the other's
+        clear(pre);
+        for (int v = 0; v < warp; ++v) {
+            float4 q[kSPL / 2];
+            f32x2 e[2][kH];
+#pragma unroll
+            for (int i = 0; i < kSPL / 2; ++i) q[i] = left[v].h[i][lane];
+            take(q, &e[0][0]);
+            const float s0 = left[v].s[lane], s1 = left[v].s[lane ^ 1];
+            decay_join(pre, sc.a2, s0, s1, e);
+            pre_s += s0;
+            pre_t += s1;
         }
-    }
-    cluster_sync();
-    if (lo < len) {
-        sc.load_seed(slot);
-        for (int r = 0; r < rank; ++r) {
+        if (CLUSTER) {
+            if (warp == kWarps - 1) {
+                f32x2 own[2][kH];
 #pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                const float s = ld_peer_f32(send + j * kThreads + threadIdx.x, r);
-                const f32x2 ss = pack2(s, s);
+                for (int i = 0; i < 2 * kH; ++i) {
+                    own[i / kH][i % kH] = sc.h[i / kH][i % kH];
+                    sc.h[i / kH][i % kH] = pre[i / kH][i % kH];
+                }
+                decay_join(sc.h, sc.a2, sc.ssum, __shfl_xor_sync(0xffffffffu, sc.ssum, 1), own);
+                sc.ssum += pre_s;
+                put(left[kWarps]);
+            }
+            cluster_sync();
+        }
+        if (lo < len) {
+            sc.load_seed(slot);
+            if (CLUSTER) {
+                for (int r = 0; r < rank; ++r) {
+                    float4 q[kSPL / 2];
+                    f32x2 e[2][kH];
 #pragma unroll
-                for (int i = 0; i < SPL / 4; ++i) {
-                    const float4 e = ld_peer_f32x4(hend + ((j * (SPL / 4) + i) * kThreads + threadIdx.x) * 4, r);
-                    f32x2* h = &sc.h[j][2 * i];
-                    h[0] = fma2(ex2_2(mul2(ss, sc.a2[j][2 * i])), h[0], pack2(e.x, e.y));
-                    h[1] = fma2(ex2_2(mul2(ss, sc.a2[j][2 * i + 1])), h[1], pack2(e.z, e.w));
+                    for (int i = 0; i < kSPL / 2; ++i)
+                        q[i] = ld_peer_f32x4(reinterpret_cast<const float*>(&left[kWarps].h[i][lane]), r);
+                    const float s0 = ld_peer_f32(&left[kWarps].s[lane], r);
+                    const float s1 = ld_peer_f32(&left[kWarps].s[lane ^ 1], r);
+                    take(q, &e[0][0]);
+                    decay_join(sc.h, sc.a2, s0, s1, e);
                 }
             }
+            decay_join(sc.h, sc.a2, pre_s, pre_t, pre);
         }
+        // all have read their peers, and the seed before any end state is stored
+        if (CLUSTER) cluster_sync();
+        else __syncthreads();
+    } else if (part == 0) {
+        sc.load_seed(slot);
     }
-    cluster_sync();   // all have read their peers, and the seed before any end state is stored
-    if (lo < len) {
-        sc.template run<true>(begin + lo, begin + hi);
-        if (!tail) sc.store_end(dest);
+    if (lo < len || (len == 0 && part == 0)) {
+        sc.template run<true, tokens_of(CLUSTER)>(begin + lo, begin + hi);
+        if (hi == len) sc.store_end(dest);
     }
 }
 
-template <int N, int SPL, int CPL>
-lar_status go(const SsmParams& p, int ranks, int min_seg, cudaStream_t st) {
-    using G = Geo<N, SPL, CPL>;
-    auto kern = ssm_prefill_kernel<N, SPL, CPL>;
-    size_t smem = static_cast<size_t>(parts_of<N, SPL, CPL>(p).total);
-    const size_t joined = static_cast<size_t>(kThreads) * CPL * (SPL + 1) * 4;
-    if (smem < joined) smem = joined;
-    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-        return LAR_ERR_LAUNCH;
-    if (ranks > 8 && cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                          cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return LAR_ERR_LAUNCH;
-    const unsigned columns = static_cast<unsigned>(p.G) * ((p.per_group + G::CH - 1) / G::CH);
-    return launch_ordered(kern, dim3(columns * ranks, p.s.n), kThreads, smem, ranks, st, p, ranks, min_seg);
+template <int N, int MODE, bool VEC>
+lar_status go(const SsmParams& p, cudaStream_t st) {
+    using G = Geo<N, MODE>;
+    Spread w;
+    w.columns = p.G * ((p.per_group + G::CW - 1) / G::CW);
+    const int64_t rows = static_cast<int64_t>(w.columns) * p.s.n;
+    // Clusters where a warp a column leaves the device empty, even if every span is
+    // split over a block: as many blocks as fill it, up to the portable 8 (16 were
+    // slower: 187 us for the 8192 x 2048 above).
+    w.ranks = 1;
+    while (w.ranks < 8 && rows * kWarps * w.ranks < kFill) w.ranks *= 2;
+    w.min_part = 32;
+    // Long: more than 1.5 times the tokens of a warp if all that the device holds had
+    // the same.  Measured at the ragged spans above: 720 us unsplit, 441, 446 and 401
+    // us at 1, 1.25 and 1.5 times, 543 us at twice.
+    const int64_t len = p.s.ntok * w.columns * 3 / (int64_t{2} * kSms * 4 * 3);
+    w.long_len = static_cast<int>(std::min<int64_t>(std::max<int64_t>(len, 64), INT32_MAX));
+    w.long_max = p.s.n > kSorted ? 0 : static_cast<int>(std::min<int64_t>(p.s.n, p.s.ntok / w.long_len));
+    const int smem = kWarps * G::warp_bytes + (kWarps + 1) * (2 * kSPL + 1) * 32 * 4;
+    const auto kern = w.ranks > 1 ? ssm_prefill_kernel<N, MODE, VEC, true> : ssm_prefill_kernel<N, MODE, VEC, false>;
+    const void* k = reinterpret_cast<const void*>(kern);
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return LAR_ERR_LAUNCH;
+    dim3 grid(static_cast<unsigned>(w.columns * w.ranks), p.s.n);
+    if (w.ranks == 1) {
+        const int64_t quads = (w.columns + kWarps - 1) / kWarps;
+        const int64_t blocks = static_cast<int64_t>(w.long_max) * w.columns + (p.s.n - w.long_max) * quads;
+        if (blocks > INT32_MAX) return LAR_ERR_SHAPE;
+        grid = dim3(static_cast<unsigned>(blocks));
+    }
+    return launch_ordered(kern, grid, kThreads, smem, w.ranks, st, p, w);
 }
 
-// Blocks of a span: one where the columns of all spans fill the device twice over,
-// else as many as fill it four times, at most 16 (the largest cluster).
-template <int N, int SPL, int CPL>
+template <int N>
 lar_status pick(const SsmParams& p, cudaStream_t st) {
-    using G = Geo<N, SPL, CPL>;
-    const int64_t rows = static_cast<int64_t>(p.G) * ((p.per_group + G::CH - 1) / G::CH) * p.s.n;
-    int ranks = 1;
-    if (rows < 2 * kSms)
-        while (ranks < 16 && rows * ranks < 4 * kSms && p.s.ntok >= 2 * ranks * kMinSeg) ranks *= 2;
-    return go<N, SPL, CPL>(p, ranks, kMinSeg, st);
+    const int dt = p.x_dt;
+    const bool alike = p.dt_dt == dt && p.B_dt == dt && p.C_dt == dt && p.out_dt == dt && (!p.z || p.z_dt == dt);
+    if (!alike) return go<N, MIXED, false>(p, st);
+    const bool vec = p.vec && p.vec_bc;
+    if (dt == LAR_BF16) return vec ? go<N, BF16, true>(p, st) : go<N, BF16, false>(p, st);
+    return vec ? go<N, F32, true>(p, st) : go<N, F32, false>(p, st);
 }
 
 }  // namespace
@@ -544,10 +553,10 @@ lar_status pick(const SsmParams& p, cudaStream_t st) {
 lar_status launch_ssm_prefill(const SsmParams& p, void* stream) {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (p.N) {
-        case 16: return pick<16, 8, 1>(p, st);
-        case 32: return pick<32, 8, 1>(p, st);
-        case 64: return pick<64, 8, 2>(p, st);
-        default: return pick<128, 8, 2>(p, st);
+        case 16: return pick<16>(p, st);
+        case 32: return pick<32>(p, st);
+        case 64: return pick<64>(p, st);
+        default: return pick<128>(p, st);
     }
 }
 
