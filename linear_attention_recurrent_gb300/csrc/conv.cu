@@ -6,6 +6,8 @@
 // Inputs before the sequence's first token come from its state; rows of a state
 // are the inputs, oldest first, channels innermost.  Bound by memory: 2 W + 5
 // operations for every element that is read and written once.
+#include <algorithm>
+
 #include "layer_common.cuh"
 
 namespace lar {
@@ -13,7 +15,11 @@ namespace lar {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTile = 64;    // tokens of a prefill tile
+constexpr int kTile = 16;    // tokens of a prefill tile, which blocks share out
+#ifndef LAR_CB
+#define LAR_CB 4
+#endif
+constexpr int kBlocks = LAR_CB;   // blocks of the prefill on an SM
 constexpr int kGroup = 4;    // tokens of a group of copies,
 constexpr int kAhead = 3;    // groups asked for ahead of the one in work,
 constexpr int kRing = kGroup * (kAhead + 1);   // and the tokens that the ring holds
@@ -189,15 +195,19 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 6 : 4) conv_token_kernel(c
     }
 }
 
-// Which span and tokens tile `tile` covers: span n takes max(1, ceil(len / kTile))
-// tiles, in order.  False past the last one.  Every thread of the block calls it.
-struct TileOf {
-    int seq, begin, len, first;   // the span, and the tile's first token in it
+// Tiles of all spans in a row: span n takes max(1, ceil(len / kTile)) of them.  A
+// block takes an equal share of the row, in runs of tiles of one span.
+struct Run {
+    int seq, begin, len;   // the span
+    int first, end;        // the run's tokens in it
+    int64_t next;          // the tile behind the run
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + kTile - 1) / kTile : 1; }
 
-__device__ __forceinline__ bool find_tile(const SlotParams& s, int64_t tile, TileOf* found, int64_t* sums) {
+// The run that starts with tile `tile` of this block's share (tile < 0: with its
+// first one).  False past the share's end.  Every thread of the block calls it.
+__device__ __forceinline__ bool find_run(const SlotParams& s, int64_t tile, Run* found, int64_t* sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (s.n + kThreads - 1) / kThreads;
     const int lo = min(tid * per, s.n), hi = min(lo + per, s.n);
@@ -222,11 +232,17 @@ __device__ __forceinline__ bool find_tile(const SlotParams& s, int64_t tile, Til
         if (w < warp) at += sums[w];
         total += sums[w];
     }
-    if (tile >= total) return false;
+    if (tile < 0) tile = total * blockIdx.y / gridDim.y;
+    const int64_t end = total * (blockIdx.y + 1) / gridDim.y;
+    if (tile >= end) return false;
     for (int n = lo; n < hi && tile >= at; ++n) {
         span_of(s, n, &begin, &len, &bits);
         const int k = tiles_of(len);
-        if (tile < at + k) *found = {n, begin, len, static_cast<int>(tile - at) * kTile};
+        if (tile < at + k) {
+            const int64_t next = min(at + k, end);
+            *found = {n, begin, len, static_cast<int>(tile - at) * kTile,
+                      static_cast<int>(min((next - at) * kTile, static_cast<int64_t>(len))), next};
+        }
         at += k;
     }
     __syncthreads();
@@ -237,7 +253,7 @@ __device__ __forceinline__ bool find_tile(const SlotParams& s, int64_t tile, Til
 // shorter.  The thread of the span's first tile does this for its channels: it has
 // read the seed, and the final state may go to the same slot.
 template <int W, int VEC, typename Input>
-__device__ __forceinline__ void close_span(const ConvParams& p, const TileOf& f, int c0, const float (*h)[VEC],
+__device__ __forceinline__ void close_span(const ConvParams& p, const Run& f, int c0, const float (*h)[VEC],
                                            int64_t slot, const Input& input) {
     float e[W - 1][VEC];
 #pragma unroll
@@ -258,16 +274,16 @@ __device__ __forceinline__ void close_span(const ConvParams& p, const TileOf& f,
     store_state<W, VEC>(p, slot, c0, e);
 }
 
-// One tile of tokens of one span a block and step; the W - 1 inputs ahead of it are
-// read again.  Any layout, element by element.
+// The W - 1 inputs ahead of a run are read again.  Any layout, element by element.
 template <int W>
 __global__ void __launch_bounds__(kThreads) conv_prefill_any_kernel(const ConvParams p) {
-    __shared__ TileOf tile_s;
+    __shared__ Run run_s;
     __shared__ int64_t sums[kThreads / 32];
     const int c0 = blockIdx.x * kThreads + threadIdx.x;
     stream_order();
-    for (int64_t tile = blockIdx.y; find_tile(p.s, tile, &tile_s, sums); tile += gridDim.y) {
-        const TileOf f = tile_s;
+    for (int64_t tile = -1; find_run(p.s, tile, &run_s, sums);) {
+        const Run f = run_s;
+        tile = f.next;
         int32_t bits = 0;
         if (c0 < p.C) {
             Taps<W, 1> taps;
@@ -285,9 +301,8 @@ __global__ void __launch_bounds__(kThreads) conv_prefill_any_kernel(const ConvPa
 #pragma unroll
                 for (int j = 0; j + 1 < W; ++j) input(f.first - (W - 1) + j, h[j]);
             }
-            const int end = min(f.first + kTile, f.len);
 #pragma unroll 4
-            for (int t = f.first; t < end; ++t) {
+            for (int t = f.first; t < f.end; ++t) {
                 float u[1], y[1];
                 input(t, u);
                 taps.step(h, u, y, p.silu);
@@ -295,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) conv_prefill_any_kernel(const ConvPa
             }
         }
         if (blockIdx.x == 0 && threadIdx.x == 0) flag_err(p.s.dev_err, bits);
-        __syncthreads();   // tile_s and sums are used again
+        __syncthreads();   // all have read run_s; sums is used again
     }
 }
 
@@ -305,18 +320,19 @@ template <int W, typename X>
 __global__ void __launch_bounds__(kThreads, 4) conv_prefill_kernel(const ConvParams p) {
     constexpr int NCH = sizeof(X) / 2;   // 16-byte pieces of 8 channels
     extern __shared__ __align__(16) unsigned char ring[];   // [kRing][NCH][kThreads] pieces
-    __shared__ TileOf tile_s;
+    __shared__ Run run_s;
     __shared__ int64_t sums[kThreads / 32];
     const int c0 = (blockIdx.x * kThreads + threadIdx.x) * 8;
     unsigned char* mine = ring + threadIdx.x * 16;
     stream_order();
-    for (int64_t tile = blockIdx.y; find_tile(p.s, tile, &tile_s, sums); tile += gridDim.y) {
-        const TileOf f = tile_s;
+    for (int64_t tile = -1; find_run(p.s, tile, &run_s, sums);) {
+        const Run f = run_s;
+        tile = f.next;
         int32_t bits = 0;
         if (c0 < p.C) {
-            const int nt = min(kTile, f.len - f.first);
+            const int nt = f.end - f.first;
             const X* src = static_cast<const X*>(p.x) + static_cast<int64_t>(f.begin + f.first) * p.xs[1] + c0;
-            const auto ask = [&](int g) {   // tokens of group g of the tile
+            const auto ask = [&](int g) {   // tokens of group g of the run
 #pragma unroll
                 for (int u = 0; u < kGroup; ++u) {
                     const int t = g * kGroup + u;
@@ -376,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 4) conv_prefill_kernel(const ConvPar
         }
         if (blockIdx.x == 0 && threadIdx.x == 0) flag_err(p.s.dev_err, bits);
         cp_async_wait<0>();
-        __syncthreads();   // tile_s and sums are used again
+        __syncthreads();   // all have read run_s; sums is used again
     }
 }
 
@@ -415,9 +431,9 @@ lar_status prefill_vec(const ConvParams& p, dim3 grid, cudaStream_t st) {
 template <int W>
 lar_status prefill(const ConvParams& p, cudaStream_t st) {
     const unsigned per = kThreads * (p.vec ? 8 : 1), cb = (p.C + per - 1) / per;
-    // disjoint spans make at most this many tiles; a block goes on to others where they are not
-    const int64_t tiles = p.s.ntok / kTile + p.s.n;
-    const dim3 grid(cb, static_cast<unsigned>(tiles < 65535 ? tiles : 65535));
+    // as many blocks as the device holds at once, if disjoint spans have the tiles
+    const int64_t tiles = p.s.ntok / kTile + p.s.n, held = (kBlocks * 152 + cb - 1) / cb;
+    const dim3 grid(cb, static_cast<unsigned>(std::min(tiles, std::max<int64_t>(held, 1))));
     if (!p.vec) return launch_ordered(conv_prefill_any_kernel<W>, grid, kThreads, 0, 1, st, p);
     return p.x_dt == LAR_BF16 ? prefill_vec<W, unsigned short>(p, grid, st) : prefill_vec<W, float>(p, grid, st);
 }

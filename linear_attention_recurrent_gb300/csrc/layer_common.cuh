@@ -110,6 +110,13 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// its two halves
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ unsigned peer_addr(const void* p, unsigned rank) {
     const unsigned local = static_cast<unsigned>(__cvta_generic_to_shared(p));
     unsigned remote;
@@ -121,6 +128,10 @@ __device__ __forceinline__ float ld_peer_f32(const float* p, unsigned rank) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(p, rank)));
     return v;
+}
+
+__device__ __forceinline__ void st_peer_f32(float* p, unsigned rank, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(p, rank)), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ float4 ld_peer_f32x4(const float* p, unsigned rank) {

@@ -124,7 +124,7 @@ template <int N, int MODE, bool VEC>
 struct Scan {
     using G = Geo<N, MODE>;
     using E = typename G::E;
-    static constexpr int LPC = G::LPC, CW = G::CW, H = kH;
+    static constexpr int LPC = G::LPC, CW = G::CW;
 
     const SsmParams& p;
     unsigned char* mem;        // this warp's shared memory
@@ -249,7 +249,6 @@ struct Scan {
                 Cs = Bs + G::R;
             }
             if (nt == kTok) {
-#pragma unroll
                 for (int t = 0; t < kTok; t += U) tokens<OUT, U>(r, Bs, Cs, tok, t);
             } else {
                 for (int t = 0; t < nt; ++t) tokens<OUT, 1>(r, Bs, Cs, tok, t);
@@ -306,7 +305,12 @@ struct Scan {
                 ssum += st[u];
             }
         }
-        if (!OUT) return;
+        if constexpr (OUT) finish<U>(r, tok, t, x, y);
+    }
+
+    // The sums over the pair's lanes, the skip, the gate and the stores
+    template <int U>
+    __device__ __forceinline__ void finish(const E* r, int64_t tok, int t, const float* x, float* y) const {
 #pragma unroll
         for (int off = 2; off < LPC; off <<= 1) {
 #pragma unroll

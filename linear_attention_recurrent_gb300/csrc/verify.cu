@@ -172,12 +172,14 @@ __device__ __forceinline__ void put_token(const VerifyParams& p, int64_t b, int 
 
 __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) {
     __shared__ Sum warp_tot[kWarps];
-    __shared__ Sum block_tot, before_s, after_s, total_s, start_s;
+    __shared__ Sum blocks[2][kMaxCluster];   // every block's sum, in both passes
+    __shared__ Sum before_s, after_s, total_s, start_s;
     __shared__ int owner_s;
     __shared__ int found[2];
     __shared__ int64_t last_seen;
     const unsigned rank = cluster_rank(), size = cluster_size();
     const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    cluster_arrive();   // this block has started: its memory may be written from now on
     stream_order();
     int32_t bits = 0;
 
@@ -267,14 +269,18 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
         const Sum mine = warp_sum(renormal(hi, lo));
         if (lane == 0) warp_tot[warp] = mine;
         __syncthreads();
+        if (pass == 0) cluster_wait();   // all blocks have
         if (warp == 0) {
+            // to every block of the cluster, so that none reads another's memory later
             const Sum own = warp_sum(lane < kWarps ? warp_tot[lane] : Sum{0.f, 0.f});
-            if (lane == 0) block_tot = own;
+            if (lane < size) {
+                st_peer_f32(&blocks[pass][rank].hi, lane, own.hi);
+                st_peer_f32(&blocks[pass][rank].lo, lane, own.lo);
+            }
         }
         cluster_sync();
         if (warp == 0) {
-            Sum all = {0.f, 0.f};
-            if (lane < size) all = {ld_peer_f32(&block_tot.hi, lane), ld_peer_f32(&block_tot.lo, lane)};
+            const Sum all = lane < size ? blocks[pass][lane] : Sum{0.f, 0.f};
             Sum run = {0.f, 0.f};   // one after another: alike in every block, and never falling
             for (unsigned r = 0; r < size; ++r) {
                 if (r == rank && lane == 0) before_s = run;
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
             }
             if (lane == 0) total_s = run;
         }
-        cluster_sync();   // every block has read the sums: they may be written again
+        __syncthreads();
         total = total_s;
         if (total.hi > 0.f || (row.q == nullptr && row.hot < 0)) break;
         // the residual is empty: draw from the target itself
