@@ -5,7 +5,9 @@
 //
 // Inputs before the sequence's first token come from its state; rows of a state
 // are the inputs, oldest first, channels innermost.  Bound by memory: 2 W + 5
-// operations for every element that is read and written once.
+// operations for every element that is read and written once.  In plain fp32: pairs
+// of channels in one instruction (as the scan has them) cost more moves than they
+// saved, 112 us against 106 in the prefill.
 #include <algorithm>
 
 #include "layer_common.cuh"
@@ -14,12 +16,12 @@ namespace lar {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;   // of a step's blocks
+// Of the prefill's blocks.  16384 x 8192 bf16 on 608 blocks of 128 threads: 105 us; on
+// 1216 of 64: 94 us, 5.7 TB/s of 6.7 (the tokens' groups ahead: 3; 4 and 5 are slower).
+constexpr int kPre = 64;
 constexpr int kTile = 16;    // tokens of a prefill tile, which blocks share out
-#ifndef LAR_CB
-#define LAR_CB 4
-#endif
-constexpr int kBlocks = LAR_CB;   // blocks of the prefill on an SM
+constexpr int kBlocks = 8;   // blocks of the prefill on an SM
 constexpr int kGroup = 4;    // tokens of a group of copies,
 constexpr int kAhead = 3;    // groups asked for ahead of the one in work,
 constexpr int kRing = kGroup * (kAhead + 1);   // and the tokens that the ring holds
@@ -144,8 +146,9 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p)
 }
 
 // One token of NB sequences, 8 channels a thread: the states and inputs of all of
-// them are asked for at once, and the filters are read once.  X: type of x; S: of
-// the pool.
+// them are asked for at once, and the filters, larger than all of them, are read once.
+// X: type of x; S: of the pool.  256 x 8192 bf16: 9.3 us (a sequence at a time 14 us);
+// 5 us of it is the memory's, the rest the way from slot to state to store.
 template <int W, typename X, typename S, int NB>
 __global__ void __launch_bounds__(kThreads, NB == 1 ? 6 : 4) conv_token_kernel(const ConvParams p) {
     const int c0 = (blockIdx.x * kThreads + threadIdx.x) * 8, b0 = blockIdx.y * NB;
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 6 : 4) conv_token_kernel(c
 struct Run {
     int seq, begin, len;   // the span
     int first, end;        // the run's tokens in it
-    int64_t next;          // the tile behind the run
+    int64_t next, last;    // the tile behind the run, and behind the block's share
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + kTile - 1) / kTile : 1; }
@@ -209,7 +212,22 @@ __device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + k
 // first one).  False past the share's end.  Every thread of the block calls it.
 __device__ __forceinline__ bool find_run(const SlotParams& s, int64_t tile, Run* found, int64_t* sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (s.n + kThreads - 1) / kThreads;
+    if (tile >= 0) {   // the tiles behind a run are the next span's
+        const int64_t last = found->last;
+        if (tile >= last) return false;
+        __syncthreads();
+        if (tid == 0) {
+            int32_t bits = 0;
+            const int seq = found->seq + 1;
+            int begin, len;
+            span_of(s, seq, &begin, &len, &bits);
+            const int64_t k = min(static_cast<int64_t>(tiles_of(len)), last - tile);
+            *found = {seq, begin, len, 0, static_cast<int>(min(k * kTile, static_cast<int64_t>(len))), tile + k, last};
+        }
+        __syncthreads();
+        return true;
+    }
+    const int per = (s.n + kPre - 1) / kPre;
     const int lo = min(tid * per, s.n), hi = min(lo + per, s.n);
     int32_t bits = 0;
     int begin, len;
@@ -228,11 +246,11 @@ __device__ __forceinline__ bool find_run(const SlotParams& s, int64_t tile, Run*
     __syncthreads();
     int64_t at = incl - own, total = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kPre / 32; ++w) {
         if (w < warp) at += sums[w];
         total += sums[w];
     }
-    if (tile < 0) tile = total * blockIdx.y / gridDim.y;
+    tile = total * blockIdx.y / gridDim.y;
     const int64_t end = total * (blockIdx.y + 1) / gridDim.y;
     if (tile >= end) return false;
     for (int n = lo; n < hi && tile >= at; ++n) {
@@ -241,7 +259,7 @@ __device__ __forceinline__ bool find_run(const SlotParams& s, int64_t tile, Run*
         if (tile < at + k) {
             const int64_t next = min(at + k, end);
             *found = {n, begin, len, static_cast<int>(tile - at) * kTile,
-                      static_cast<int>(min((next - at) * kTile, static_cast<int64_t>(len))), next};
+                      static_cast<int>(min((next - at) * kTile, static_cast<int64_t>(len))), next, end};
         }
         at += k;
     }
@@ -258,16 +276,16 @@ __device__ __forceinline__ void close_span(const ConvParams& p, const Run& f, in
     float e[W - 1][VEC];
 #pragma unroll
     for (int j = 0; j + 1 < W; ++j) {
-        const int t = f.len - (W - 1) + j;   // may lie before the span
+        const int t = f.len - (W - 1) + j;   // may lie before the span: input f.len + j of the seed
         if (t >= 0) {
             input(t, e[j]);
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                e[j][i] = h[0][i];
+                e[j][i] = h[j][i];
 #pragma unroll
-                for (int k = 1; k + 1 < W; ++k)
-                    if (t + W - 1 == k) e[j][i] = h[k][i];
+                for (int m = 1; m + j + 1 < W; ++m)
+                    if (f.len == m) e[j][i] = h[j + m][i];
             }
         }
     }
@@ -276,10 +294,10 @@ __device__ __forceinline__ void close_span(const ConvParams& p, const Run& f, in
 
 // The W - 1 inputs ahead of a run are read again.  Any layout, element by element.
 template <int W>
-__global__ void __launch_bounds__(kThreads) conv_prefill_any_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kPre) conv_prefill_any_kernel(const ConvParams p) {
     __shared__ Run run_s;
-    __shared__ int64_t sums[kThreads / 32];
-    const int c0 = blockIdx.x * kThreads + threadIdx.x;
+    __shared__ int64_t sums[kPre / 32];
+    const int c0 = blockIdx.x * kPre + threadIdx.x;
     stream_order();
     for (int64_t tile = -1; find_run(p.s, tile, &run_s, sums);) {
         const Run f = run_s;
@@ -317,12 +335,12 @@ __global__ void __launch_bounds__(kThreads) conv_prefill_any_kernel(const ConvPa
 // The same, 8 channels a thread, inputs on their way through a ring of cp.async
 // copies.  A thread reads back only what it copied: the ring needs no barrier.
 template <int W, typename X>
-__global__ void __launch_bounds__(kThreads, 4) conv_prefill_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kPre, kBlocks) conv_prefill_kernel(const ConvParams p) {
     constexpr int NCH = sizeof(X) / 2;   // 16-byte pieces of 8 channels
-    extern __shared__ __align__(16) unsigned char ring[];   // [kRing][NCH][kThreads] pieces
+    extern __shared__ __align__(16) unsigned char ring[];   // [kRing][NCH][kPre] pieces
     __shared__ Run run_s;
-    __shared__ int64_t sums[kThreads / 32];
-    const int c0 = (blockIdx.x * kThreads + threadIdx.x) * 8;
+    __shared__ int64_t sums[kPre / 32];
+    const int c0 = (blockIdx.x * kPre + threadIdx.x) * 8;
     unsigned char* mine = ring + threadIdx.x * 16;
     stream_order();
     for (int64_t tile = -1; find_run(p.s, tile, &run_s, sums);) {
@@ -338,9 +356,9 @@ __global__ void __launch_bounds__(kThreads, 4) conv_prefill_kernel(const ConvPar
                     const int t = g * kGroup + u;
                     if (t < nt) {
                         const X* from = src + t * p.xs[1];
-                        unsigned char* dst = mine + ((g % (kAhead + 1)) * kGroup + u) * NCH * kThreads * 16;
+                        unsigned char* dst = mine + ((g % (kAhead + 1)) * kGroup + u) * NCH * kPre * 16;
 #pragma unroll
-                        for (int k = 0; k < NCH; ++k) cp_async16(dst + k * kThreads * 16, from + k * (16 / sizeof(X)));
+                        for (int k = 0; k < NCH; ++k) cp_async16(dst + k * kPre * 16, from + k * (16 / sizeof(X)));
                     }
                 }
                 cp_async_commit();
@@ -366,13 +384,13 @@ __global__ void __launch_bounds__(kThreads, 4) conv_prefill_kernel(const ConvPar
             for (int g = 0; g * kGroup < nt; ++g) {
                 ask(g + kAhead);
                 cp_async_wait<kAhead>();
-                const unsigned char* at = mine + (g % (kAhead + 1)) * kGroup * NCH * kThreads * 16;
+                const unsigned char* at = mine + (g % (kAhead + 1)) * kGroup * NCH * kPre * 16;
 #pragma unroll
                 for (int u = 0; u < kGroup; ++u) {   // past the last token: what the ring holds, not used
                     Eight<X, false> e;
 #pragma unroll
                     for (int k = 0; k < NCH; ++k)
-                        e.u[k] = *reinterpret_cast<const uint4*>(at + (u * NCH + k) * kThreads * 16);
+                        e.u[k] = *reinterpret_cast<const uint4*>(at + (u * NCH + k) * kPre * 16);
                     e.widen(win[W - 1 + u]);
                 }
 #pragma unroll
@@ -421,20 +439,21 @@ lar_status step(const ConvParams& p, cudaStream_t st) {
 template <int W, typename X>
 lar_status prefill_vec(const ConvParams& p, dim3 grid, cudaStream_t st) {
     const auto kern = conv_prefill_kernel<W, X>;
-    const size_t smem = static_cast<size_t>(kRing) * kThreads * 8 * sizeof(X);
+    const size_t smem = static_cast<size_t>(kRing) * kPre * 8 * sizeof(X);
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
         return LAR_ERR_LAUNCH;
-    return launch_ordered(kern, grid, kThreads, smem, 1, st, p);
+    return launch_ordered(kern, grid, kPre, smem, 1, st, p);
 }
 
 template <int W>
 lar_status prefill(const ConvParams& p, cudaStream_t st) {
-    const unsigned per = kThreads * (p.vec ? 8 : 1), cb = (p.C + per - 1) / per;
+    const unsigned per = kPre * (p.vec ? 8 : 1), cb = (p.C + per - 1) / per;
     // as many blocks as the device holds at once, if disjoint spans have the tiles
-    const int64_t tiles = p.s.ntok / kTile + p.s.n, held = (kBlocks * 152 + cb - 1) / cb;
+    // (element by element, a thread keeps a third of the registers)
+    const int64_t tiles = p.s.ntok / kTile + p.s.n, held = (kBlocks * (p.vec ? 1 : 3) * 152 + cb - 1) / cb;
     const dim3 grid(cb, static_cast<unsigned>(std::min(tiles, std::max<int64_t>(held, 1))));
-    if (!p.vec) return launch_ordered(conv_prefill_any_kernel<W>, grid, kThreads, 0, 1, st, p);
+    if (!p.vec) return launch_ordered(conv_prefill_any_kernel<W>, grid, kPre, 0, 1, st, p);
     return p.x_dt == LAR_BF16 ? prefill_vec<W, unsigned short>(p, grid, st) : prefill_vec<W, float>(p, grid, st);
 }
 

@@ -24,7 +24,8 @@ bool empty(const lar_tensor* t) {
     return false;
 }
 
-// Rank in [lo, hi], non-negative sizes and strides, a pointer unless empty.
+// Rank in [lo, hi], non-negative sizes and strides, a pointer (unless empty) that is
+// aligned to the elements.
 lar_status check(const lar_tensor* t, int lo, int hi, bool index) {
     if (!t) return LAR_ERR_NULL;
     if (t->ndim < 1 || t->ndim > 5 || t->ndim < lo || t->ndim > hi) return LAR_ERR_RANK;
@@ -34,6 +35,7 @@ lar_status check(const lar_tensor* t, int lo, int hi, bool index) {
     }
     if (!t->data && !empty(t)) return LAR_ERR_NULL;
     if (index ? !is_index(t) : !is_float(t)) return LAR_ERR_DTYPE;
+    if (reinterpret_cast<uintptr_t>(t->data) % elem_size(t->dtype)) return LAR_ERR_ALIGN;
     return LAR_OK;
 }
 

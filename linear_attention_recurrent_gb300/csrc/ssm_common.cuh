@@ -65,6 +65,13 @@ __device__ __forceinline__ uint4 load_raw(const SsmParams& p, int64_t slot, int 
     return *reinterpret_cast<const uint4*>(static_cast<const char*>(p.pool) + off * (p.pool_dt == LAR_F32 ? 4 : 2));
 }
 
+// 16 bytes of states from or to p, rounded to nearest even, once, where they are bf16
+template <int SPL>
+__device__ __forceinline__ void store_raw(void* p, const float* h) {
+    if constexpr (SPL == 4) st_state(static_cast<float4*>(p), make_float4(h[0], h[1], h[2], h[3]));
+    else st_state(static_cast<uint4*>(p), pack8(h));
+}
+
 // 4 fp32 or 8 bf16 of them
 template <int SPL>
 __device__ __forceinline__ void raw_states(const uint4 u, float* h) {

@@ -34,7 +34,7 @@ __device__ __forceinline__ float2 ld_pair(const void* base, int64_t off, int64_t
 // SPL states a lane, 16 bytes of the pool; N / SPL lanes a pair of channels.  Any
 // layout and types.
 template <int N, int SPL>
-__global__ void __launch_bounds__(kThreads, SPL == 4 ? 8 : 5) ssm_step_any_kernel(const SsmParams p, int per_block) {
+__global__ void __launch_bounds__(kThreads, 4) ssm_step_any_kernel(const SsmParams p, int per_block) {
     constexpr int LPC = N / SPL;
     constexpr int CPB = 2 * kThreads / LPC;
     __shared__ int64_t from[kMaxSeqs], to[kMaxSeqs];
@@ -89,12 +89,13 @@ __global__ void __launch_bounds__(kThreads, SPL == 4 ? 8 : 5) ssm_step_any_kerne
                     load_row<SPL>(p.B, b * p.bs[0] + t * p.bs[1] + g[1] * p.bs[2] + n0 * p.bs[3], p.bs[3], p.B_dt, Bv);
                     load_row<SPL>(p.C, b * p.cs[0] + t * p.cs[1] + g[1] * p.cs[2] + n0 * p.cs[3], p.cs[3], p.C_dt, Cv);
                 }
-                y[r] = 0.f;
+                float acc[2] = {0.f, 0.f};   // as the pairs below add them: the same bits in any layout
 #pragma unroll
                 for (int k = 0; k < SPL; ++k) {
                     h[r][k] = fmaf(exp2_f(sr * a2[r][k]), h[r][k], sr * xr * Bv[k]);
-                    y[r] = fmaf(Cv[k], h[r][k], y[r]);
+                    acc[k % 2] = fmaf(Cv[k], h[r][k], acc[k % 2]);
                 }
+                y[r] = acc[0] + acc[1];
             }
 #pragma unroll
             for (int off = LPC / 2; off > 0; off >>= 1) {
@@ -173,7 +174,7 @@ struct Token {
 // Everything of the next token, and the next sequence's states, is asked for
 // before the current one is worked on.  ONE: a single token, one state stored.
 template <int N, int SPL, typename X, bool ONE>
-__global__ void __launch_bounds__(kThreads, SPL == 4 ? 7 : 4) ssm_step_kernel(const SsmParams p, int per_block) {
+__global__ void __launch_bounds__(kThreads, SPL == 4 ? (sizeof(X) == 2 ? 7 : 5) : 4) ssm_step_kernel(const SsmParams p, int per_block) {
     constexpr int LPC = N / SPL, H = SPL / 2;
     constexpr int CPB = 2 * kThreads / LPC;
     using Tok = Token<X, SPL>;
@@ -187,10 +188,12 @@ __global__ void __launch_bounds__(kThreads, SPL == 4 ? 7 : 4) ssm_step_kernel(co
     stream_order();
     int32_t bits = 0;
     const bool each = !ONE && p.s.tslot;   // a slot for every token
+    constexpr int PB = 16 / SPL;           // bytes of a state in the pool
+    const auto bytes_of = [&](int64_t slot) { return slot < 0 ? int64_t{-1} : slot * p.ps[0] * PB; };
     const int writes = each ? nb * T : nb;
     for (int i = threadIdx.x; i < writes; i += kThreads)
-        to[i] = each ? write_slot(p.s, b0 + i / T, i % T, &bits) : write_slot(p.s, b0 + i, 0, &bits);
-    if (threadIdx.x < nb) from[threadIdx.x] = read_slot(p.s, b0 + threadIdx.x, &bits);
+        to[i] = bytes_of(each ? write_slot(p.s, b0 + i / T, i % T, &bits) : write_slot(p.s, b0 + i, 0, &bits));
+    if (threadIdx.x < nb) from[threadIdx.x] = bytes_of(read_slot(p.s, b0 + threadIdx.x, &bits));
     if (blockIdx.x == 0) flag_err(p.s.dev_err, bits);
 
     const int g = d / p.per_group;
@@ -221,9 +224,18 @@ __global__ void __launch_bounds__(kThreads, SPL == 4 ? 7 : 4) ssm_step_kernel(co
     if (p.dt_bias) bias = make_float2(p.dt_bias[d * p.dtb_s], p.dt_bias[(d + 1) * p.dtb_s]);
     if (p.skip) skip = make_float2(p.skip[d * p.skip_s], p.skip[(d + 1) * p.skip_s]);
     __syncthreads();
+    // this lane's states in a slot
+    char* const mine = static_cast<char*>(p.pool) + (d * p.ps[1] + n0) * PB;
+    const int64_t other = p.ps[1] * PB;   // and the pair's other channel
     uint4 raw[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) raw[r] = load_raw(p, from[0], d + r, n0);
+    const auto ask_states = [&](int64_t off) {
+        raw[0] = raw[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (off >= 0) {
+            raw[0] = *reinterpret_cast<const uint4*>(mine + off);
+            raw[1] = *reinterpret_cast<const uint4*>(mine + off + other);
+        }
+    };
+    ask_states(from[0]);
     for (int i = 0; i < nb; ++i) {
         f32x2 h[2][H];
 #pragma unroll
@@ -233,19 +245,23 @@ __global__ void __launch_bounds__(kThreads, SPL == 4 ? 7 : 4) ssm_step_kernel(co
 #pragma unroll
             for (int k = 0; k < H; ++k) h[r][k] = pack2(f[2 * k], f[2 * k + 1]);
         }
-        if (i + 1 < nb) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) raw[r] = load_raw(p, from[i + 1], d + r, n0);
-        }
+        if (i + 1 < nb) ask_states(from[i + 1]);
         for (int t = 0; t < T; ++t) {
             const Tok cur = next;
             const bool same = t + 1 < T;   // the next token is this sequence's
-            if (same || i + 1 < nb) {
-                px += same ? p.xs[1] : p.xs[0] - (T - 1) * p.xs[1];
-                pd += same ? p.ds[1] : p.ds[0] - (T - 1) * p.ds[1];
-                if (p.z) pz += same ? p.zs[1] : p.zs[0] - (T - 1) * p.zs[1];
-                pB += same ? p.bs[1] : p.bs[0] - (T - 1) * p.bs[1];
-                pC += same ? p.cs[1] : p.cs[0] - (T - 1) * p.cs[1];
+            if (same) {
+                px += p.xs[1];
+                pd += p.ds[1];
+                pz += p.zs[1];
+                pB += p.bs[1];
+                pC += p.cs[1];
+                ask();
+            } else if (i + 1 < nb) {
+                px += p.xs[0] - (T - 1) * p.xs[1];
+                pd += p.ds[0] - (T - 1) * p.ds[1];
+                pz += p.zs[0] - (T - 1) * p.zs[1];
+                pB += p.bs[0] - (T - 1) * p.bs[1];
+                pC += p.cs[0] - (T - 1) * p.cs[1];
                 ask();
             }
             float x[2], s[2], Bv[SPL], Cv[SPL], y[2];
@@ -289,13 +305,15 @@ __global__ void __launch_bounds__(kThreads, SPL == 4 ? 7 : 4) ssm_step_kernel(co
             }
             po += same ? p.os[1] : p.os[0] - (T - 1) * p.os[1];
             if (live && (each || !same)) {
-                const int64_t slot = to[each ? i * T + t : i];
+                const int64_t off = to[each ? i * T + t : i];
+                if (off >= 0) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float f[SPL];
+                    for (int r = 0; r < 2; ++r) {
+                        float f[SPL];
 #pragma unroll
-                    for (int k = 0; k < H; ++k) unpack2(h[r][k], f[2 * k], f[2 * k + 1]);
-                    store_states<SPL>(p, slot, d + r, n0, f);
+                        for (int k = 0; k < H; ++k) unpack2(h[r][k], f[2 * k], f[2 * k + 1]);
+                        store_raw<SPL>(mine + off + r * other, f);
+                    }
                 }
             }
         }

@@ -132,6 +132,32 @@ def test_prefill(lens, C, W, dtype, pdt, cuda_device):
     assert bool((out[:lead] == 7).all()) and bool((out[off[-1]:] == 7).all())
 
 
+@pytest.mark.parametrize("C,W,dtype", [(8, 4, BF16), (7, 3, F32), (16, 2, F32)])
+def test_prefill_shares(C, W, dtype, cuda_device):
+    """More tokens than the blocks take in one go: shares that begin and end within
+    spans and run over several of them."""
+    dev = cuda_device
+    lens = [9000, 0, 3, 17, 16, 1, 5] + [40] * 100 + [0] * 20 + [1] * 150 + [7000, 2]
+    g = gen(C)
+    off = np.cumsum([0] + lens)
+    n, tok = len(lens), int(off[-1])
+    x = torch.randn(tok, C, generator=g).to(dtype)
+    w, b = params(g, C, W)
+    pool = torch.randn(2 * n, W - 1, C, generator=g)
+    gp = pool.to(dev)
+    read, write = torch.randperm(n, generator=g), torch.randperm(n, generator=g) + n
+    out = lar.conv_prefill(x.to(dev), w.to(dev), gp, torch.tensor(off, device=dev), read.to(dev), write.to(dev),
+                           bias=b.to(dev), silu=True)
+    want = R.f64(pool)
+    ref, bound = np.zeros((tok, C)), np.zeros((tok, C))
+    for i in range(n):
+        ref[off[i]:off[i + 1]], bound[off[i]:off[i + 1]], row = R.conv_tokens(
+            R.f64(x)[off[i]:off[i + 1]], R.f64(w), R.f64(b), R.f64(pool)[read[i]], True)
+        want[write[i]] = row[lens[i]:]
+    R.assert_within(out, ref, bound)
+    assert np.array_equal(R.f64(gp), want)
+
+
 def test_prefill_bad_spans(cuda_device):
     """A reversed span and one past the arrays count as empty: their read state is
     copied, the others run."""

@@ -146,9 +146,42 @@ def test_prefill_long(lens, D, N, cuda_device):
     check_prefill(cuda_device, lens, D, N, 1, F32, F32, True)
 
 
-def test_prefill_many_channels(cuda_device):
-    """Enough blocks that no span is split, several channels a lane."""
-    check_prefill(cuda_device, [40] * 12 + [0, 300], 2056, 16, 1, BF16, F32, True)
+@pytest.mark.parametrize("lens,D,N,G,dtype,pdt", [
+    ([40] * 12 + [0, 300], 2056, 16, 1, BF16, F32),
+    ([20] * 40 + [0, 300, 1, 7, 131], 808, 16, 1, BF16, BF16),      # long spans among many
+    ([150, 3, 0, 65, 64] * 10, 345, 16, 3, BF16, F32),              # no aligned rows
+    ([9] * 66 + [400, 0, 30, 1], 512, 16, 1, F32, F32),             # too many spans to be sorted
+    ([90] * 36, 512, 32, 2, F32, BF16),                             # all alike, all split
+    ([300, 0, 1, 70, 9], 1030, 128, 2, F32, F32),
+    ([33, 100], 4096, 128, 1, BF16, F32)])
+def test_prefill_many_channels(lens, D, N, G, dtype, pdt, cuda_device):
+    """Enough columns of channels that a warp takes one by itself, but for long spans."""
+    check_prefill(cuda_device, lens, D, N, G, dtype, pdt, True)
+
+
+@pytest.mark.parametrize("lens,D", [([200, 1, 0, 77], 48), ([30] * 45, 808)])
+def test_prefill_mixed_types(lens, D, cuda_device):
+    """x, dt, z, B, C and out of different types."""
+    dev, N, n = cuda_device, 16, len(lens)
+    off = np.cumsum([0] + lens)
+    tok = int(off[-1])
+    g, a, opt = inputs(D, (tok,), D, N, 1, F32)
+    a["x"], a["C"], opt["z"] = a["x"].to(BF16), a["C"].to(BF16), opt["z"].to(BF16)
+    pool = torch.zeros(n, D, N, device=dev)
+    out = lar.ssm_prefill(**on(a, dev), **on(opt, dev), pool=pool, cu_seqlens=torch.tensor(off, device=dev),
+                          read_idx=torch.full((n,), -1, device=dev), write_idx=torch.arange(n, device=dev),
+                          dt_softplus=True, out_dtype=F32)
+    step = lar.ssm_decode(**{k: (v[:1] if k != "A" else v) for k, v in on(a, dev).items()},
+                          **{k: (v[:1] if k == "z" else v) for k, v in on(opt, dev).items()}, pool=pool.clone(),
+                          read_idx=torch.tensor([-1], device=dev), write_idx=torch.tensor([0], device=dev),
+                          dt_softplus=True, out_dtype=F32)
+    for i in range(n):
+        if lens[i]:
+            ref, bound, hs, Es = ref_of(a, opt, slice(off[i], off[i + 1]), np.zeros((D, N)))
+            R.assert_within(out[off[i]:off[i + 1]], ref, bound, f"span {i}")
+            R.assert_within(pool[i], hs[-1], Es[-1], f"state {i}")
+    ref, bound, _, _ = ref_of(a, opt, slice(0, 1), np.zeros((D, N)))
+    R.assert_within(step, ref, bound)
 
 
 def test_prefill_equals_steps(cuda_device):

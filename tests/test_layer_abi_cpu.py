@@ -78,6 +78,7 @@ def test_nothing_to_do(lib, kind):
     (dict(out=fake([2, 3, 64], BF16, strides=[192, 32, 1])), 0, STRIDE),      # overlaps itself
     (dict(out=fake([2, 3, 64], BF16, strides=[192, 64, -1])), 0, STRIDE),
     (dict(read_idx=fake([3], I32)), 0, SHAPE), (dict(read_idx=fake([2])), 0, DTYPE),
+    (dict(x=fake([2, 3, 64], BF16, addr=0x7000001)), 0, ALIGN), (dict(read_idx=fake([2], I64, addr=0x7000004)), 0, ALIGN),
     (dict(write_idx=fake([2, 1], I32)), 0, RANK), (dict(write_idx=fake([1], I32)), 0, SHAPE),
     (dict(x=fake([2, 17, 64], BF16), out=fake([2, 17, 64], BF16)), 0, SHAPE),
     (dict(x=fake([2, 0, 64], BF16), out=fake([2, 0, 64], BF16)), 0, SHAPE),
