@@ -489,12 +489,17 @@ class PreparedCall:
         extra = [n for n, t in tensors.items() if t is not None and n not in names]
         if extra:
             raise ValueError(f"{self._name} takes no {', '.join(sorted(extra))}")
-        self._fn = getattr(lib, self._name)
+        # A function object of its own, without argtypes: every argument is the C value
+        # already, and a call need not check them again (2.8 us instead of 4.1 for the
+        # scan's 13 tensors, which is what the smallest steps cost).
+        self._fn = lib[self._name]
+        self._fn.restype = ctypes.c_int
         self._keep = (tensors, dev_err)
         self._dev = _device_of(tensors.values(), dev_err, stream)
         err = dev_err.data_ptr() if dev_err is not None else None
         self._descs = [describe(tensors.get(n)) for n in names]
-        self._args = [_ref(d) for d in self._descs] + tail + [err, _stream(stream, self._dev)]
+        self._args = [ctypes.c_void_p(ctypes.addressof(d) if d is not None else None) for d in self._descs] + \
+            [ctypes.c_uint32(f) for f in tail] + [ctypes.c_void_p(err), ctypes.c_void_p(_stream(stream, self._dev))]
 
     def __call__(self):
         if torch.cuda.current_device() == self._dev.index:

@@ -35,7 +35,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSPL = 8;        // states of a channel on a lane,
 constexpr int kH = kSPL / 2;   // and pairs of them
 constexpr int kTok = 8;        // tokens of a stage
-constexpr int kStages = 3;
 // Tokens whose steps and gates are worked out together, and blocks an SM: a whole
 // stage with the registers of three blocks, or half of one with four, which spans
 // over clusters want (8192 x 2048 x 16: 162 us, with three 181 us; 24 ragged spans of
@@ -60,8 +59,9 @@ struct Geo {
     // a stage: x, dt, z [kTok][CW], B, C [kTok][N] as they come
     static constexpr int X = kTok * CW, R = kTok * N;
     static constexpr int stage = (3 * X + 2 * R) * static_cast<int>(sizeof(E));
+    static constexpr int stages = stage > 3072 ? 2 : 3;         // in work and on their way
     static constexpr int wide = MODE == BF16 ? 2 * R * 4 : 0;   // B, C of the stage in work, in fp32
-    static constexpr int warp_bytes = kStages * stage + wide;
+    static constexpr int warp_bytes = stages * stage + wide;
     static_assert(stage % 16 == 0, "stages start on 16 bytes");
 };
 
@@ -124,7 +124,7 @@ template <int N, int MODE, bool VEC>
 struct Scan {
     using G = Geo<N, MODE>;
     using E = typename G::E;
-    static constexpr int LPC = G::LPC, CW = G::CW;
+    static constexpr int LPC = G::LPC, CW = G::CW, kStages = G::stages;
 
     const SsmParams& p;
     unsigned char* mem;        // this warp's shared memory
@@ -386,8 +386,11 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
         float4 h[kSPL / 2][32];
         float s[32];
     };
+    constexpr int WB = Geo<N, MODE>::warp_bytes;
+    static_assert(WB >= 2 * static_cast<int>(sizeof(Left)) && WB % 16 == 0, "the stages' memory, between the two runs, holds both");
+    const auto left = [&](int v) -> Left& { return *reinterpret_cast<Left*>(smem + v * WB); };
+    Left& whole = *reinterpret_cast<Left*>(smem + sizeof(Left));
     __shared__ int lens[kSorted], found;
-    Left* left = reinterpret_cast<Left*>(smem + kWarps * Geo<N, MODE>::warp_bytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int rank = CLUSTER ? static_cast<int>(blockIdx.x) % w.ranks : 0;
     stream_order();
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
         part = split ? warp : 0;
         if (column >= w.columns) return;     // split blocks are whole: no barrier misses this warp
     }
-    Scan<N, MODE, VEC> sc(p, smem + warp * Geo<N, MODE>::warp_bytes, column);
+    Scan<N, MODE, VEC> sc(p, smem + warp * WB, column);
     const int64_t slot = read_slot(p.s, seq, &bits), dest = write_slot(p.s, seq, 0, &bits);
     if (column == 0 && part == 0 && lane == 0) flag_err(p.s.dev_err, bits);
     // whole stages a part; the last ones may have none
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
         clear(sc.h);
         sc.ssum = 0.f;
         if (hi < len) sc.template run<false, tokens_of(CLUSTER)>(begin + lo, begin + hi);   // somebody comes after this warp
-        put(left[warp]);
+        put(left(warp));
         __syncthreads();
         // what the warps before this one in the block come to; the last one, with its
         // own part, what the block does
@@ -460,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
             float4 q[kSPL / 2];
             f32x2 e[2][kH];
 #pragma unroll
-            for (int i = 0; i < kSPL / 2; ++i) q[i] = left[v].h[i][lane];
+            for (int i = 0; i < kSPL / 2; ++i) q[i] = left(v).h[i][lane];
             take(q, &e[0][0]);
-            const float s0 = left[v].s[lane], s1 = left[v].s[lane ^ 1];
+            const float s0 = left(v).s[lane], s1 = left(v).s[lane ^ 1];
             decay_join(pre, sc.a2, s0, s1, e);
             pre_s += s0;
             pre_t += s1;
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
                 }
                 decay_join(sc.h, sc.a2, sc.ssum, __shfl_xor_sync(0xffffffffu, sc.ssum, 1), own);
                 sc.ssum += pre_s;
-                put(left[kWarps]);
+                put(whole);
             }
             cluster_sync();
         }
@@ -489,9 +492,9 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
                     f32x2 e[2][kH];
 #pragma unroll
                     for (int i = 0; i < kSPL / 2; ++i)
-                        q[i] = ld_peer_f32x4(reinterpret_cast<const float*>(&left[kWarps].h[i][lane]), r);
-                    const float s0 = ld_peer_f32(&left[kWarps].s[lane], r);
-                    const float s1 = ld_peer_f32(&left[kWarps].s[lane ^ 1], r);
+                        q[i] = ld_peer_f32x4(reinterpret_cast<const float*>(&whole.h[i][lane]), r);
+                    const float s0 = ld_peer_f32(&whole.s[lane], r);
+                    const float s1 = ld_peer_f32(&whole.s[lane ^ 1], r);
                     take(q, &e[0][0]);
                     decay_join(sc.h, sc.a2, s0, s1, e);
                 }
@@ -516,11 +519,12 @@ lar_status go(const SsmParams& p, cudaStream_t st) {
     Spread w;
     w.columns = p.G * ((p.per_group + G::CW - 1) / G::CW);
     const int64_t rows = static_cast<int64_t>(w.columns) * p.s.n;
-    // Clusters where a warp a column leaves the device empty, even if every span is
-    // split over a block: as many blocks as fill it, up to the portable 8 (16 were
-    // slower: 187 us for the 8192 x 2048 above).
+    // Clusters where a warp a column leaves the device empty even with every span split
+    // over a block: blocks enough to fill it, with parts of 32 tokens or more, up to the
+    // portable 8 (a span of 8192 x 2048 x 16: 262, 182, 163 us with 2, 4, 8; sizes
+    // between, as 7 with 188 us, fit the device worse than the next power of two).
     w.ranks = 1;
-    while (w.ranks < 8 && rows * kWarps * w.ranks < kFill) w.ranks *= 2;
+    while (w.ranks < 8 && rows * kWarps * w.ranks < kFill && p.s.ntok >= int64_t{128} * w.ranks * p.s.n) w.ranks *= 2;
     w.min_part = 32;
     // Long: more than 1.5 times the tokens of a warp if all that the device holds had
     // the same.  Measured at the ragged spans above: 720 us unsplit, 441, 446 and 401
@@ -528,7 +532,7 @@ lar_status go(const SsmParams& p, cudaStream_t st) {
     const int64_t len = p.s.ntok * w.columns * 3 / (int64_t{2} * kSms * 4 * 3);
     w.long_len = static_cast<int>(std::min<int64_t>(std::max<int64_t>(len, 64), INT32_MAX));
     w.long_max = p.s.n > kSorted ? 0 : static_cast<int>(std::min<int64_t>(p.s.n, p.s.ntok / w.long_len));
-    const int smem = kWarps * G::warp_bytes + (kWarps + 1) * (2 * kSPL + 1) * 32 * 4;
+    const int smem = kWarps * G::warp_bytes;
     const auto kern = w.ranks > 1 ? ssm_prefill_kernel<N, MODE, VEC, true> : ssm_prefill_kernel<N, MODE, VEC, false>;
     const void* k = reinterpret_cast<const void*>(kern);
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return LAR_ERR_LAUNCH;
