@@ -351,8 +351,8 @@ lar_status la_prefill(const lar_tensor* q, const lar_tensor* k, const lar_tensor
  * and out = y, or y / (1 + exp(-y)) with LAR_SILU.  A sequence's state is its last
  * W - 1 inputs; inputs before its first token come from the state it starts from.
  *   x, out   [B, T, C] (rank 2 [B, C] means T = 1), T from 1 to 16; fp32 or bf16,
- *            any strides (out: no two elements at one address).  conv_prefill:
- *            packed spans, [Ntok, C].
+ *            any strides (out and pool: no two elements at one address).
+ *            conv_prefill: packed spans, [Ntok, C].
  *   weight   [C, W], W from 2 to 4; bias [C] or NULL; fp32 or bf16, any strides.
  *   pool     fp32 or bf16 [P, W - 1, C], channel stride 1, any slot and row
  *            strides: row j of a slot is the input W - 1 - j tokens before the
@@ -364,7 +364,10 @@ lar_status la_prefill(const lar_tensor* q, const lar_tensor* k, const lar_tensor
  *            conv_prefill with an empty span copies the read state.
  *   C        from 1 to 2^24.
  * Channels that are contiguous, a multiple of 8, with 16-byte aligned rows move in
- * 16-byte accesses; other layouts element by element.
+ * 16-byte accesses; other layouts element by element, with the same results.  Every
+ * pointer is aligned to its elements (else LAR_ERR_ALIGN).  conv_prefill and ssm_prefill
+ * set their kernel's shared-memory limit (a function attribute) on every call; all calls
+ * of this header from here on may be captured into CUDA graphs.
  * Ownership, streams, errors and aliasing as for the decode calls above: pool and
  * out overlap nothing else of the call, entries name distinct write slots and read
  * no slot that another entry writes; an entry may read a slot that it writes.
@@ -403,7 +406,11 @@ lar_status conv_prefill(const lar_tensor* x, const lar_tensor* weight, const lar
  *            and channel strides that are multiples of 16 bytes.  The arithmetic
  *            is fp32; a bf16 state is rounded to nearest even once per store.
  *   read_idx, write_idx, num_accepted, state_idx, cu_seqlens   as for conv_*.
- *   Dch      from 1 to 2^24.
+ *   Dch      from 1 to 2^24; ssm_prefill refuses a call of 2^31 blocks or more
+ *            (LAR_ERR_SHAPE; a block is at least 4 warps of 64 / (N / 8) channels).
+ * Spans that are long beside the others, or few, are computed in parts that are joined
+ * (equal up to rounding); how depends on the sizes and span lengths alone, so a call
+ * repeated gives the same bits.
  */
 lar_status ssm_decode(const lar_tensor* x, const lar_tensor* dt, const lar_tensor* A, const lar_tensor* B,
                       const lar_tensor* C, const lar_tensor* D, const lar_tensor* z,

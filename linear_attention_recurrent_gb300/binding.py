@@ -105,10 +105,9 @@ def describe(t: torch.Tensor | None):
     d = LarTensor()
     d.data = t.data_ptr()
     d.dtype = _DT[t.dtype]
-    d.ndim = t.dim()
-    for i, (s, st) in enumerate(zip(t.shape, t.stride())):
-        d.shape[i] = s
-        d.stride[i] = st
+    n = d.ndim = t.dim()
+    d.shape[:n] = t.shape
+    d.stride[:n] = t.stride()
     return d
 
 

@@ -131,16 +131,26 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p)
     if (c0 < p.C) {
         Taps<W, VEC> taps;
         taps.load(p, c0);
-        float h[W - 1][VEC];
+        float h[W - 1][VEC], next[VEC];
+        const auto input = [&](int t, float* u) {
+            ld_ch<VEC, true>(p.x, b * p.xs[0] + t * p.xs[1], p.xs[2], c0, p.x_dt, u);
+        };
+        input(0, next);
+        int64_t to = write_slot(p.s, b, 0, &bits);
         load_state<W, VEC>(p, slot, c0, h);
         for (int t = 0; t < p.s.T; ++t) {
             float u[VEC], y[VEC];
-            ld_ch<VEC, true>(p.x, b * p.xs[0] + t * p.xs[1], p.xs[2], c0, p.x_dt, u);
+            const int64_t dest = to;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) u[i] = next[i];
+            if (t + 1 < p.s.T) {   // on its way while this token is worked on
+                input(t + 1, next);
+                if (p.s.tslot) to = write_slot(p.s, b, t + 1, &bits);
+            }
             taps.step(h, u, y, p.silu);
             st_ch<VEC>(p.out, b * p.os[0] + t * p.os[1], p.os[2], c0, p.out_dt, y);
-            if (p.s.tslot) store_state<W, VEC>(p, write_slot(p.s, b, t, &bits), c0, h);
+            if (p.s.tslot || t + 1 == p.s.T) store_state<W, VEC>(p, dest, c0, h);
         }
-        if (!p.s.tslot) store_state<W, VEC>(p, write_slot(p.s, b, 0, &bits), c0, h);
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) flag_err(p.s.dev_err, bits);
 }

@@ -175,11 +175,6 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
     return r;
 }
 
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 __device__ __forceinline__ f32x2 ex2_2(f32x2 a) {
     float lo, hi;
@@ -283,11 +278,5 @@ __device__ __forceinline__ float rcp_f(float x) {
 // y / (1 + e^-y).  Both SFU steps are good to 2 ulp; where e^-y overflows, the
 // reciprocal is 0 and so is the limit.
 __device__ __forceinline__ float silu_f(float y) { return y * rcp_f(1.f + exp2_f(-kLog2e * y)); }
-
-__device__ __forceinline__ f32x2 silu2(f32x2 y) {
-    float lo, hi;
-    unpack2(add2(ex2_2(mul2(y, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f)), lo, hi);
-    return mul2(y, pack2(rcp_f(lo), rcp_f(hi)));
-}
 
 }  // namespace lar

@@ -9,26 +9,6 @@ namespace lar {
 // a polynomial of degree 8, fitted to the relative error (Chebyshev nodes,
 // Lawson's weights): off by 2e-7 at most in fp32 arithmetic, for small u too,
 // where 1 + u would lose it.  Small steps matter: most are near 0.001.
-__device__ __forceinline__ float2 softplus2(float2 v) {
-    const f32x2 u = pack2(exp2_f(-fabsf(v.x) * kLog2e), exp2_f(-fabsf(v.y) * kLog2e));
-    const auto both = [](float c) { return pack2(c, c); };
-    f32x2 q = both(0.005232624243944883f);
-    q = fma2(q, u, both(-0.029504956677556038f));
-    q = fma2(q, u, both(0.07822549343109131f));
-    q = fma2(q, u, both(-0.1366320699453354f));
-    q = fma2(q, u, both(0.1910598874092102f));
-    q = fma2(q, u, both(-0.2484297752380371f));
-    q = fma2(q, u, both(0.3331909477710724f));
-    q = fma2(q, u, both(-0.4999949336051941f));
-    q = fma2(q, u, both(0.9999999403953552f));
-    q = fma2(q, u, pack2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
-    float2 r;
-    unpack2(q, r.x, r.y);
-    return r;
-}
-
-// The same for one, with the coefficients as immediates: where few are wanted at a
-// time, pairs of them would first have to be built in registers.
 __device__ __forceinline__ float softplus1(float v) {
     const float u = exp2_f(-fabsf(v) * kLog2e);
     float q = fmaf(0.005232624243944883f, u, -0.029504956677556038f);

@@ -1,26 +1,32 @@
 // ssm_prefill.cu -- the selective scan over packed spans (ssm_prefill).
 //
 // A warp walks the tokens of (a part of) one span for CW channels with the states
-// in registers, by itself: a lane holds 16 states, N / 16 neighbouring lanes hold a
-// channel.  Inputs come in by cp.async, eight tokens a stage and some stages ahead,
-// into shared memory of the warp's own; B and C are widened there once for all
-// channels.  A lane works out the step, the gate and the output of its channel
-// itself, so warps never wait for one another.
+// in registers, by itself: a lane holds eight states of each of two channels, N / 8
+// neighbouring lanes hold a pair of channels.  Inputs come in by cp.async, eight tokens
+// a stage and a stage ahead, into shared memory of the warp's own; B and C are widened
+// there once for all channels.  The lanes work out the steps, gates and outputs of
+// their channels themselves, so warps never wait for one another.
 //
 // What bounds it, at N = 16 for a (token, channel): 19 SFU operations (32 a clock on
-// an SM, 0.6 clocks), 64 fp32 multiplies and adds (128 a clock, 0.5 clocks), and
-// their issue beside everything else (4 instructions of 32 lanes a clock).  Products
-// are taken in pairs, one instruction for two: operands that lie in neighbouring
-// registers anyway (states, A, B, C).  An earlier form, in which blocks of threads
-// prepared s and s x in shared memory for all lanes of a channel and met at three
-// barriers a tile, needed 154 instructions for a (token, channel).
+// an SM: 0.6 clocks), 64 fp32 multiplies and adds (128 a clock: 0.5 clocks), and their
+// issue beside everything else: 116 instructions of 32 lanes, four a clock, 0.9
+// clocks.  Products are taken in pairs, one instruction for two: their operands lie in
+// neighbouring registers anyway.  A lane has eight states of each of two channels, of
+// which it owns one: it works out that one's step, gate and output, and gets the other's
+// step from the neighbour that owns it; so B and C, which every lane reads from shared
+// memory for itself, serve two channels (with 16 states of one channel a lane, N = 64
+// and 128 took 1.6 and 2.4 times as long).  64 spans of 256 tokens, 4096 channels:
+// 290 us, 1.2 clocks a (token, channel), at 68 % of the issue slots.  An earlier form,
+// in which blocks prepared the steps of all channels in shared memory and met at three
+// barriers a tile, had 154 instructions.
 //
-// Few rows, long spans: the tokens of a span are split over the warps of a cluster
-// of blocks.  Every warp but the last first runs its tokens from a zero state and
-// keeps the end state and the sum of its steps (the decay over its part is exp(A
-// sum)); they are joined within a block, then over the blocks through distributed
-// shared memory, and every warp runs its tokens again from the state it starts
-// with, now with outputs.
+// Long spans among others: a block's four warps share the tokens of one column.  Every
+// warp but the last first runs its tokens from a zero state and keeps the end state and
+// the sum of its steps (the decay over its part is exp(A sum)); the parts before it,
+// joined, are the state that each then starts from, with outputs this time.  That is
+// 1.7 times the work.  Few rows: the same over the blocks of a cluster, through
+// distributed shared memory.  8192 tokens, 2048 channels: 163 us (unsplit 940 us);
+// 24 ragged spans of 16384 tokens, 4096 channels: 366 us (unsplit 720 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -59,7 +65,7 @@ struct Geo {
     // a stage: x, dt, z [kTok][CW], B, C [kTok][N] as they come
     static constexpr int X = kTok * CW, R = kTok * N;
     static constexpr int stage = (3 * X + 2 * R) * static_cast<int>(sizeof(E));
-    static constexpr int stages = stage > 3072 ? 2 : 3;         // in work and on their way
+    static constexpr int stages = 2;                            // in work and on its way
     static constexpr int wide = MODE == BF16 ? 2 * R * 4 : 0;   // B, C of the stage in work, in fp32
     static constexpr int warp_bytes = stages * stage + wide;
     static_assert(stage % 16 == 0, "stages start on 16 bytes");

@@ -31,6 +31,9 @@ def cu(t, dev):
     (4, 16, 264, 4, BF16, BF16, True),
     (2, 3, 2056, 2, F32, F32, True),
     (70, 1, 72, 4, BF16, BF16, False),
+    (81, 1, 8192, 4, BF16, BF16, True),      # several sequences a thread
+    (81, 1, 8192, 3, F32, BF16, True),
+    (81, 1, 8192, 2, BF16, F32, True),
 ])
 def test_decode(B, T, C, W, dtype, pdt, silu, cuda_device):
     dev = cuda_device

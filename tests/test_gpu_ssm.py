@@ -42,6 +42,9 @@ def ref_of(a, opt, pick, seed):
     (2, 2, 128, 128, 128, BF16, F32, True),
     (66, 1, 520, 16, 1, BF16, F32, True),
     (67, 2, 24, 32, 1, F32, BF16, True),
+    (71, 1, 2048, 16, 1, BF16, F32, True),       # several sequences a block
+    (71, 3, 2048, 16, 2, BF16, BF16, True),
+    (71, 2, 2047, 16, 1, F32, F32, False),
 ])
 def test_decode(B, T, D, N, G, dtype, pdt, full, cuda_device):
     dev = cuda_device

@@ -47,10 +47,10 @@ def test_random(B, T, V, dtype, drafts, cuda_device):
     check(cuda_device, p, q, tok, u, v, nd=torch.arange(B, dtype=torch.int32) % T)
 
 
-@pytest.mark.parametrize("V", [100, 131072, 1 << 18])
-def test_flat_rows(V, cuda_device):
+@pytest.mark.parametrize("V,B", [(100, 24), (131072, 24), (1 << 18, 24), ((1 << 20) + 3, 5)])
+def test_flat_rows(V, B, cuda_device):
     """Neighbouring running sums 1 / V apart: sums of 32 bits would miss the token."""
-    B, T = 24, 2
+    T = 2
     p, q, tok, u, v = case(V, B, T, V, sharp=0.01, near=0.01)
     u[:] = 0.9999                                      # mostly rejected: the residual is drawn from
     q[:, :, ::2] *= 0.5
@@ -109,6 +109,21 @@ def test_empty_and_odd_weights(cuda_device):
     p[3, 0, int(tok[3, 0])], p[2, 0, int(tok[2, 0])] = 1e-6, 1e-6
     acc, out = check(dev, p, q, tok, u, v, dev_err=err)
     assert out[1].tolist() == [-1, -1] and int(err) == lar.LAR_DEVERR_PROBS
+
+
+def test_large_rows_without_residual(cuda_device):
+    """The second look at a row, drawn from the target, where the vocabulary is spread
+    over blocks and a warp's stretch over several turns; weight in its last tokens only."""
+    p, q, tok, u, v = case(21, 4, 2, 300007)
+    q[:] = p[:, :1]
+    u[:] = 1.0
+    p[2, 0, :-3], q[2] = 0, 1.0
+    tok[2] = 5
+    p[3, 0] = 0
+    p[3, 0, 299990] = 1e-20
+    q[3] = 1.0
+    acc, out = check(cuda_device, p, q, tok, u, v)
+    assert (acc == 1).all() and out[2, 0] >= 300004 and out[3, 0] == 299990
 
 
 def test_bad_tokens_and_counts(cuda_device):
