@@ -152,8 +152,8 @@ enum {
                                   (sequence, head) skipped the rest of its span and its writeback */
     LAR_DEVERR_DRAFT = 32,     /* spec_verify: some drafted token outside [0, V) (rejected), or some
                                   num_draft[b] outside [0, T - 1] (taken as the nearer end) */
-    LAR_DEVERR_PROBS = 64      /* spec_verify: some row to draw from has no positive finite weight
-                                  (its token is -1) */
+    LAR_DEVERR_PROBS = 64      /* spec_verify: some row to draw from has no positive finite weight,
+                                  or a sum that fp32 does not hold (its token is -1) */
 };
 
 /*
@@ -352,7 +352,7 @@ lar_status la_prefill(const lar_tensor* q, const lar_tensor* k, const lar_tensor
  * W - 1 inputs; inputs before its first token come from the state it starts from.
  *   x, out   [B, T, C] (rank 2 [B, C] means T = 1), T from 1 to 16; fp32 or bf16,
  *            any strides (out and pool: no two elements at one address).
- *            conv_prefill: packed spans, [Ntok, C].
+ *            conv_prefill: packed spans, [Ntok, C], Ntok to 2^30.
  *   weight   [C, W], W from 2 to 4; bias [C] or NULL; fp32 or bf16, any strides.
  *   pool     fp32 or bf16 [P, W - 1, C], channel stride 1, any slot and row
  *            strides: row j of a slot is the input W - 1 - j tokens before the
@@ -395,7 +395,7 @@ lar_status conv_prefill(const lar_tensor* x, const lar_tensor* weight, const lar
  * without z: out = y; without D (NULL): no skip term.  g = d / (Dch / G), Dch
  * channels in G groups (G divides Dch).
  *   x, dt, z, out   [B, T, Dch] (rank 2 for T = 1), T from 1 to 16; ssm_prefill:
- *            [Ntok, Dch].  fp32 or bf16, any strides (out: no two elements at one
+ *            [Ntok, Dch], Ntok to 2^30.  fp32 or bf16, any strides (out: no two elements at one
  *            address); z may be NULL.
  *   A        fp32 [Dch, N], any strides (usually negative); N 16, 32, 64 or 128.
  *   B, C     [B, T, G, N] (rank 3 [B, G, N] for T = 1; packed [Ntok, G, N]), fp32

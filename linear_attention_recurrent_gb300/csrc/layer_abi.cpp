@@ -161,7 +161,8 @@ lar_status check_where(const Where& w, const lar_tensor* lead, int rest, SlotPar
         LAR_TRY(check(w.cu_seqlens, 1, 1, true));
         n = w.cu_seqlens->shape[0] - 1;
         if (lead->ndim != 1 + rest) return LAR_ERR_RANK;
-        if (n < 0 || n > 65535 || lead->shape[0] > INT32_MAX) return LAR_ERR_SHAPE;
+        // places in the token arrays, and a part's end past them, fit 32 bits in the kernels
+        if (n < 0 || n > 65535 || lead->shape[0] > (1 << 30)) return LAR_ERR_SHAPE;
         s.cu = w.cu_seqlens->data;
         s.cu_s = w.cu_seqlens->stride[0];
         s.cu_dt = w.cu_seqlens->dtype;

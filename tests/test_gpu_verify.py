@@ -111,6 +111,17 @@ def test_empty_and_odd_weights(cuda_device):
     assert out[1].tolist() == [-1, -1] and int(err) == lar.LAR_DEVERR_PROBS
 
 
+def test_sum_past_fp32(cuda_device):
+    """Finite weights whose sum overflows: -1 and a flag, as without any weight."""
+    p, q, tok, u, v = case(9, 2, 2, 5000)
+    p[0, 0, [3, 4000]] = 3e38
+    tok[:], p[:, 0, 7] = 7, 0                          # rejected
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    acc, out = run(cuda_device, p, q, tok, u, v, dev_err=err)
+    assert acc.tolist() == [1, 1] and out[0].tolist() == [-1, -1] and int(err) == lar.LAR_DEVERR_PROBS
+    assert 0 <= out[1, 0] < 5000
+
+
 def test_large_rows_without_residual(cuda_device):
     """The second look at a row, drawn from the target, where the vocabulary is spread
     over blocks and a warp's stretch over several turns; weight in its last tokens only."""

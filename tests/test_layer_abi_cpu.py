@@ -129,6 +129,7 @@ def test_slots_refuse(lib, form, make, flags):
     assert call(lib, form, "prefill", dict(a, cu_seqlens=fake([0], I32)), flags) == SHAPE
     assert call(lib, form, "prefill", dict(a, read_idx=fake([3], I32)), flags) == SHAPE
     assert call(lib, form, "prefill", dict(a, x=fake([1, 20, 64], BF16)), flags) == RANK
+    assert call(lib, form, "prefill", dict(a, x=fake([2**30 + 1, 64], BF16)), flags) == SHAPE
 
 
 @pytest.mark.parametrize("form,make,flags", [("conv", conv_args, 16), ("ssm", ssm_args, 32)])
