@@ -151,20 +151,36 @@ __device__ __forceinline__ float exp2_f(float x) {
 }
 
 // Two fp32 numbers in a register pair: one instruction issued for two products.
-using f32x2 = float2;
+using f32x2 = unsigned long long;
 
-__device__ __forceinline__ f32x2 pack2(float lo, float hi) { return make_float2(lo, hi); }
-
-__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
-    lo = v.x;
-    hi = v.y;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
 
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
 
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
-__device__ __forceinline__ f32x2 ex2_2(f32x2 a) { return make_float2(exp2_f(a.x), exp2_f(a.y)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+
+__device__ __forceinline__ f32x2 ex2_2(f32x2 a) {
+    float lo, hi;
+    unpack2(a, lo, hi);
+    return pack2(exp2_f(lo), exp2_f(hi));
+}
 
 // 8 neighbouring channels as fp32, 16-byte loads; NC: through the read-only path
 // (never for the pool, which the same call writes).

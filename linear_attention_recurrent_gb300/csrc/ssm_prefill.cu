@@ -286,19 +286,19 @@ struct Scan {
             const float s0 = st[u], x0 = st[u] * x[u];
             const float s1 = __shfl_xor_sync(0xffffffffu, s0, 1), x1 = __shfl_xor_sync(0xffffffffu, x0, 1);
             const f32x2 ss[2] = {pack2(s0, s0), pack2(s1, s1)}, xx[2] = {pack2(x0, x0), pack2(x1, x1)};
-            f32x2 acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+            f32x2 acc[2] = {0ull, 0ull};
 #pragma unroll
             for (int i = 0; i < kH; i += 2) {
-                const float4 b = *reinterpret_cast<const float4*>(Bs + (t + u) * N + 2 * i);
-                float4 c = b;
-                if (OUT) c = *reinterpret_cast<const float4*>(Cs + (t + u) * N + 2 * i);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(Bs + (t + u) * N + 2 * i);
+                ulonglong2 c = b;
+                if (OUT) c = *reinterpret_cast<const ulonglong2*>(Cs + (t + u) * N + 2 * i);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    h[j][i] = fma2(ex2_2(mul2(ss[j], a2[j][i])), h[j][i], mul2(xx[j], pack2(b.x, b.y)));
-                    h[j][i + 1] = fma2(ex2_2(mul2(ss[j], a2[j][i + 1])), h[j][i + 1], mul2(xx[j], pack2(b.z, b.w)));
+                    h[j][i] = fma2(ex2_2(mul2(ss[j], a2[j][i])), h[j][i], mul2(xx[j], b.x));
+                    h[j][i + 1] = fma2(ex2_2(mul2(ss[j], a2[j][i + 1])), h[j][i + 1], mul2(xx[j], b.y));
                     if (OUT) {
-                        acc[j] = i == 0 ? mul2(pack2(c.x, c.y), h[j][i]) : fma2(pack2(c.x, c.y), h[j][i], acc[j]);
-                        acc[j] = fma2(pack2(c.z, c.w), h[j][i + 1], acc[j]);
+                        acc[j] = i == 0 ? mul2(c.x, h[j][i]) : fma2(c.x, h[j][i], acc[j]);
+                        acc[j] = fma2(c.y, h[j][i + 1], acc[j]);
                     }
                 }
             }
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
         };
         const auto clear = [](f32x2 (*h)[kH]) {
 #pragma unroll
-            for (int i = 0; i < 2 * kH; ++i) h[i / kH][i % kH] = pack2(0.f, 0.f);
+            for (int i = 0; i < 2 * kH; ++i) h[i / kH][i % kH] = 0ull;
         };
         clear(sc.h);
         sc.ssum = 0.f;

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, SPL == 4 ? (sizeof(X) == 2 ? 7 : 5) 
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const f32x2 ss = pack2(s[r], s[r]), xx = pack2(s[r] * x[r], s[r] * x[r]);
-                f32x2 acc = pack2(0.f, 0.f);
+                f32x2 acc = 0ull;
 #pragma unroll
                 for (int k = 0; k < H; ++k) {
                     h[r][k] = fma2(ex2_2(mul2(ss, a2[r][k])), h[r][k], mul2(xx, pack2(Bv[2 * k], Bv[2 * k + 1])));
