@@ -175,7 +175,6 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
     return r;
 }
 
-
 __device__ __forceinline__ f32x2 ex2_2(f32x2 a) {
     float lo, hi;
     unpack2(a, lo, hi);

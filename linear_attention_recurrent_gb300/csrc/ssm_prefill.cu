@@ -16,7 +16,9 @@
 // step from the neighbour that owns it; so B and C, which every lane reads from shared
 // memory for itself, serve two channels (with 16 states of one channel a lane, N = 64
 // and 128 took 1.6 and 2.4 times as long).  64 spans of 256 tokens, 4096 channels:
-// 290 us, 1.2 clocks a (token, channel), at 68 % of the issue slots.  An earlier form,
+// 293 us, 1.2 clocks a (token, channel), at 68 % of the issue slots: an instruction on
+// pairs (32 of the 116) holds dispatch and its pipe for two cycles, which the counters
+// show as what warps wait for.  An earlier form,
 // in which blocks prepared the steps of all channels in shared memory and met at three
 // barriers a tile, had 154 instructions.
 //
@@ -25,8 +27,10 @@
 // the sum of its steps (the decay over its part is exp(A sum)); the parts before it,
 // joined, are the state that each then starts from, with outputs this time.  That is
 // 1.7 times the work.  Few rows: the same over the blocks of a cluster, through
-// distributed shared memory.  8192 tokens, 2048 channels: 163 us (unsplit 940 us);
-// 24 ragged spans of 16384 tokens, 4096 channels: 366 us (unsplit 720 us).
+// distributed shared memory.  8192 tokens, 2048 channels: 158 us (unsplit 940 us);
+// 24 ragged spans of 16384 tokens, 4096 channels: 400 us (unsplit 720 us).  With the
+// first part's outputs made at once from the seed, as 1.4 times the work, the loop
+// around both runs cost more than it saved: 167 and 416 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -43,7 +47,7 @@ constexpr int kH = kSPL / 2;   // and pairs of them
 constexpr int kTok = 8;        // tokens of a stage
 // Tokens whose steps and gates are worked out together, and blocks an SM: a whole
 // stage with the registers of three blocks, or half of one with four, which spans
-// over clusters want (8192 x 2048 x 16: 162 us, with three 181 us; 24 ragged spans of
+// over clusters want (8192 x 2048 x 16: 158 us, with three 181 us; 24 ragged spans of
 // 16384 x 4096 x 16 within blocks: 401 us with three, 450 us with four).
 __host__ __device__ constexpr int tokens_of(bool cluster) { return cluster ? 4 : kTok; }
 __host__ __device__ constexpr int blocks_of(bool cluster) { return cluster ? 4 : 3; }
@@ -340,14 +344,34 @@ struct Scan {
     }
 };
 
-// h <- 2^(s a2) h + e for both channels of a lane, s0 and s1 the sums of their steps
-__device__ __forceinline__ void decay_join(f32x2 (*h)[kH], const f32x2 (*a2)[kH], float s0, float s1,
+// h <- 2^(s a2) h + e for both channels of a lane, s0 and s1 the sums of their steps.
+// Where the state decays (falls: no a2 above 0) in one factor.  Over a long part a
+// growing factor may be past fp32 where its product with h is not, with an empty h
+// above all: it is taken in two halves, and half of it is past fp32 only where the
+// product with the least h is, too.
+__device__ __forceinline__ void decay_join(f32x2 (*h)[kH], const f32x2 (*a2)[kH], bool falls, float s0, float s1,
                                            const f32x2 (*e)[kH]) {
+    if (falls && s0 >= 0.f && s1 >= 0.f) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x2 ss = j ? pack2(s1, s1) : pack2(s0, s0);
+#pragma unroll
+            for (int i = 0; i < kH; ++i) h[j][i] = fma2(ex2_2(mul2(ss, a2[j][i])), h[j][i], e[j][i]);
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const f32x2 ss = j ? pack2(s1, s1) : pack2(s0, s0);
+        const float half = 0.5f * (j ? s1 : s0);
 #pragma unroll
-        for (int i = 0; i < kH; ++i) h[j][i] = fma2(ex2_2(mul2(ss, a2[j][i])), h[j][i], e[j][i]);
+        for (int i = 0; i < kH; ++i) {
+            float v[2], f[2];
+            unpack2(mul2(pack2(half, half), a2[j][i]), v[0], v[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) f[k] = v[k] > 127.f ? 0x1p127f : exp2_f(v[k]);   // a NaN stays one
+            const f32x2 ff = pack2(f[0], f[1]);
+            h[j][i] = fma2(mul2(h[j][i], ff), ff, e[j][i]);
+        }
     }
 }
 
@@ -455,6 +479,13 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
 #pragma unroll
             for (int i = 0; i < 2 * kH; ++i) h[i / kH][i % kH] = 0ull;
         };
+        bool falls = true;
+#pragma unroll
+        for (int i = 0; i < 2 * kH; ++i) {
+            float a, b;
+            unpack2(sc.a2[i / kH][i % kH], a, b);
+            falls = falls && a <= 0.f && b <= 0.f;
+        }
         clear(sc.h);
         sc.ssum = 0.f;
         if (hi < len) sc.template run<false, tokens_of(CLUSTER)>(begin + lo, begin + hi);   // somebody comes after this warp
@@ -472,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
             for (int i = 0; i < kSPL / 2; ++i) q[i] = left(v).h[i][lane];
             take(q, &e[0][0]);
             const float s0 = left(v).s[lane], s1 = left(v).s[lane ^ 1];
-            decay_join(pre, sc.a2, s0, s1, e);
+            decay_join(pre, sc.a2, falls, s0, s1, e);
             pre_s += s0;
             pre_t += s1;
         }
@@ -484,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
                     own[i / kH][i % kH] = sc.h[i / kH][i % kH];
                     sc.h[i / kH][i % kH] = pre[i / kH][i % kH];
                 }
-                decay_join(sc.h, sc.a2, sc.ssum, __shfl_xor_sync(0xffffffffu, sc.ssum, 1), own);
+                decay_join(sc.h, sc.a2, falls, sc.ssum, __shfl_xor_sync(0xffffffffu, sc.ssum, 1), own);
                 sc.ssum += pre_s;
                 put(whole);
             }
@@ -502,10 +533,10 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
                     const float s0 = ld_peer_f32(&whole.s[lane], r);
                     const float s1 = ld_peer_f32(&whole.s[lane ^ 1], r);
                     take(q, &e[0][0]);
-                    decay_join(sc.h, sc.a2, s0, s1, e);
+                    decay_join(sc.h, sc.a2, falls, s0, s1, e);
                 }
             }
-            decay_join(sc.h, sc.a2, pre_s, pre_t, pre);
+            decay_join(sc.h, sc.a2, falls, pre_s, pre_t, pre);
         }
         // all have read their peers, and the seed before any end state is stored
         if (CLUSTER) cluster_sync();
@@ -527,7 +558,7 @@ lar_status go(const SsmParams& p, cudaStream_t st) {
     const int64_t rows = static_cast<int64_t>(w.columns) * p.s.n;
     // Clusters where a warp a column leaves the device empty even with every span split
     // over a block: blocks enough to fill it, with parts of 32 tokens or more, up to the
-    // portable 8 (a span of 8192 x 2048 x 16: 262, 182, 163 us with 2, 4, 8; sizes
+    // portable 8 (a span of 8192 x 2048 x 16: 262, 182, 163 us with 2, 4, 8 when chosen; sizes
     // between, as 7 with 188 us, fit the device worse than the next power of two).
     w.ranks = 1;
     while (w.ranks < 8 && rows * kWarps * w.ranks < kFill && p.s.ntok >= int64_t{128} * w.ranks * p.s.n) w.ranks *= 2;

@@ -162,6 +162,50 @@ def test_prefill_many_channels(lens, D, N, G, dtype, pdt, cuda_device):
     check_prefill(cuda_device, lens, D, N, G, dtype, pdt, True)
 
 
+@pytest.mark.parametrize("lens,D", [([1500], 64), ([20] * 40 + [0, 600, 1], 808)])
+def test_prefill_empty_state_that_would_grow(lens, D, cuda_device):
+    """A is positive and inputs come late: the factor over a part of a split span is
+    past fp32, the state that it multiplies is zero."""
+    dev, N, n = cuda_device, 16, len(lens)
+    off = np.cumsum([0] + lens)
+    g, a, _ = inputs(4, (int(off[-1]),), D, N, 1, F32, False)
+    a["A"] = 20 * torch.rand(D, N, generator=g)
+    for i in range(n):
+        a["x"][off[i]:max(off[i + 1] - 6, off[i])] = 0
+    pool = torch.ones(n, D, N, device=dev)
+    out = lar.ssm_prefill(**on(a, dev), pool=pool, cu_seqlens=torch.tensor(off, device=dev),
+                          read_idx=torch.full((n,), -1, device=dev), write_idx=torch.arange(n, device=dev))
+    for i in range(n):
+        if lens[i]:
+            ref, bound, hs, Es = ref_of(a, {}, slice(off[i], off[i + 1]), np.zeros((D, N)))
+            R.assert_within(out[off[i]:off[i + 1]], ref, bound, f"span {i}")
+            R.assert_within(pool[i], hs[-1], Es[-1], f"state {i}")
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_prefill_small_state_grows(sign, cuda_device):
+    """A state near the least fp32 numbers grows by e^150 over a split span: its product
+    with the factor over a part fits where the factor does not.  The steps may be the
+    negative ones."""
+    dev, D, N, lens = cuda_device, 808, 16, [20] * 40 + [0, 600, 1]
+    off = np.cumsum([0] + lens)
+    n, i = len(lens), 41
+    g, a, _ = inputs(5, (int(off[-1]),), D, N, 1, F32, False)
+    a["A"] = sign * (1.5 + 0.1 * torch.rand(D, N, generator=g))
+    a["dt"], a["x"][:] = sign * a["dt"], 0
+    pool = 1e-36 * (1 + torch.rand(n, D, N, generator=g))
+    gp = pool.to(dev)
+    out = lar.ssm_prefill(**on(a, dev), pool=gp, cu_seqlens=torch.tensor(off, device=dev),
+                          read_idx=torch.arange(n, device=dev))
+    ref, bound, hs, Es = ref_of(a, {}, slice(off[i], off[i + 1]), R.f64(pool)[i])
+    # a sum of L steps in fp32 is off by at most L 2^-24 of itself, its exponent by that
+    # times A: so much of |C| |h|, summed, for the outputs
+    more = lens[i] * 2.0**-24 * np.abs(R.f64(a["A"]) * R.f64(a["dt"])[off[i]:off[i + 1], :].sum(0)[:, None])
+    c = np.abs(R.f64(a["C"])[off[i]:off[i + 1], 0])
+    R.assert_within(out[off[i]:off[i + 1]], ref, bound + np.einsum("tn,tdn->td", c, np.abs(hs) * more), "out")
+    R.assert_within(gp[i], hs[-1], Es[-1] + np.abs(hs[-1]) * more, "state")
+
+
 @pytest.mark.parametrize("lens,D", [([200, 1, 0, 77], 48), ([30] * 45, 808)])
 def test_prefill_mixed_types(lens, D, cuda_device):
     """x, dt, z, B, C and out of different types."""
