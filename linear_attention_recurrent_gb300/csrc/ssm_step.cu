@@ -11,8 +11,10 @@
 // state, is read once for all of them, and asks for the next sequence's states
 // before it works on the current ones.  256 x 4096 x 16, fp32 states: 27 us for 143 MB
 // (5.3 TB/s; one sequence a block with single loads: 139 us); 64 sequences of 4 tokens
-// with a bf16 state stored after each: 16 us for 50 MB, bound by the tokens' way
+// with a bf16 state stored after each: 15 us for 50 MB, bound by the tokens' way
 // through one another and by issue (about 300 instructions a lane and token).
+#include <algorithm>
+
 #include "ssm_common.cuh"
 
 namespace lar {
@@ -176,8 +178,9 @@ struct Token {
 // The same for x, dt, z, B, C and out of one type X, in 16-byte aligned rows.
 // Everything of the next token, and the next sequence's states, is asked for
 // before the current one is worked on.  ONE: a single token, one state stored.
-template <int N, int SPL, typename X, bool ONE>
-__global__ void __launch_bounds__(kThreads, SPL == 4 ? (sizeof(X) == 2 ? 7 : 5) : 4) ssm_step_kernel(const SsmParams p, int per_block) {
+// R: blocks that an SM holds at once.
+template <int N, int SPL, typename X, bool ONE, int R>
+__global__ void __launch_bounds__(kThreads, R) ssm_step_kernel(const SsmParams p, int per_block) {
     constexpr int LPC = N / SPL, H = SPL / 2;
     constexpr int CPB = 2 * kThreads / LPC;
     using Tok = Token<X, SPL>;
@@ -323,24 +326,42 @@ __global__ void __launch_bounds__(kThreads, SPL == 4 ? (sizeof(X) == 2 ? 7 : 5) 
     }
 }
 
+// Sequences of a block: the fewest with which the device holds all blocks at once
+// (100 x 3 tokens, 2048 channels, bf16: 10.5 us; in two rounds of fewer, 12.7 us).
+int seqs_of_block(const SsmParams& p, int64_t columns, int resident) {
+    const int64_t held = int64_t{152} * resident;
+    return static_cast<int>(std::min<int64_t>(kMaxSeqs, (columns * p.s.n + held - 1) / held));
+}
+
+template <int N, int SPL, typename X, int R>
+lar_status alike(const SsmParams& p, int64_t columns, cudaStream_t st) {
+    const int per = seqs_of_block(p, columns, R);
+    const dim3 grid(static_cast<unsigned>(columns), (p.s.n + per - 1) / per);
+    return launch_ordered(p.s.T == 1 ? ssm_step_kernel<N, SPL, X, true, R> : ssm_step_kernel<N, SPL, X, false, R>, grid,
+                          kThreads, 0, 1, st, p, per);
+}
+
 template <int N, int SPL>
 lar_status go(const SsmParams& p, cudaStream_t st) {
     constexpr int CPB = 2 * kThreads / (N / SPL);
     const int64_t columns = (p.D + CPB - 1) / CPB;
-    // sequences of a block: as many as leave the device four blocks an SM
-    int per = 1;
-    while (per < kMaxSeqs && columns * ((p.s.n + 2 * per - 1) / (2 * per)) >= 152 * 4) per *= 2;
-    const dim3 grid(static_cast<unsigned>(columns), (p.s.n + per - 1) / per);
     const int dt = p.x_dt;
-    const bool alike = p.dt_dt == dt && p.B_dt == dt && p.C_dt == dt && p.out_dt == dt && (!p.z || p.z_dt == dt);
-    if (!alike || !p.vec || !p.vec_bc) return launch_ordered(ssm_step_any_kernel<N, SPL>, grid, kThreads, 0, 1, st, p, per);
-    using H = unsigned short;
-    const bool one = p.s.T == 1;
-    if (dt == LAR_BF16)
-        return launch_ordered(one ? ssm_step_kernel<N, SPL, H, true> : ssm_step_kernel<N, SPL, H, false>, grid, kThreads,
-                              0, 1, st, p, per);
-    return launch_ordered(one ? ssm_step_kernel<N, SPL, float, true> : ssm_step_kernel<N, SPL, float, false>, grid,
-                          kThreads, 0, 1, st, p, per);
+    if (!p.vec || !p.vec_bc || p.dt_dt != dt || p.B_dt != dt || p.C_dt != dt || p.out_dt != dt || (p.z && p.z_dt != dt)) {
+        const int per = seqs_of_block(p, columns, 4);
+        const dim3 grid(static_cast<unsigned>(columns), (p.s.n + per - 1) / per);
+        return launch_ordered(ssm_step_any_kernel<N, SPL>, grid, kThreads, 0, 1, st, p, per);
+    }
+    if constexpr (SPL == 8) {
+        if (dt == LAR_F32) return alike<N, SPL, float, 4>(p, columns, st);
+        // With the registers of five blocks the code is slower (17 x 4 tokens, 4096
+        // channels: 6.9 us against 6.0), and pays where a block then takes fewer
+        // sequences (64 x 4 tokens: 14.9 us against 16.0).
+        if (seqs_of_block(p, columns, 5) < seqs_of_block(p, columns, 4))
+            return alike<N, SPL, unsigned short, 5>(p, columns, st);
+        return alike<N, SPL, unsigned short, 4>(p, columns, st);
+    } else {
+        return dt == LAR_F32 ? alike<N, SPL, float, 5>(p, columns, st) : alike<N, SPL, unsigned short, 7>(p, columns, st);
+    }
 }
 
 }  // namespace
