@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, R) ssm_step_kernel(const SsmParams p
 }
 
 // Sequences of a block: the fewest with which the device holds all blocks at once
-// (100 x 3 tokens, 2048 channels, bf16: 10.5 us; in two rounds of fewer, 12.7 us).
+// (100 x 3 tokens, 2048 channels, bf16: 10.5 us; in two waves of fewer, 12.7 us).
 int seqs_of_block(const SsmParams& p, int64_t columns, int resident) {
     const int64_t held = int64_t{152} * resident;
     return static_cast<int>(std::min<int64_t>(kMaxSeqs, (columns * p.s.n + held - 1) / held));
