@@ -348,21 +348,20 @@ struct Scan {
 // Where the state decays (falls: no a2 above 0) in one factor.  Over a long part a
 // growing factor may be past fp32 where its product with h is not, with an empty h
 // above all: it is taken in two halves, and half of it is past fp32 only where the
-// product with the least h is, too.
-__device__ __forceinline__ void decay_join(f32x2 (*h)[kH], const f32x2 (*a2)[kH], bool falls, float s0, float s1,
+// product with the least h is, too.  Each channel by its own numbers alone: beside the
+// last channel of an odd count there is a lane whose numbers are whatever shared memory held.
+__device__ __forceinline__ void decay_join(f32x2 (*h)[kH], const f32x2 (*a2)[kH], const bool* falls, float s0, float s1,
                                            const f32x2 (*e)[kH]) {
-    if (falls && s0 >= 0.f && s1 >= 0.f) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const f32x2 ss = j ? pack2(s1, s1) : pack2(s0, s0);
-#pragma unroll
-            for (int i = 0; i < kH; ++i) h[j][i] = fma2(ex2_2(mul2(ss, a2[j][i])), h[j][i], e[j][i]);
-        }
-        return;
-    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const float half = 0.5f * (j ? s1 : s0);
+        const float s = j ? s1 : s0;
+        if (falls[j] && s >= 0.f) {
+            const f32x2 ss = pack2(s, s);
+#pragma unroll
+            for (int i = 0; i < kH; ++i) h[j][i] = fma2(ex2_2(mul2(ss, a2[j][i])), h[j][i], e[j][i]);
+            continue;
+        }
+        const float half = 0.5f * s;
 #pragma unroll
         for (int i = 0; i < kH; ++i) {
             float v[2], f[2];
@@ -479,12 +478,12 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
 #pragma unroll
             for (int i = 0; i < 2 * kH; ++i) h[i / kH][i % kH] = 0ull;
         };
-        bool falls = true;
+        bool falls[2] = {true, true};
 #pragma unroll
         for (int i = 0; i < 2 * kH; ++i) {
             float a, b;
             unpack2(sc.a2[i / kH][i % kH], a, b);
-            falls = falls && a <= 0.f && b <= 0.f;
+            falls[i / kH] = falls[i / kH] && a <= 0.f && b <= 0.f;
         }
         clear(sc.h);
         sc.ssum = 0.f;

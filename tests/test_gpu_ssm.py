@@ -378,3 +378,35 @@ def test_far_offsets(cuda_device):
     ref, bound, hs, Es = ref_of(a, opt, 0, R.f64(seed))
     R.assert_within(out[0], ref, bound)
     R.assert_within(pool[P - 2], hs[-1], Es[-1])
+
+
+def dirty_shared(dev, value):
+    """Leaves `value` in the shared memory of every SM, by a call that stages it there."""
+    x = torch.full((32768, 512), value, device=dev)
+    lar.conv_prefill(x, torch.ones(512, 4, device=dev), torch.zeros(1, 3, 512, device=dev),
+                     torch.tensor([0, x.shape[0]], device=dev), torch.tensor([-1], device=dev))
+
+
+@pytest.mark.parametrize("lens,D,N,G", [([1500], 37, 16, 1), ([20] * 40 + [0, 600, 1], 809, 16, 1),
+                                        ([300, 5, 200], 98, 64, 2)])
+@pytest.mark.parametrize("soft", [True, False])
+def test_prefill_parts_repeat(lens, D, N, G, soft, cuda_device):
+    """Odd channel counts of rows that 16-byte loads do not fit, in spans that are split:
+    the lane beside the last channel has none of its own, and what shared memory held
+    before the call decides no bit of the result; nor does the layout."""
+    dev, n = cuda_device, len(lens)
+    off = torch.tensor(np.cumsum([0] + lens), device=dev)
+    g, a, _ = inputs(sum(lens) + D, (int(off[-1]),), D, N, G, F32, False)
+    if soft:
+        a["dt"] = a["dt"] - 2
+    a = on(a, dev)
+    seed = torch.randn(n, D, N, generator=g).to(dev)
+    wide = {k: torch.zeros(*a[k].shape[:-1], 2 * D, device=dev)[..., ::2].copy_(a[k]) for k in ("x", "dt")}
+    res = []
+    for value, b in ((1.0, a), (-1e30, a), (float("nan"), a), (1.0, {**a, **wide})):
+        pool = seed.clone()
+        dirty_shared(dev, value)
+        out = lar.ssm_prefill(**b, pool=pool, cu_seqlens=off, read_idx=torch.arange(n, device=dev), dt_softplus=soft)
+        res.append((out, pool))
+    for out, pool in res[1:]:
+        assert torch.equal(out, res[0][0]) and torch.equal(pool, res[0][1])
