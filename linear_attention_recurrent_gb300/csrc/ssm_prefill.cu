@@ -345,23 +345,15 @@ struct Scan {
 };
 
 // h <- 2^(s a2) h + e for both channels of a lane, s0 and s1 the sums of their steps.
-// Where the state decays (falls: no a2 above 0) in one factor.  Over a long part a
-// growing factor may be past fp32 where its product with h is not, with an empty h
-// above all: it is taken in two halves, and half of it is past fp32 only where the
-// product with the least h is, too.  Each channel by its own numbers alone: beside the
-// last channel of an odd count there is a lane whose numbers are whatever shared memory held.
-__device__ __forceinline__ void decay_join(f32x2 (*h)[kH], const f32x2 (*a2)[kH], const bool* falls, float s0, float s1,
+// Over a long part the factor may be past fp32 on either side where its product with h
+// is not: a large h falls far, a small one grows, an empty one stays.  It is taken in two
+// halves.  Each channel by its own numbers alone: beside the last channel of an odd
+// count there is a lane whose numbers are whatever shared memory held.
+__device__ __forceinline__ void decay_join(f32x2 (*h)[kH], const f32x2 (*a2)[kH], float s0, float s1,
                                            const f32x2 (*e)[kH]) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const float s = j ? s1 : s0;
-        if (falls[j] && s >= 0.f) {
-            const f32x2 ss = pack2(s, s);
-#pragma unroll
-            for (int i = 0; i < kH; ++i) h[j][i] = fma2(ex2_2(mul2(ss, a2[j][i])), h[j][i], e[j][i]);
-            continue;
-        }
-        const float half = 0.5f * s;
+        const float half = 0.5f * (j ? s1 : s0);
 #pragma unroll
         for (int i = 0; i < kH; ++i) {
             float v[2], f[2];
@@ -478,13 +470,6 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
 #pragma unroll
             for (int i = 0; i < 2 * kH; ++i) h[i / kH][i % kH] = 0ull;
         };
-        bool falls[2] = {true, true};
-#pragma unroll
-        for (int i = 0; i < 2 * kH; ++i) {
-            float a, b;
-            unpack2(sc.a2[i / kH][i % kH], a, b);
-            falls[i / kH] = falls[i / kH] && a <= 0.f && b <= 0.f;
-        }
         clear(sc.h);
         sc.ssum = 0.f;
         if (hi < len) sc.template run<false, tokens_of(CLUSTER)>(begin + lo, begin + hi);   // somebody comes after this warp
@@ -502,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
             for (int i = 0; i < kSPL / 2; ++i) q[i] = left(v).h[i][lane];
             take(q, &e[0][0]);
             const float s0 = left(v).s[lane], s1 = left(v).s[lane ^ 1];
-            decay_join(pre, sc.a2, falls, s0, s1, e);
+            decay_join(pre, sc.a2, s0, s1, e);
             pre_s += s0;
             pre_t += s1;
         }
@@ -514,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
                     own[i / kH][i % kH] = sc.h[i / kH][i % kH];
                     sc.h[i / kH][i % kH] = pre[i / kH][i % kH];
                 }
-                decay_join(sc.h, sc.a2, falls, sc.ssum, __shfl_xor_sync(0xffffffffu, sc.ssum, 1), own);
+                decay_join(sc.h, sc.a2, sc.ssum, __shfl_xor_sync(0xffffffffu, sc.ssum, 1), own);
                 sc.ssum += pre_s;
                 put(whole);
             }
@@ -532,10 +517,10 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
                     const float s0 = ld_peer_f32(&whole.s[lane], r);
                     const float s1 = ld_peer_f32(&whole.s[lane ^ 1], r);
                     take(q, &e[0][0]);
-                    decay_join(sc.h, sc.a2, falls, s0, s1, e);
+                    decay_join(sc.h, sc.a2, s0, s1, e);
                 }
             }
-            decay_join(sc.h, sc.a2, falls, pre_s, pre_t, pre);
+            decay_join(sc.h, sc.a2, pre_s, pre_t, pre);
         }
         // all have read their peers, and the seed before any end state is stored
         if (CLUSTER) cluster_sync();

@@ -410,3 +410,34 @@ def test_prefill_parts_repeat(lens, D, N, G, soft, cuda_device):
         res.append((out, pool))
     for out, pool in res[1:]:
         assert torch.equal(out, res[0][0]) and torch.equal(pool, res[0][1])
+
+
+def decayed(a, off, i, seed):
+    """The reference over span i with what the sums of steps add to its bounds.  A sum of L steps,
+    all of one sign, is off by at most L 2^-24 of itself, and its product with A in up to
+    64 joins by 2^-24 each: so much of the exponent, times |h|, and |C| |h| for the outputs."""
+    lo, hi = off[i], off[i + 1]
+    ref, bound, hs, Es = ref_of(a, {}, slice(lo, hi), seed)
+    v = np.abs(R.f64(a["A"])[None] * np.cumsum(np.abs(R.f64(a["dt"])[lo:hi]), 0)[..., None])
+    more = (hi - lo + 64) * 2.0**-24 * v * np.abs(hs)
+    return ref, bound + np.einsum("tn,tdn->td", np.abs(R.f64(a["C"])[lo:hi, 0]), more), hs, Es + more
+
+
+@pytest.mark.parametrize("lens,i,D,rate", [([20] * 40 + [0, 600, 1], 41, 808, 0.35), ([1500], 0, 64, 0.7)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_prefill_large_state_falls(lens, i, D, rate, sign, cuda_device):
+    """A state of 1e30 that falls by 2^-130 and more over a part of a split span: the
+    factor is below what fp32 holds, its product with the state is not."""
+    dev, N, n = cuda_device, 16, len(lens)
+    off = np.cumsum([0] + lens)
+    g, a, _ = inputs(6, (int(off[-1]),), D, N, 1, F32, False)
+    a["A"] = -sign * rate * np.log(2) * (1 + 0.1 * torch.rand(D, N, generator=g))
+    a["dt"], a["x"][:] = sign * (0.9 + 0.2 * torch.rand(int(off[-1]), D, generator=g)), 0
+    pool = 1e30 * (1 + torch.rand(n, D, N, generator=g))
+    gp = pool.to(dev)
+    out = lar.ssm_prefill(**on(a, dev), pool=gp, cu_seqlens=torch.tensor(off, device=dev),
+                          read_idx=torch.arange(n, device=dev))
+    ref, bound, hs, Es = decayed(a, off, i, R.f64(pool)[i])
+    assert (np.abs(hs[440 if n > 1 else 200]) > 1e-30).all()
+    R.assert_within(out[off[i]:off[i + 1]], ref, bound, "out")
+    R.assert_within(gp[i], hs[-1], Es[-1], "state")
