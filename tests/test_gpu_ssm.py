@@ -441,3 +441,26 @@ def test_prefill_large_state_falls(lens, i, D, rate, sign, cuda_device):
     assert (np.abs(hs[440 if n > 1 else 200]) > 1e-30).all()
     R.assert_within(out[off[i]:off[i + 1]], ref, bound, "out")
     R.assert_within(gp[i], hs[-1], Es[-1], "state")
+
+
+def test_prefill_least_states_grow(cuda_device):
+    """Subnormal states that grow by 2^265 over the first three of a span's four parts (152
+    tokens each, the last one shorter): the last part starts from the product.  Within the
+    first part a token's own product with such a state is rounded to few bits, which
+    the bounds do not cover: its outputs are not looked at."""
+    dev, D, N, lens, i = cuda_device, 808, 16, [20] * 40 + [0, 600, 1], 41
+    off = np.cumsum([0] + lens)
+    n, last = len(lens), 456
+    g, a, _ = inputs(7, (int(off[-1]),), D, N, 1, F32, False)
+    a["A"] = 265 / last * np.log(2) * (1 - 0.02 * torch.rand(D, N, generator=g))
+    a["dt"][:], a["x"][:] = 1, 0
+    a["dt"][off[i] + last:] = 0
+    pool = torch.randint(1, 9, (n, D, N), generator=g) * 2.0**-149
+    pool[:i] = 0
+    gp = pool.to(dev)
+    out = lar.ssm_prefill(**on(a, dev), pool=gp, cu_seqlens=torch.tensor(off, device=dev),
+                          read_idx=torch.arange(n, device=dev))
+    ref, bound, hs, Es = decayed(a, off, i, R.f64(pool)[i])
+    assert np.isfinite(hs[-1].astype(np.float32)).all() and (hs[-1] > 2.0**107).all()
+    R.assert_within(out[off[i] + last:off[i + 1]], ref[last:], bound[last:], "out")
+    R.assert_within(gp[i], hs[-1], Es[-1], "state")
