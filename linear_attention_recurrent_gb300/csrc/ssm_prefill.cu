@@ -522,7 +522,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of(CLUSTER)) ssm_prefill_kern
                     decay_join(sc.h, sc.a2, s0, s1, e);
                 }
             }
-            decay_join(sc.h, sc.a2, pre_s, pre_t, pre);
+            // the first warp has none before it: no steps times a rate of -infinity would be NaN
+            if (warp > 0) decay_join(sc.h, sc.a2, pre_s, pre_t, pre);
         }
         // all have read their peers, and the seed before any end state is stored
         if (CLUSTER) cluster_sync();

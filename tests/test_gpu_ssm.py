@@ -464,3 +464,24 @@ def test_prefill_least_states_grow(cuda_device):
     assert np.isfinite(hs[-1].astype(np.float32)).all() and (hs[-1] > 2.0**107).all()
     R.assert_within(out[off[i] + last:off[i + 1]], ref[last:], bound[last:], "out")
     R.assert_within(gp[i], hs[-1], Es[-1], "state")
+
+
+@pytest.mark.parametrize("lens,i,D", [([20] * 40 + [0, 600, 1], 41, 808), ([1500], 0, 64)])
+def test_prefill_infinite_rates(lens, i, D, cuda_device):
+    """A rate of -infinity forgets at every step, in spans that are split too."""
+    dev, N, n = cuda_device, 16, len(lens)
+    off = np.cumsum([0] + lens)
+    g, a, _ = inputs(8, (int(off[-1]),), D, N, 1, F32, False)
+    a["dt"] = 0.5 + a["dt"]
+    a["A"][:, 3] = -1e4                                 # e^-5000: zero in 64 bits too
+    pool = torch.randn(n, D, N, generator=g)
+    idx = dict(cu_seqlens=torch.tensor(off, device=dev), read_idx=torch.arange(n, device=dev))
+    ref, bound, hs, Es = decayed(a, off, i, R.f64(pool)[i])
+    A = a["A"].clone()
+    A[:, 3] = float("-inf")
+    b, gp = on(dict(a, A=A), dev), pool.to(dev)
+    out = lar.ssm_prefill(**b, pool=gp, **idx)
+    # what falls at e^-5000 a step has no part in the bound but that of its last input
+    R.assert_within(gp[i][:, 4:], hs[-1][:, 4:], Es[-1][:, 4:], "state")
+    np.testing.assert_array_less(np.abs(R.f64(gp[i])[:, 3] - hs[-1][:, 3]), 8 * R.U * np.abs(hs[-1][:, 3]) + 1e-37)
+    assert bool(torch.isfinite(out).all())
