@@ -347,9 +347,9 @@ struct Scan {
 // h <- 2^(s a2) h + e for both channels of a lane, s0 and s1 the sums of their steps.
 // Over a long part the factor may be past fp32 on either side where its product with h
 // is not: a large h falls far, a small one grows, an empty one stays.  So it is taken in
-// four equal factors (a quarter of s is exact), each within [0, 2^127]: 2^-149, the least
-// h, times 2^508 is past fp32 for certain, and a quarter of the exponent at which a factor
-// is flushed to 0 takes any h to 0.  Each channel by its own numbers alone: beside the last
+// four equal factors (a quarter of s is exact), each held within [2^-125, 2^127]: 2^-500
+// takes any finite h to 0 and 2^508 the least one, 2^-149, past fp32, and neither makes a
+// NaN of an infinite or an empty h.  Each channel by its own numbers alone: beside the last
 // channel of an odd count there is a lane whose numbers are whatever shared memory held.
 __device__ __forceinline__ void decay_join(f32x2 (*h)[kH], const f32x2 (*a2)[kH], float s0, float s1,
                                            const f32x2 (*e)[kH]) {
@@ -361,7 +361,7 @@ __device__ __forceinline__ void decay_join(f32x2 (*h)[kH], const f32x2 (*a2)[kH]
             float v[2], f[2];
             unpack2(mul2(pack2(quarter, quarter), a2[j][i]), v[0], v[1]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) f[k] = v[k] > 127.f ? 0x1p127f : exp2_f(v[k]);   // a NaN stays one
+            for (int k = 0; k < 2; ++k) f[k] = exp2_f(fmaxf(fminf(v[k], 127.f), -125.f));   // of a NaN: e is one, too
             const f32x2 ff = pack2(f[0], f[1]);
             h[j][i] = fma2(mul2(mul2(mul2(h[j][i], ff), ff), ff), ff, e[j][i]);
         }

@@ -485,3 +485,30 @@ def test_prefill_infinite_rates(lens, i, D, cuda_device):
     R.assert_within(gp[i][:, 4:], hs[-1][:, 4:], Es[-1][:, 4:], "state")
     np.testing.assert_array_less(np.abs(R.f64(gp[i])[:, 3] - hs[-1][:, 3]), 8 * R.U * np.abs(hs[-1][:, 3]) + 1e-37)
     assert bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("lens,i,D", [([20] * 40 + [0, 600, 1], 41, 808), ([1500], 0, 64)])
+def test_prefill_infinite_states(lens, i, D, cuda_device):
+    """An infinite state stays one while it falls, in spans that are split as token by token."""
+    dev, N, n = cuda_device, 16, len(lens)
+    off = np.cumsum([0] + lens)
+    g, a, _ = inputs(8, (int(off[-1]),), D, N, 1, F32, False)
+    a["dt"] = 0.5 + a["dt"]
+    pool = torch.randn(n, D, N, generator=g)
+    idx = dict(cu_seqlens=torch.tensor(off, device=dev), read_idx=torch.arange(n, device=dev))
+    pool[:, ::2, 5] = float("inf")
+    a["A"][:, 5] = -1.0                                 # falls by 2^-126 and more before the last part
+    res = []
+    for one in (False, True):                           # in a call that splits it, then token by token
+        gp, b = pool.to(dev), on(a, dev)
+        if one:
+            step = lambda t: dict({k: b[k][t:t + 1] for k in ("x", "dt", "B", "C")}, A=b["A"])  # noqa: E731
+            out = torch.cat([lar.ssm_decode(**step(t), pool=gp, read_idx=torch.tensor([i], device=dev))
+                             for t in range(off[i], off[i + 1])])
+        else:
+            out = lar.ssm_prefill(**b, pool=gp, **idx)[off[i]:off[i + 1]]
+        assert bool((gp[i, ::2, 5] == float("inf")).all())
+        assert bool(torch.isinf(out[:, ::2]).all()) and bool(torch.isfinite(out[:, 1::2]).all())
+        assert bool(torch.isfinite(gp[i, 1::2]).all())
+        res.append(out[:, ::2])
+    assert torch.equal(*res)
