@@ -29,12 +29,18 @@ __device__ __forceinline__ void load_row(const void* base, int64_t off, int64_t 
     for (int i = 0; i < SPL; i += 4) ld_in4(base, off + i * st, st, dt, f + i);
 }
 
-// A log2(e): the decay of a step s is 2^(s a2).
+// A log2(e): the decay of a step s is 2^(s a2).  A finite rate stays finite (the least number
+// is a usual one for "forget"): a step of 0 times it is 0, and any step of 1e-36 or more
+// forgets with the largest a2 as with 1.44 times it.
 template <int SPL>
 __device__ __forceinline__ void load_a2(const SsmParams& p, int d, int n0, float* a2) {
     load_row<SPL>(p.A, d * p.as[0] + n0 * p.as[1], p.as[1], LAR_F32, a2);
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) a2[i] *= kLog2e;
+    for (int i = 0; i < SPL; ++i) {
+        const float a = a2[i], most = 3.402823466e38f;
+        a2[i] = a * kLog2e;
+        if (fabsf(a) <= most) a2[i] = fminf(fmaxf(a2[i], -most), most);
+    }
 }
 
 // 16 bytes of channel d's states from n0 on, as they lie in the pool; zero

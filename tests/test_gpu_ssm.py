@@ -512,3 +512,31 @@ def test_prefill_infinite_states(lens, i, D, cuda_device):
         assert bool(torch.isfinite(gp[i, 1::2]).all())
         res.append(out[:, ::2])
     assert torch.equal(*res)
+
+
+def test_lowest_rate(cuda_device):
+    """The least fp32 number as a rate: a step of 0 keeps the state, any other forgets it."""
+    dev, D, N, L = cuda_device, 40, 16, 700
+    g, a, _ = inputs(12, (L,), D, N, 1, F32, False)
+    a["A"][:, ::4] = torch.finfo(F32).min
+    a["dt"] = 0.1 + a["dt"]
+    a["dt"][torch.rand(L, D, generator=g) < 0.9] = 0
+    a["dt"][:100] = 0                                   # the seed stands for a while
+    pool = torch.randn(2, D, N, generator=g)
+    ref = dict(a, A=a["A"].clamp_min(-1e4))             # e^-1000: zero as well
+    out, bound, hs, Es = ref_of(ref, {}, slice(0, L), R.f64(pool)[0])
+    kept = np.where(R.f64(a["A"]) < -1e4, 0, R.f64(a["A"]))
+    more = (L + 64) * 2.0**-24 * np.abs(kept * np.cumsum(R.f64(a["dt"]), 0)[..., None] * hs)
+    gp = pool.to(dev)
+    idx = lambda v: torch.tensor([v], device=dev)  # noqa: E731
+    one = lar.ssm_prefill(**on(a, dev), pool=gp, cu_seqlens=torch.tensor([0, L], device=dev), read_idx=idx(0),
+                          write_idx=idx(1))
+    R.assert_within(one, out, bound + np.einsum("tn,tdn->td", np.abs(R.f64(a["C"])[:, 0]), more), "out")
+    R.assert_within(gp[1], hs[-1], Es[-1] + more[-1], "state")
+    for lay in (lambda v: v, lambda v: torch.stack([v, v], -1)[..., 0]):   # aligned rows, and any layout
+        gp, outs = pool.to(dev), []
+        for t in range(90, 110):                        # the state before token 90 is the seed still
+            b = on({k: v[t:t + 1] for k, v in a.items() if k != "A"}, dev)
+            outs.append(lar.ssm_decode(lay(b["x"]), b["dt"], a["A"].to(dev), b["B"], b["C"], gp, idx(0)))
+        R.assert_within(torch.cat(outs), out[90:110], bound[90:110], "steps")
+        R.assert_within(gp[0], hs[109], Es[109], "state after steps")
