@@ -202,9 +202,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
         } else {
             const float pt = ld_in(p.p, b * p.ps[0] + lane * p.ps[1] + tok * p.ps[2], p.p_dt);
             const float qt = p.q ? ld_in(p.q, b * p.qs[0] + lane * p.qs[1] + tok * p.qs[2], p.q_dt) : 1.f;
-            // u q < p for the product itself: where it rounds to p, its error decides
+            // u q < p for the product itself: where it rounds to p, its error decides, which
+            // is an fp32 number once numbers near the least ones are scaled up
             const float u = __ldg(p.ua + b * p.ua_s[0] + lane * p.ua_s[1]), uq = u * qt;
-            good = uq < pt || (uq == pt && fmaf(u, qt, -uq) < 0.f);
+            const float up = pt < 0x1p-60f ? 0x1p60f : 1.f;
+            good = uq < pt || (uq == pt && fmaf(u, qt * up, -pt * up) < 0.f);
         }
     }
     const unsigned bad = ~__ballot_sync(0xffffffffu, good);

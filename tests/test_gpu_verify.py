@@ -195,3 +195,21 @@ def test_distribution(cuda_device):
     share = torch.bincount(out[:, 0].cpu(), minlength=V).double() / B
     want = p0[0].double()
     assert bool(((share - want).abs() < 5 * (want * (1 - want) / B).sqrt()).all()), (share, want)
+
+
+def test_products_below_normal_numbers(cuda_device):
+    """u q that fp32 rounds to p while the product itself is below or above it."""
+    e, V = 2.0 ** -149, 8
+    q_d, u_d, p_d = zip(*[(3 * e, 0.5, 2 * e),                 # 1.5 < 2: stands
+                          (5 * e, 0.5, 2 * e),                 # 2.5 > 2
+                          (4 * e, 0.5, 2 * e),                 # equal: rejected
+                          (7 * e, 0.5, 4 * e),                 # 3.5 < 4
+                          (e, 0.75, e),                        # 0.75 < 1
+                          (e, 0.25, 0.0),                      # 0.25 > 0
+                          (2.0 ** -126 + e, 1 - 2.0 ** -24, 2.0 ** -126 + e),
+                          (2.0 ** -60 + 2.0 ** -83, 2.0 ** -80 + 2.0 ** -103, 2.0 ** -140 + 2.0 ** -149)])
+    B = len(q_d)
+    p, q = torch.full((B, 2, V), 0.125), torch.full((B, 1, V), 0.125)
+    p[:, 0, 3], q[:, 0, 3] = torch.tensor(p_d), torch.tensor(q_d)
+    acc, _ = check(cuda_device, p, q, torch.full((B, 1), 3), torch.tensor(u_d)[:, None], torch.full((B,), 0.4))
+    assert acc[:6].tolist() == [2, 1, 1, 2, 2, 1]
