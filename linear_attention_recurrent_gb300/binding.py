@@ -141,6 +141,23 @@ def _stream(stream, dev=None):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for an output, from the allocator's pool of the stream that the call
+    runs on: what the current stream has freed may still be in use there.  Once it is
+    let go, it is not given out again before the current stream, whose work reads it
+    in all likelihood, has come to that point."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        # a raw handle; those up to 2 name the default streams
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 2 else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def _check(fn, status):
     if status != 0:
         raise LarError(fn, status, load().lar_status_string(status).decode())
@@ -174,7 +191,7 @@ def _delta(name, q, k, v, g, beta, pool, read_idx, write_idx, out, inter, A_log,
            flags, dev_err, out_dtype, stream):
     lib = load()
     if out is None:
-        out = torch.empty(v.shape, dtype=out_dtype or v.dtype, device=v.device)
+        out = _empty(v.shape, out_dtype or v.dtype, v.device, stream)
     ts = (q, k, v, g, beta, A_log, dt_bias, pool, read_idx, write_idx, out, inter)
     dev = _device_of(ts, dev_err, stream)
     ds = [describe(t) for t in ts]
@@ -209,7 +226,7 @@ def _tokens(name, q, k, v, g, beta, pool, state_idx, read_idx, num_accepted, out
             scale, flags, dev_err, out_dtype, stream):
     lib = load()
     if out is None:
-        out = torch.empty(v.shape, dtype=out_dtype or v.dtype, device=v.device)
+        out = _empty(v.shape, out_dtype or v.dtype, v.device, stream)
     ts = (q, k, v, g, beta, A_log, dt_bias, pool, read_idx, num_accepted, state_idx, out)
     dev = _device_of(ts, dev_err, stream)
     ds = [describe(t) for t in ts]
@@ -225,7 +242,7 @@ def la_decode(q, k, v, decay, pool, read_idx, write_idx=None, *, out=None, inter
     """Lightning-Attention decode.  Updates `pool` in place; returns `out`."""
     lib = load()
     if out is None:
-        out = torch.empty(v.shape, dtype=out_dtype or v.dtype, device=v.device)
+        out = _empty(v.shape, out_dtype or v.dtype, v.device, stream)
     ts = (q, k, v, decay, pool, read_idx, write_idx, out, inter)
     dev = _device_of(ts, dev_err, stream)
     ds = [describe(t) for t in ts]
@@ -296,7 +313,7 @@ def _varlen(name, q, k, v, gates, pool, cu_seqlens, read_idx, write_idx, out, in
             out_dtype, stream):
     lib = load()
     if out is None:
-        out = torch.empty(v.shape, dtype=out_dtype or v.dtype, device=v.device)
+        out = _empty(v.shape, out_dtype or v.dtype, v.device, stream)
     tail_t = () if inter is _NO_CACHE else (inter,)
     ts = (q, k, v) + tuple(gates) + (pool, cu_seqlens, read_idx, write_idx, out) + tail_t
     dev = _device_of(ts, dev_err, stream)
@@ -329,7 +346,7 @@ def _layer(form, kind, tensors, flags, dev_err, out_dtype, stream):
     name = f"{form}_{kind}"
     if tensors["out"] is None:
         x = tensors["x"]
-        tensors["out"] = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        tensors["out"] = _empty(x.shape, out_dtype or x.dtype, x.device, stream)
     ts = [tensors[n] for n in _LAYER[form] + _SLOTS[kind] + ("out",)]
     dev = _device_of(ts, dev_err, stream)
     ds = [describe(t) for t in ts]
@@ -405,9 +422,9 @@ def spec_verify(draft_tokens, target_probs, u_accept, u_sample, *, draft_probs=N
     draft_probs None: the drafts were their model's choices (probability 1)."""
     lib = load()
     if num_accepted is None:
-        num_accepted = torch.empty(target_probs.shape[0], dtype=torch.int32, device=target_probs.device)
+        num_accepted = _empty(target_probs.shape[:1], torch.int32, target_probs.device, stream)
     if tokens is None:
-        tokens = torch.empty(target_probs.shape[:2], dtype=draft_tokens.dtype, device=target_probs.device)
+        tokens = _empty(target_probs.shape[:2], draft_tokens.dtype, target_probs.device, stream)
     ts = (draft_tokens, draft_probs, target_probs, u_accept, u_sample, num_draft, num_accepted, tokens)
     dev = _device_of(ts, dev_err, stream)
     ds = [describe(t) for t in ts]

@@ -157,3 +157,69 @@ def test_calls_from_several_host_threads(cuda_device):
         steps(pool_s, idx, st)
     torch.cuda.synchronize()
     assert torch.equal(pool_t, pool_s)
+
+
+def _stream_of(t):
+    """The stream whose pool of the caching allocator t's memory is from."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not of the caching allocator")
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_are_the_calls_streams(handle, cuda_device):
+    """An output that a call allocates comes from the pool of the stream that the call runs
+    on: memory that the current stream has freed may still be in use there."""
+    dev = cuda_device
+    side = torch.cuda.Stream(device=dev)
+    st = side.cuda_stream if handle else side
+    r = lambda *s: torch.rand(s, device=dev)  # noqa: E731
+    idx, off = torch.arange(2, device=dev), torch.tensor([0, 1, 2], device=dev)
+    qkv = (r(2, 1, 16), r(2, 1, 16), r(2, 1, 16))
+    qkv128 = (r(2, 1, 128), r(2, 1, 128), r(2, 1, 128))
+    gate, kgate, beta = -r(2, 1), -r(2, 1, 16), r(2, 1)
+    pool, pool128 = r(2, 1, 16, 16), r(2, 1, 128, 128)
+    rows = idx[:, None]
+    x, w, cpool = r(2, 8), r(8, 4), r(2, 3, 8)
+    ssm = (r(2, 8), r(2, 8), -r(8, 16), r(2, 1, 16), r(2, 1, 16), r(2, 8, 16))
+    decay, probs, ua, us = r(1), torch.full((2, 2, 8), 0.125, device=dev), r(2, 1), r(2)
+    torch.cuda.synchronize()
+    outs = [lar.gdn_decode(*qkv, gate, beta, pool, idx, stream=st),
+            lar.kda_decode(*qkv, kgate, beta, pool, idx, stream=st),
+            lar.gdn_decode_tokens(*[t[:, None] for t in qkv], gate[:, None], beta[:, None], pool, rows, read_idx=idx,
+                                  stream=st),
+            lar.la_decode(*qkv, decay, pool, idx, stream=st),
+            lar.gdn_decode_varlen(*qkv, gate, beta, pool, off, idx, stream=st),
+            lar.gdn_prefill(*qkv128, gate, beta, pool128, off, idx, stream=st),
+            lar.conv_decode(x, w, cpool, idx, stream=st),
+            lar.conv_decode_tokens(x, w, cpool, rows, read_idx=idx, stream=st),
+            lar.conv_prefill(x, w, cpool, off, idx, stream=st),
+            lar.ssm_decode(*ssm, idx, stream=st),
+            lar.ssm_decode_tokens(*ssm, rows, read_idx=idx, stream=st),
+            lar.ssm_prefill(*ssm, off, idx, stream=st),
+            *lar.spec_verify(idx[:, None], probs, ua, us, stream=st)]
+    torch.cuda.synchronize()
+    assert [_stream_of(t) for t in outs] == [side.cuda_stream] * len(outs)
+    assert _stream_of(lar.conv_decode(x, w, cpool, idx)) == torch.cuda.current_stream(dev).cuda_stream
+
+
+def test_outputs_wait_for_the_current_stream(cuda_device):
+    """An output of a call on another stream, read by the current one and let go, is not
+    handed out again on that other stream while the reader is still to come."""
+    dev = cuda_device
+    side = torch.cuda.Stream(device=dev)
+    x, w, pool = torch.rand(2, 1 << 20, device=dev), torch.rand(1 << 20, 4, device=dev), torch.zeros(2, 3, 1 << 20, device=dev)
+    idx = torch.arange(2, device=dev)
+    torch.cuda.synchronize()
+    want = lar.conv_decode(x, w, pool.clone(), idx)
+    torch.cuda.synchronize()
+    out = lar.conv_decode(x, w, pool, idx, stream=side)
+    torch.cuda.current_stream(dev).wait_stream(side)
+    torch.cuda._sleep(100_000_000)                     # some 50 ms
+    seen = out.clone()
+    del out
+    with torch.cuda.stream(side):
+        other = torch.zeros(2, 1 << 20, device=dev)
+    torch.cuda.synchronize()
+    assert torch.equal(seen, want) and bool((other == 0).all())
