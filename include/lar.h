@@ -397,7 +397,8 @@ lar_status conv_prefill(const lar_tensor* x, const lar_tensor* weight, const lar
  *   x, dt, z, out   [B, T, Dch] (rank 2 for T = 1), T from 1 to 16; ssm_prefill:
  *            [Ntok, Dch], Ntok to 2^30.  fp32 or bf16, any strides (out: no two elements at one
  *            address); z may be NULL.
- *   A        fp32 [Dch, N], any strides (usually negative); N 16, 32, 64 or 128.
+ *   A        fp32 [Dch, N], any strides (usually negative, -infinity included: a step
+ *            above 0 then forgets); N 16, 32, 64 or 128.
  *   B, C     [B, T, G, N] (rank 3 [B, G, N] for T = 1; packed [Ntok, G, N]), fp32
  *            or bf16, any strides.
  *   D        fp32 [Dch] or NULL.
@@ -410,7 +411,10 @@ lar_status conv_prefill(const lar_tensor* x, const lar_tensor* weight, const lar
  *            (LAR_ERR_SHAPE; a block is at least 4 warps of 64 / (N / 8) channels).
  * Spans that are long beside the others, or few, are computed in parts that are joined
  * (equal up to rounding); how depends on the sizes and span lengths alone, so a call
- * repeated gives the same bits.
+ * repeated gives the same bits.  In a call of more than 64 spans, unless all their channels
+ * fill less than the device, none is split: a prompt of thousands of tokens is then faster in
+ * a call without the single tokens.  Fast are x, dt, z, B, C and out of one type with 16-byte
+ * aligned rows (Dch / G a multiple of 8); mixed types take 4 to 6 times as long.
  */
 lar_status ssm_decode(const lar_tensor* x, const lar_tensor* dt, const lar_tensor* A, const lar_tensor* B,
                       const lar_tensor* C, const lar_tensor* D, const lar_tensor* z,
@@ -452,8 +456,8 @@ lar_status ssm_prefill(const lar_tensor* x, const lar_tensor* dt, const lar_tens
  *   tokens        out, int32 or int64 [B, T]: the accepted drafts, the next token,
  *                 then -1.
  * Any strides.  A weight that is not a positive finite number counts as 0; sums are
- * held to about 2^-48 of their value (weights up to 2^64), so that the index is the
- * one that exact sums give.
+ * held to about 2^-48 of their value (weights up to 2^64, whole sums of 2^-100 or more), so
+ * that the index is the one that exact sums give.  Acceptance is by the exact product.
  */
 lar_status spec_verify(const lar_tensor* draft_tokens, const lar_tensor* draft_probs,
                        const lar_tensor* target_probs, const lar_tensor* u_accept,

@@ -21,7 +21,10 @@ constexpr int kThreads = 128;   // of a step's blocks
 // 1216 of 64: 94 us, 5.7 TB/s of 6.7 (the tokens' groups ahead: 3; 4 and 5 are slower).
 constexpr int kPre = 64;
 constexpr int kTile = 16;    // tokens of a prefill tile, which blocks share out
-constexpr int kBlocks = 8;   // blocks of the prefill on an SM
+// Blocks of the prefill on an SM.  bf16: all of a call's blocks are held at once.  The fp32
+// ring, 32 KB a block, admits 6, and a call runs in two waves: 16384 x 4096, 161 us for
+// the bytes that bf16 moves in 93.
+constexpr int kBlocks = 8;
 constexpr int kGroup = 4;    // tokens of a group of copies,
 constexpr int kAhead = 3;    // groups asked for ahead of the one in work,
 constexpr int kRing = kGroup * (kAhead + 1);   // and the tokens that the ring holds
@@ -459,8 +462,8 @@ lar_status prefill_vec(const ConvParams& p, dim3 grid, cudaStream_t st) {
 template <int W>
 lar_status prefill(const ConvParams& p, cudaStream_t st) {
     const unsigned per = kPre * (p.vec ? 8 : 1), cb = (p.C + per - 1) / per;
-    // as many blocks as the device holds at once, if disjoint spans have the tiles
-    // (element by element, a thread keeps a third of the registers)
+    // as many blocks as the device holds at once (in bf16: see kBlocks), if disjoint spans
+    // have the tiles (element by element, a thread keeps a third of the registers)
     const int64_t tiles = p.s.ntok / kTile + p.s.n, held = (kBlocks * (p.vec ? 1 : 3) * 152 + cb - 1) / cb;
     const dim3 grid(cb, static_cast<unsigned>(std::min(tiles, std::max<int64_t>(held, 1))));
     if (!p.vec) return launch_ordered(conv_prefill_any_kernel<W>, grid, kPre, 0, 1, st, p);

@@ -16,7 +16,7 @@
 // step from the neighbour that owns it; so B and C, which every lane reads from shared
 // memory for itself, serve two channels (with 16 states of one channel a lane, N = 64
 // and 128 took 1.6 and 2.4 times as long).  64 spans of 256 tokens, 4096 channels:
-// 293 us, 1.2 clocks a (token, channel), at 68 % of the issue slots: an instruction on
+// 303 us, 1.3 clocks a (token, channel), at 68 % of the issue slots: an instruction on
 // pairs (32 of the 116) holds dispatch and its pipe for two cycles, which the counters
 // show as what warps wait for.  An earlier form,
 // in which blocks prepared the steps of all channels in shared memory and met at three
@@ -27,10 +27,18 @@
 // the sum of its steps (the decay over its part is exp(A sum)); the parts before it,
 // joined, are the state that each then starts from, with outputs this time.  That is
 // 1.7 times the work.  Few rows: the same over the blocks of a cluster, through
-// distributed shared memory.  8192 tokens, 2048 channels: 158 us (unsplit 940 us);
-// 24 ragged spans of 16384 tokens, 4096 channels: 400 us (unsplit 720 us).  With the
+// distributed shared memory.  8192 tokens, 2048 channels: 161 us (unsplit 940 us);
+// 24 ragged spans of 16384 tokens, 4096 channels: 380 to 400 us (unsplit 720 us).  With the
 // first part's outputs made at once from the seed, as 1.4 times the work, the loop
-// around both runs cost more than it saved: 167 and 416 us.
+// around both runs cost more than it saved: 167 and 416 us against 158 and 400.
+//
+// What is split is decided from averages.  One long span among many short ones therefore
+// does worse than alone: 8192 tokens x 2048 beside 16 or 60 single tokens, over the four
+// warps of a block, 740 and 620 us; beside 64 or more, where spans are not sorted and
+// none is split, 1.1 to 1.2 ms.
+//
+// Types that differ, and rows that 16-byte loads do not fit, are staged by single elements
+// through registers: 8192 x 2047 bf16 234 us; 8192 x 2048 with dt alone in fp32 590 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -544,15 +552,17 @@ lar_status go(const SsmParams& p, cudaStream_t st) {
     w.columns = p.G * ((p.per_group + G::CW - 1) / G::CW);
     const int64_t rows = static_cast<int64_t>(w.columns) * p.s.n;
     // Clusters where a warp a column leaves the device empty even with every span split
-    // over a block: blocks enough to fill it, with parts of 32 tokens or more, up to the
-    // portable 8 (a span of 8192 x 2048 x 16: 262, 182, 163 us with 2, 4, 8 when chosen; sizes
-    // between, as 7 with 188 us, fit the device worse than the next power of two).
+    // over a block: blocks enough to fill it, up to the portable 8 (a span of 8192 x 2048 x
+    // 16: 262, 182, 163 us with 2, 4, 8 when chosen; sizes between, as 7 with 188 us, fit the
+    // device worse than the next power of two), while the spans have 16 tokens a warp on
+    // average.  Parts have 32 at least: a span of average length then leaves half of the
+    // blocks without tokens, a longer one does not.
     w.ranks = 1;
     while (w.ranks < 8 && rows * kWarps * w.ranks < kFill && p.s.ntok >= int64_t{128} * w.ranks * p.s.n) w.ranks *= 2;
     w.min_part = 32;
     // Long: more than 1.5 times the tokens of a warp if all that the device holds had
     // the same.  Measured at the ragged spans above: 720 us unsplit, 441, 446 and 401
-    // us at 1, 1.25 and 1.5 times, 543 us at twice.
+    // us at 1, 1.25 and 1.5 times, 543 us at twice.  Past kSorted spans none is split.
     const int64_t len = p.s.ntok * w.columns * 3 / (int64_t{2} * kSms * 4 * 3);
     w.long_len = static_cast<int>(std::min<int64_t>(std::max<int64_t>(len, 64), INT32_MAX));
     w.long_max = p.s.n > kSorted ? 0 : static_cast<int>(std::min<int64_t>(p.s.n, p.s.ntok / w.long_len));

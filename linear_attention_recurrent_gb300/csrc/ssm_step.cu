@@ -9,10 +9,11 @@
 // activations.  A lane holds 16 bytes of each of two neighbouring channels; a
 // block takes its channels through several sequences, so that A, as large as one
 // state, is read once for all of them, and asks for the next sequence's states
-// before it works on the current ones.  256 x 4096 x 16, fp32 states: 27 us for 143 MB
-// (5.3 TB/s; one sequence a block with single loads: 139 us); 64 sequences of 4 tokens
-// with a bf16 state stored after each: 15 us for 50 MB, bound by the tokens' way
-// through one another and by issue (about 300 instructions a lane and token).
+// before it works on the current ones.  256 x 4096 x 16, fp32 states: 26 us for 143 MB
+// (5.4 TB/s; one sequence a block with single loads: 139 us); 64 sequences of 4 tokens
+// with a bf16 state stored after each: 15 us for 50 MB, at 275 instructions a warp and
+// token (the scan over spans has 116: there a lane works out one channel's step, here
+// both) in 55 % of the issue slots, the tokens one after another.
 #include <algorithm>
 
 #include "ssm_common.cuh"

@@ -16,8 +16,9 @@
 // error of p - q is itself a float), good to about 2^-48.  Doubles would do as well,
 // but fp64 additions are so slow here that joining the lanes' sums in them took most
 // of the call: 15.6 us for one sequence and 51 us for 64 x 131072 fp32, against 7.0
-// and 18 us so.  Of the 18 us the two rows' bytes are 10; the rest is the way from the
-// drafts to the row (three loads one after another) and from the sums to the token.
+// and 18 us so.  Of the 18 us the rows' bytes are 8.5 (10 if every sequence read both; one
+// whose drafts all stand reads the target's alone); the rest is the way from the drafts
+// to the row (three loads one after another) and from the sums to the token.
 #include "layer_common.cuh"
 
 namespace lar {
