@@ -101,7 +101,8 @@ typedef enum {
     LAR_F32 = 0,
     LAR_BF16 = 1,
     LAR_I32 = 2,
-    LAR_I64 = 3
+    LAR_I64 = 3,
+    LAR_E4M3 = 4   /* 8 bits, 4 of exponent and 3 of mantissa, no infinities: pages of kv_append and attn_decode */
 } lar_dtype;
 
 /* A strided view of device memory.  data points at element [0, ..., 0]. */
@@ -141,6 +142,11 @@ enum {
     LAR_DT_SOFTPLUS = 1u << 5 /* ssm_*: dt <- softplus(dt + dt_bias), in kernel */
 };
 
+/* flags for kv_append */
+enum {
+    LAR_ROPE_INTERLEAVED = 1u << 6 /* rotated pairs are dimensions (2i, 2i + 1), not (i, i + rot / 2) */
+};
+
 /* bits OR-ed into *dev_err */
 enum {
     LAR_DEVERR_READ_SLOT = 1,  /* some read_idx[b] >= P (that entry started from zero) */
@@ -152,8 +158,10 @@ enum {
                                   (sequence, head) skipped the rest of its span and its writeback */
     LAR_DEVERR_DRAFT = 32,     /* spec_verify: some drafted token outside [0, V) (rejected), or some
                                   num_draft[b] outside [0, T - 1] (taken as the nearer end) */
-    LAR_DEVERR_PROBS = 64      /* spec_verify: some row to draw from has no positive finite weight,
-                                  or a sum that fp32 does not hold (its token is -1) */
+    LAR_DEVERR_PROBS = 64,     /* spec_verify: some row to draw from has no positive finite weight,
+                                  or a sum that fp32 does not hold (its token is -1); sample_tokens:
+                                  some row has no logit above -infinity (its token is -1) */
+    LAR_DEVERR_PAGE = 128      /* kv_append, attn_decode: some block_table entry >= P (not written, not seen) */
 };
 
 /*
@@ -464,6 +472,105 @@ lar_status spec_verify(const lar_tensor* draft_tokens, const lar_tensor* draft_p
                        const lar_tensor* u_sample, const lar_tensor* num_draft,
                        const lar_tensor* num_accepted, const lar_tensor* tokens, int32_t* dev_err,
                        void* stream);
+
+/*
+ * A paged cache of keys and values, as the softmax-attention layers between the recurrent
+ * ones keep it.  What the two calls below share:
+ *   k_cache, v_cache   [P, page, H, D]: P pages of `page` tokens (a multiple of 16, to
+ *            1024), H heads (to 1024), D 64, 128 or 256.  bf16 or e4m3, both of one type.
+ *            Dimension stride 1, 16-byte aligned, all other strides multiples of 16
+ *            bytes: views of [P, H, page, D] or of one buffer with both halves will do.
+ *   k_scale, v_scale   fp32 [P, H], any strides, with e4m3 pages; NULL with bf16 ones.  A
+ *            value is its code times the scale of its page and head.
+ *   block_table   int32/int64 [B, M]: place t of sequence b is token t % page of page
+ *            block_table[b][t / page]; M page to 2^30.  A negative entry is no page (not
+ *            written, not seen), one >= P neither, and flagged (LAR_DEVERR_PAGE).
+ *   seq_lens int32/int64 [B]: tokens that sequence b has BEFORE the step: the step's token t
+ *            is at place seq_lens[b] + t, in both calls.  Negative: no sequence here.
+ *            Places from M page on are not written, not seen, and flagged
+ *            (LAR_DEVERR_SEQLEN).
+ *
+ * kv_append: the keys and values of a step's (or a prompt's) tokens enter the cache, the
+ * keys rotated by their place; with q, the queries are rotated into q_out.
+ *   k, v     [B, T, H, D] (rank 3 for T = 1), T from 1 to 16; with cu_seqlens (int32/int64
+ *            [B + 1], ascending) packed spans, [Ntok, H, D], Ntok to 2^30.  fp32 or bf16,
+ *            any strides.
+ *   q, q_out [.., Hq, D] or both NULL; H divides Hq, to 65535; fp32 or bf16, any strides
+ *            (q_out: no two elements at one address).  Rows of tokens outside every span,
+ *            or of no sequence, are left as they were.
+ *   inv_freq fp32 [rot / 2], rot to D: pair i of dimensions (x, y) of a token at place t
+ *            becomes rope_scale (x cos a - y sin a, y cos a + x sin a), a = t inv_freq[i]
+ *            (held to 2^-50 turns, so far places are as exact as near ones).  Dimensions
+ *            from rot on are copied.  NULL: no rotation (then no flags, rope_scale 1).
+ * e4m3: the scale is a power of two, 2^-64 to 2^64: the least with |x| <= 448 scale for the
+ * values that enter a (page, head) in this call, and no less than that of the tokens that
+ * stand before them in the page; if those have a smaller one, their codes are rounded to the
+ * new one (exact unless a code falls below the least normal one).  A code is value / scale
+ * rounded to nearest even.  What is not finite becomes a NaN and has no say in the scale.
+ * Tokens behind the appended ones in a page count as not there.
+ * Aliasing: caches and scales are in and out; they and q_out overlap nothing else of the call
+ * (keys' and values' views may lie between one another).  No page is named by two sequences,
+ * or twice, where tokens are appended; pages in front of those are not touched, and may be
+ * shared.  Offsets that do not ascend are flagged (LAR_DEVERR_SEQLEN); which of the spans
+ * behind them are taken is not defined.
+ */
+lar_status kv_append(const lar_tensor* q, const lar_tensor* k, const lar_tensor* v, const lar_tensor* q_out,
+                     const lar_tensor* k_cache, const lar_tensor* v_cache, const lar_tensor* k_scale,
+                     const lar_tensor* v_scale, const lar_tensor* block_table, const lar_tensor* seq_lens,
+                     const lar_tensor* cu_seqlens, const lar_tensor* inv_freq, float rope_scale, uint32_t flags,
+                     int32_t* dev_err, void* stream);
+
+/*
+ * attn_decode: attention of a step's tokens over the cache, after kv_append of the same
+ * step (the same seq_lens).  Token t of sequence b sees the places 0 .. seq_lens[b] + t, or,
+ * with window > 0, the last `window` of them:
+ *     out = sum_j softmax_j(scale q K_j) V_j,   lse = log sum_j exp(scale q K_j)
+ *   q, out   [B, T, Hq, D] (rank 3 for T = 1), T from 1 to 16, H divides Hq, Hq / H to 256;
+ *            q bf16, out bf16 or fp32, any strides (out: no two elements at one address).
+ *            Query head i reads key/value head i / (Hq / H).
+ *   lse      fp32 [B, T, Hq] or NULL.  A row that sees nothing has out 0 and lse -infinity.
+ *   workspace   fp32, contiguous, 16-byte aligned, of attn_workspace(T, Hq, H, D) elements
+ *            or more; what it holds need not be kept between calls, and calls that may run
+ *            at the same time need one each.
+ * What stands at places that a row does not see has no say in it, whatever it is.  Scores,
+ * maxima and sums are fp32; the weights of the second product are rounded to 11 bits (e4m3
+ * pages: fp16) or 16 bits (bf16 pages).  How the work is split depends on the lengths and
+ * sizes alone, so a repeated call gives the same bits.  Scales are positive and finite.
+ * Two kernels on `stream`.
+ */
+int64_t attn_workspace(int32_t T, int32_t Hq, int32_t H, int32_t D);
+
+lar_status attn_decode(const lar_tensor* q, const lar_tensor* k_cache, const lar_tensor* v_cache,
+                       const lar_tensor* k_scale, const lar_tensor* v_scale, const lar_tensor* block_table,
+                       const lar_tensor* seq_lens, const lar_tensor* out, const lar_tensor* lse,
+                       const lar_tensor* workspace, float scale, int32_t window, int32_t* dev_err, void* stream);
+
+/*
+ * The draw of tokens from logits and given random numbers, one a row:
+ *     w[i] = exp((x[i] - max x) / temperature)
+ * Of the tokens in falling order of x (equal ones by index) the first ones are kept: top_k of
+ * them, those with w >= min_p, and, measured on what top_k leaves, the fewest whose weights
+ * sum to top_p of the whole or more; the shortest of the three, one at least.
+ *     token: the first i (by index) with  sum_{kept j <= i} w[j] > u sum_{kept j} w[j]
+ *     probs[i] = w[i] / sum_{kept j} w[j], or 0: what spec_verify takes as draft_probs and
+ *     target_probs
+ *   logits   fp32 or bf16 [B, T, V] (rank 2 [B, V] for T = 1), T from 1 to 16, V from 1 to
+ *            2^24.  NaN counts as -infinity; if the greatest is +infinity, the tokens that
+ *            have it weigh 1 and the others nothing.
+ *   u        fp32 [B, T] (rank 1 for T = 1), in [0, 1).
+ *   temperature   fp32 [B] or NULL (1); 0 or less (or NaN) means the greatest logit alone.
+ *   top_k    int32/int64 [B] or NULL; 0 or less: all.
+ *   top_p    fp32 [B] or NULL; 1 or more: all; 0 or less (or NaN): the first.
+ *   min_p    fp32 [B] or NULL; 0 or less (or NaN): all.
+ *   tokens   out, int32 or int64 [B, T] (rank 1 for T = 1).
+ *   probs    out, fp32 [B, T, V] (rank 2) or NULL.
+ * Any strides (outputs: no two elements at one address).  Weights are held to 2^-30 of
+ * themselves or 2^-40 of the greatest, sums exactly: the token is the one that exact
+ * arithmetic gives unless u or a threshold is as near as that to a border.
+ */
+lar_status sample_tokens(const lar_tensor* logits, const lar_tensor* u, const lar_tensor* temperature,
+                         const lar_tensor* top_k, const lar_tensor* top_p, const lar_tensor* min_p,
+                         const lar_tensor* tokens, const lar_tensor* probs, int32_t* dev_err, void* stream);
 
 /* Static, human-readable name of a status code. */
 const char* lar_status_string(lar_status status);

@@ -14,18 +14,18 @@ from . import _build
 
 _LIB_PATH = _build.LIB
 
-LAR_F32, LAR_BF16, LAR_I32, LAR_I64 = 0, 1, 2, 3
+LAR_F32, LAR_BF16, LAR_I32, LAR_I64, LAR_E4M3 = 0, 1, 2, 3, 4
 LAR_QK_L2NORM, LAR_GATE_RAW, LAR_BETA_RAW, LAR_STATE_KV = 1, 2, 4, 8
-LAR_SILU, LAR_DT_SOFTPLUS = 16, 32
+LAR_SILU, LAR_DT_SOFTPLUS, LAR_ROPE_INTERLEAVED = 16, 32, 64
 LAR_DEVERR_READ_SLOT, LAR_DEVERR_WRITE_SLOT, LAR_DEVERR_ACCEPTED, LAR_DEVERR_SEQLEN = 1, 2, 4, 8
-LAR_DEVERR_TIMEOUT, LAR_DEVERR_DRAFT, LAR_DEVERR_PROBS = 16, 32, 64
+LAR_DEVERR_TIMEOUT, LAR_DEVERR_DRAFT, LAR_DEVERR_PROBS, LAR_DEVERR_PAGE = 16, 32, 64, 128
 
 STATUS = {0: "LAR_OK", 1: "LAR_ERR_NULL", 2: "LAR_ERR_DTYPE", 3: "LAR_ERR_RANK",
           4: "LAR_ERR_SHAPE", 5: "LAR_ERR_STRIDE", 6: "LAR_ERR_ALIGN", 7: "LAR_ERR_ARG",
           8: "LAR_ERR_ALIAS", 9: "LAR_ERR_LAUNCH"}
 
 _DT = {torch.float32: LAR_F32, torch.bfloat16: LAR_BF16, torch.int32: LAR_I32,
-       torch.int64: LAR_I64}
+       torch.int64: LAR_I64, torch.float8_e4m3fn: LAR_E4M3}
 
 
 class LarTensor(ctypes.Structure):
@@ -86,6 +86,14 @@ def load() -> ctypes.CDLL:
             fn.argtypes = [P] * n + [ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]
         lib.spec_verify.restype = ctypes.c_int
         lib.spec_verify.argtypes = [P] * 8 + [ctypes.c_void_p, ctypes.c_void_p]
+        lib.kv_append.restype = ctypes.c_int
+        lib.kv_append.argtypes = [P] * 12 + [ctypes.c_float, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]
+        lib.attn_workspace.restype = ctypes.c_int64
+        lib.attn_workspace.argtypes = [ctypes.c_int32] * 4
+        lib.attn_decode.restype = ctypes.c_int
+        lib.attn_decode.argtypes = [P] * 10 + [ctypes.c_float, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
+        lib.sample_tokens.restype = ctypes.c_int
+        lib.sample_tokens.argtypes = [P] * 8 + [ctypes.c_void_p, ctypes.c_void_p]
         lib.lar_status_string.restype = ctypes.c_char_p
         lib.lar_status_string.argtypes = [ctypes.c_int]
         _lib = lib
@@ -435,6 +443,88 @@ def spec_verify(draft_tokens, target_probs, u_accept, u_sample, *, draft_probs=N
     return num_accepted, tokens
 
 
+# The tensors of kv_append, attn_decode and sample_tokens, in the library's order.
+_SERVE = {"kv_append": ("q", "k", "v", "q_out", "k_cache", "v_cache", "k_scale", "v_scale", "block_table", "seq_lens",
+                        "cu_seqlens", "inv_freq"),
+          "attn": ("q", "k_cache", "v_cache", "k_scale", "v_scale", "block_table", "seq_lens", "out", "lse",
+                   "workspace"),
+          "sample": ("logits", "u", "temperature", "top_k", "top_p", "min_p", "tokens", "probs")}
+_SERVE_FN = {"kv_append": "kv_append", "attn": "attn_decode", "sample": "sample_tokens"}
+
+
+def _serve(form, tensors, tail, dev_err, stream):
+    """One of the calls above; `tensors` by name, `tail` the numbers behind them."""
+    lib = load()
+    name = _SERVE_FN[form]
+    ts = [tensors.get(n) for n in _SERVE[form]]
+    dev = _device_of(ts, dev_err, stream)
+    ds = [describe(t) for t in ts]
+    err = dev_err.data_ptr() if dev_err is not None else None
+    with torch.cuda.device(dev):
+        st = getattr(lib, name)(*[_ref(d) for d in ds], *tail, err, _stream(stream, dev))
+    _check(name, st)
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, *, k_scale=None, v_scale=None, q=None, q_out=None,
+              cu_seqlens=None, inv_freq=None, interleaved=False, rope_scale=1.0, dev_err=None, stream=None):
+    """Append k, v [B, T, H, D] (or [B, H, D]; packed [Ntok, H, D] with cu_seqlens) to the
+    paged cache k_cache, v_cache [P, page, H, D] at places seq_lens[b] + t, rotated by
+    inv_freq [rot / 2] (None: not at all) with their place.  e4m3 pages take k_scale,
+    v_scale [P, H].  Returns q [.., Hq, D] rotated (None without q)."""
+    if q is not None and q_out is None:
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    _serve("kv_append", dict(q=q, k=k, v=v, q_out=q_out, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale,
+                             v_scale=v_scale, block_table=block_table, seq_lens=seq_lens, cu_seqlens=cu_seqlens,
+                             inv_freq=inv_freq),
+           (float(rope_scale), LAR_ROPE_INTERLEAVED if interleaved else 0), dev_err, stream)
+    return q_out
+
+
+def attn_workspace(T, Hq, H, D):
+    """Elements of the fp32 workspace that attn_decode takes for these sizes."""
+    n = load().attn_workspace(T, Hq, H, D)
+    if n < 0:
+        raise ValueError(f"attn_decode does not take T={T}, Hq={Hq}, H={H}, D={D}")
+    return n
+
+
+def _attn_tensors(tensors, stream):
+    """The workspace, where the caller has none."""
+    q, kc = tensors.get("q"), tensors.get("k_cache")
+    if tensors.get("workspace") is None and q is not None and kc is not None and q.dim() in (3, 4) and kc.dim() == 4:
+        n = load().attn_workspace(1 if q.dim() == 3 else q.shape[1], q.shape[-2], kc.shape[2], q.shape[-1])
+        tensors["workspace"] = _empty((max(n, 1),), torch.float32, q.device, stream)   # the call refuses other sizes
+    return tensors
+
+
+def attn_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None, v_scale=None, scale=None, window=0,
+                out=None, lse=None, workspace=None, dev_err=None, out_dtype=None, stream=None):
+    """Attention of q [B, T, Hq, D] (or [B, Hq, D]), the tokens at places seq_lens[b] + t,
+    over the paged cache that kv_append fills, causal, with window > 0 over the last
+    `window` places alone.  scale: D ** -0.5 by default.  Returns out; lse [B, T, Hq] takes
+    the logarithms of the sums."""
+    if out is None:
+        out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
+    _serve("attn", _attn_tensors(dict(q=q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                                      block_table=block_table, seq_lens=seq_lens, out=out, lse=lse,
+                                      workspace=workspace), stream),
+           (float(q.shape[-1] ** -0.5 if scale is None else scale), int(window)), dev_err, stream)
+    return out
+
+
+def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None,
+                  dev_err=None, stream=None):
+    """Draw a token from each row of logits [B, T, V] (or [B, V]) with the random numbers
+    u [B, T] (or [B]) in [0, 1), after temperature, top_k, top_p and min_p [B]; probs
+    [B, T, V] takes the distribution that it was drawn from, as spec_verify reads it.
+    Returns tokens [B, T] (or [B]), int32 unless given."""
+    if tokens is None:
+        tokens = _empty(logits.shape[:-1], torch.int32, logits.device, stream)
+    _serve("sample", dict(logits=logits, u=u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p,
+                          tokens=tokens, probs=probs), (), dev_err, stream)
+    return tokens
+
+
 class PreparedCall:
     """A decode call whose descriptors are built once, for tight launch loops.
     The tensors it was built from must stay alive and keep their storage.
@@ -444,11 +534,23 @@ class PreparedCall:
     ``prefill=True`` the chunked prefill call (gdn_prefill / la_prefill).
     Forms "conv" and "ssm" select conv_* / ssm_* the same way (``cu_seqlens``
     with ``prefill=True``; flags ``silu`` and ``dt_softplus``), form "verify"
-    spec_verify; a name that the call does not take is refused."""
+    spec_verify; forms "kv_append" (``interleaved``, ``rope_scale``), "attn" (``scale``,
+    ``window``; with a workspace of its own unless one is given) and "sample" select the
+    calls of those names.  A name that the call does not take is refused."""
 
-    def __init__(self, form, *, scale=1.0, qk_l2norm=False, gate_raw=False, beta_raw=False,
-                 state_kv=False, silu=False, dt_softplus=False, dev_err=None, stream=None, prefill=False, **tensors):
+    def __init__(self, form, *, scale=None, qk_l2norm=False, gate_raw=False, beta_raw=False,
+                 state_kv=False, silu=False, dt_softplus=False, window=0, interleaved=False, rope_scale=1.0,
+                 dev_err=None, stream=None, prefill=False, **tensors):
         lib = load()
+        if form != "attn" and window or form != "kv_append" and (interleaved or rope_scale != 1.0):
+            raise ValueError("window is for the form 'attn', interleaved and rope_scale for 'kv_append'")
+        if form in _SERVE:
+            if qk_l2norm or gate_raw or beta_raw or state_kv or silu or dt_softplus or prefill or \
+                    (scale is not None and form != "attn"):
+                raise ValueError(f"form {form!r} takes none of the other forms' flags")
+            self._prepare_serve(lib, form, tensors, scale, window, interleaved, rope_scale, dev_err, stream)
+            return
+        scale = 1.0 if scale is None else scale
         if form in ("conv", "ssm", "verify"):
             if scale != 1.0 or qk_l2norm or gate_raw or beta_raw or state_kv:
                 raise ValueError(f"form {form!r} takes neither a scale nor the decode flags")
@@ -502,6 +604,21 @@ class PreparedCall:
                 raise ValueError("packed spans take cu_seqlens and prefill=True together")
             kind = "prefill" if prefill else ("decode_tokens" if tensors.get("state_idx") is not None else "decode")
             self._name, names, tail = f"{form}_{kind}", _LAYER[form] + _SLOTS[kind] + ("out",), [flags]
+        self._prepare_flat(lib, names, tensors, [ctypes.c_uint32(f) for f in tail], dev_err, stream)
+
+    def _prepare_serve(self, lib, form, tensors, scale, window, interleaved, rope_scale, dev_err, stream):
+        self._name, tail = _SERVE_FN[form], []
+        if form == "attn":
+            tensors = _attn_tensors(dict(tensors), stream)
+            q = tensors.get("q")
+            tail = [ctypes.c_float((q.shape[-1] ** -0.5 if q is not None else 1.0) if scale is None else scale),
+                    ctypes.c_int32(window)]
+        elif form == "kv_append":
+            tail = [ctypes.c_float(rope_scale), ctypes.c_uint32(LAR_ROPE_INTERLEAVED if interleaved else 0)]
+        self._prepare_flat(lib, _SERVE[form], tensors, tail, dev_err, stream)
+
+    def _prepare_flat(self, lib, names, tensors, tail, dev_err, stream):
+        """The library's arguments as C values: tensors, the numbers in `tail`, error word, stream."""
         extra = [n for n, t in tensors.items() if t is not None and n not in names]
         if extra:
             raise ValueError(f"{self._name} takes no {', '.join(sorted(extra))}")
@@ -515,7 +632,7 @@ class PreparedCall:
         err = dev_err.data_ptr() if dev_err is not None else None
         self._descs = [describe(tensors.get(n)) for n in names]
         self._args = [ctypes.c_void_p(ctypes.addressof(d) if d is not None else None) for d in self._descs] + \
-            [ctypes.c_uint32(f) for f in tail] + [ctypes.c_void_p(err), ctypes.c_void_p(_stream(stream, self._dev))]
+            tail + [ctypes.c_void_p(err), ctypes.c_void_p(_stream(stream, self._dev))]
 
     def __call__(self):
         if torch.cuda.current_device() == self._dev.index:
