@@ -500,13 +500,15 @@ lar_status spec_verify(const lar_tensor* draft_tokens, const lar_tensor* draft_p
  *            or of no sequence, are left as they were.
  *   inv_freq fp32 [rot / 2], rot to D: pair i of dimensions (x, y) of a token at place t
  *            becomes rope_scale (x cos a - y sin a, y cos a + x sin a), a = t inv_freq[i]
- *            (held to 2^-50 turns, so far places are as exact as near ones).  Dimensions
+ *            (its whole turns dropped before it is rounded, so far places are as exact as near ones;
+ *            frequencies to 2^60).  Dimensions
  *            from rot on are copied.  NULL: no rotation (then no flags, rope_scale 1).
  * e4m3: the scale is a power of two, 2^-64 to 2^64: the least with |x| <= 448 scale for the
  * values that enter a (page, head) in this call, and no less than that of the tokens that
  * stand before them in the page; if those have a smaller one, their codes are rounded to the
  * new one (exact unless a code falls below the least normal one).  A code is value / scale
- * rounded to nearest even.  What is not finite becomes a NaN and has no say in the scale.
+ * rounded to nearest even; magnitudes past 448 2^64 are held there.  What is not finite
+ * becomes a NaN and has no say in the scale.
  * Tokens behind the appended ones in a page count as not there.
  * Aliasing: caches and scales are in and out; they and q_out overlap nothing else of the call
  * (keys' and values' views may lie between one another).  No page is named by two sequences,

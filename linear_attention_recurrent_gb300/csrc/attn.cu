@@ -20,6 +20,8 @@
 // attn_join adds them.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "layer_common.cuh"
 #include "serve_params.h"
 
@@ -478,55 +480,97 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                 }
             }
 
-            // the values
+            // the values.  A weight of 0 does not keep an infinity or NaN out of a sum: where a
+            // tile that not all rows see all of holds one, each of the step's tokens has its
+            // product with the places that it sees, and its rows alone take it.
+            bool apart = false;
+            if (!inner && p.T > 1) {
+                for (int j = lane; j < S::TILE / 16; j += 32) {
+                    const uint4 u = lds16(vt + j * 16);
+                    const unsigned x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr) {
-                const int ra = gr * 16 + t4 * 2;
+                    for (int w = 0; w < 4; ++w)
+                        apart |= F8 ? (__vcmpeq4(x[w] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u)
+                                    : (__vcmpgeu2(x[w] & 0x7fff7fffu, 0x7f807f80u) != 0u);
+                }
+                apart = __any_sync(0xffffffffu, apart);
+            }
+            auto values = [&](auto careful) {
 #pragma unroll
-                for (int ci = 0; ci < (S::CH + 7) / 8; ++ci) {
-                    uint4 u[4];
+                for (int gr = 0; gr < GR; ++gr) {
+                    const int ra = gr * 16 + t4 * 2;
+                    auto add = [&](int n, unsigned b0, unsigned b1) {
+                        if constexpr (!decltype(careful)::value) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = ra + (r & 1) + (r >> 1) * 8;
-                        if constexpr (S::CH == 4) {   // half a chunk a lane
-                            const uint2 w = lds8(vt + place<S::CH, false>(row, g >> 1) + (g & 1) * 8);
-                            u[r] = make_uint4(w.x, w.y, 0u, 0u);
-                        } else {
-                            u[r] = lds16(vt + place<S::CH, false>(row, g + ci * 8));
-                        }
-                    }
-                    constexpr int W = S::CH == 4 ? 2 : 4;
-#pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        auto word = [&](int r) { return w == 0 ? u[r].x : w == 1 ? u[r].y : w == 2 ? u[r].z : u[r].w; };
-                        if constexpr (F8) {
-                            unsigned x[2], y[2];
-                            x[0] = __byte_perm(word(0), word(1), 0x5140);
-                            x[1] = __byte_perm(word(0), word(1), 0x7362);
-                            y[0] = __byte_perm(word(2), word(3), 0x5140);
-                            y[1] = __byte_perm(word(2), word(3), 0x7362);
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) {
-                                const unsigned b0 = f16_of_e4m3(static_cast<unsigned short>(x[d >> 1] >> ((d & 1) * 16)));
-                                const unsigned b1 = f16_of_e4m3(static_cast<unsigned short>(y[d >> 1] >> ((d & 1) * 16)));
-#pragma unroll
-                                for (int m = 0; m < MT; ++m) mma<F8>(o[m][(ci * W + w) * 4 + d], pa[m][gr], b0, b1);
+                            for (int m = 0; m < MT; ++m) {
+                                mma<F8>(o[m][n], pa[m][gr], b0, b1);
+                                if constexpr (!F8) mma<F8>(o[m][n], pb[m][gr], b0, b1);
                             }
                         } else {
+                            for (int tk = 0; tk < p.T; ++tk) {
+                                const int end = min(seen.own + tk + 1, seen.hi), begin = p.window ? seen.own + tk + 1 - p.window : 0;
+                                unsigned keep[2];
 #pragma unroll
-                            for (int d = 0; d < 2; ++d) {
-                                const unsigned b0 = __byte_perm(word(0), word(1), d ? 0x7632 : 0x5410);
-                                const unsigned b1 = __byte_perm(word(2), word(3), d ? 0x7632 : 0x5410);
+                                for (int k = 0; k < 2; ++k) {
+                                    const int at = pos + ra + k * 8;
+                                    keep[k] = (at >= begin && at < end ? 0xffffu : 0u) | (at + 1 >= begin && at + 1 < end ? 0xffff0000u : 0u);
+                                }
 #pragma unroll
                                 for (int m = 0; m < MT; ++m) {
-                                    mma<F8>(o[m][(ci * W + w) * 2 + d], pa[m][gr], b0, b1);
-                                    mma<F8>(o[m][(ci * W + w) * 2 + d], pb[m][gr], b0, b1);
+                                    float y[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma<F8>(y, pa[m][gr], b0 & keep[0], b1 & keep[1]);
+                                    if constexpr (!F8) mma<F8>(y, pb[m][gr], b0 & keep[0], b1 & keep[1]);
+                                    if (e0[m] == seen.own + tk + 1) {
+                                        o[m][n][0] += y[0];
+                                        o[m][n][1] += y[1];
+                                    }
+                                    if (e1[m] == seen.own + tk + 1) {
+                                        o[m][n][2] += y[2];
+                                        o[m][n][3] += y[3];
+                                    }
                                 }
+                            }
+                        }
+                    };
+#pragma unroll
+                    for (int ci = 0; ci < (S::CH + 7) / 8; ++ci) {
+                        uint4 u[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int row = ra + (r & 1) + (r >> 1) * 8;
+                            if constexpr (S::CH == 4) {   // half a chunk a lane
+                                const uint2 w = lds8(vt + place<S::CH, false>(row, g >> 1) + (g & 1) * 8);
+                                u[r] = make_uint4(w.x, w.y, 0u, 0u);
+                            } else {
+                                u[r] = lds16(vt + place<S::CH, false>(row, g + ci * 8));
+                            }
+                        }
+                        constexpr int W = S::CH == 4 ? 2 : 4;
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            auto word = [&](int r) { return w == 0 ? u[r].x : w == 1 ? u[r].y : w == 2 ? u[r].z : u[r].w; };
+                            if constexpr (F8) {
+                                unsigned x[2], y[2];
+                                x[0] = __byte_perm(word(0), word(1), 0x5140);
+                                x[1] = __byte_perm(word(0), word(1), 0x7362);
+                                y[0] = __byte_perm(word(2), word(3), 0x5140);
+                                y[1] = __byte_perm(word(2), word(3), 0x7362);
+#pragma unroll
+                                for (int d = 0; d < 4; ++d)
+                                    add((ci * W + w) * 4 + d, f16_of_e4m3(static_cast<unsigned short>(x[d >> 1] >> ((d & 1) * 16))),
+                                        f16_of_e4m3(static_cast<unsigned short>(y[d >> 1] >> ((d & 1) * 16))));
+                            } else {
+#pragma unroll
+                                for (int d = 0; d < 2; ++d)
+                                    add((ci * W + w) * 2 + d, __byte_perm(word(0), word(1), d ? 0x7632 : 0x5410),
+                                        __byte_perm(word(2), word(3), d ? 0x7632 : 0x5410));
                             }
                         }
                     }
                 }
-            }
+            };
+            if (apart) values(std::true_type{});
+            else values(std::false_type{});
         }
 
         // the warps' parts together
