@@ -11,7 +11,17 @@
 // Both products run on the tensor cores with fp32 sums.  bf16 pages take weights split
 // into two bf16 terms (16 bits of each weight).
 //
-// Work.  A tile is WT tokens of one pair (sequence, key/value head, 16 MT query rows).
+// Both products are taken transposed, S^T = K Q^T and O^T = V^T P^T, tokens and dimensions
+// along the 16 rows of an instruction and 8 query rows along its columns: the G T rows of a
+// step are few, and the other way around half of every instruction, and of every register
+// of sums, would be padding.  A lane's 16 bytes of a key are four steps' operands in an
+// order that the queries are laid out to match; a value's 16 bytes are the same dimensions
+// of eight steps.
+//
+// A weight is taken against a maximum that is moved only when a score passes it by 2^8
+// (fp16 reaches 2^16): no maximum is looked for, only that none is too large.
+//
+// Work.  A tile is WT tokens of one pair (sequence, key/value head, 8 NR query rows).
 // The tiles of all pairs in a row are dealt out to the blocks in equal shares, a
 // multiple of four tiles, whatever the lengths, which only the device knows: a block's
 // four warps take its tiles in turn, every warp with a ring of its own in shared memory
@@ -34,6 +44,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxBlocks = 608;    // of a call: bounds the workspace
+#ifndef LAR_ATTN_STAGES
+#define LAR_ATTN_STAGES 2
+#endif
+
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;      // a weight may grow to 2^8 before the sums are scaled down
 
@@ -43,28 +57,36 @@ constexpr int tile_tokens(int D, bool f8) {
     return t > 32 ? 32 : t < 16 ? 16 : t;
 }
 
-constexpr int kStages = 3;
+constexpr float kNone = -1e30f;    // the maximum of a row that has seen nothing
 
-template <int D, bool F8, int MT>
+template <int D, bool F8, int NR>
 struct Shape {
     static constexpr int WT = tile_tokens(D, F8);
-    static constexpr int ROW = D * (F8 ? 1 : 2);       // bytes of a token's row
+    static constexpr int GR = WT / 16;                 // granules of 16 tokens: a page at most
+    static constexpr int ES = F8 ? 1 : 2;
+    static constexpr int ROW = D * ES;                 // bytes of a token's row
     static constexpr int CH = ROW / 16;                // its 16-byte chunks
     static constexpr int TILE = WT * ROW;              // bytes of a tile's keys
-    static constexpr int RING = kStages * 2 * TILE;    // a warp's
+    static constexpr int STAGES = LAR_ATTN_STAGES;
+    static constexpr int RING = STAGES * 2 * TILE;     // a warp's
     static constexpr int KS = D / 16;                  // steps of the first product
-    static constexpr int NT = D / 8;                   // column tiles of the second
-    static constexpr int ROWS = 16 * MT;
-    static constexpr int QF = KS * MT * 32 * 16;       // query fragments, bytes
-    static constexpr int PART = ROWS * (D + 2);        // floats of a part: sums, maxima, outputs
+    static constexpr int MT = D / 16;                  // row tiles of the second
+    static constexpr int ROWS = 8 * NR;
+    static constexpr int QF = KS * NR * 32 * 8;        // query fragments, bytes
+    static constexpr int PART = ROWS * (D + 2);        // floats of a part: maxima, sums, outputs
     static constexpr int JOIN = kWarps * PART * 4;
     static constexpr int BODY = kWarps * RING > JOIN ? kWarps * RING : JOIN;
     static constexpr int SMEM = BODY + QF + ROWS * 4;
-    static constexpr bool QREG = D * MT <= 128;        // fragments stay in registers
+    static constexpr bool QREG = D * NR <= 256;        // fragments stay in registers
+    static constexpr int BLOCKS = D * NR <= 128 ? 3 : 2;   // an SM, by registers
 };
 
 __device__ __forceinline__ void cp16_zfill(unsigned dst, const void* src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp16(unsigned dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds16(unsigned a) {
@@ -104,6 +126,13 @@ __device__ __forceinline__ unsigned pack_f16x2(float lo, float hi) {
     return y;
 }
 
+// An 8 x 8 matrix of 16-bit numbers, two neighbours of row lane / 4 in a lane: transposed
+__device__ __forceinline__ unsigned turned(unsigned x) {
+    unsigned y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // d += a b, 16 x 8 x 16, fp32 sums
 template <bool F8>
 __device__ __forceinline__ void mma(float* d, const unsigned* a, unsigned b0, unsigned b1) {
@@ -139,14 +168,13 @@ __device__ __forceinline__ int tiles_of(const Seen& s) {
     return s.hi > s.lo ? (s.hi + WT - 1) / WT - s.lo / WT : 0;
 }
 
-// All tiles of the call, and for a block that asks with `first`: the sequence that
-// holds tile `first` and how many tiles come before it.  By the whole block.
-struct Deal {
-    int64_t total;
-    int b;
-    int64_t before;
-};
+// Tiles of a block: equal shares, in whole turns of its warps
+__device__ __forceinline__ int64_t share_of(int64_t total, int64_t blocks) {
+    return ((total + blocks - 1) / blocks + kWarps - 1) / kWarps * kWarps;
+}
 
+// The call's tiles a pair and row block, over all sequences, in part[THREADS / 32]; returns
+// those before sequence `lo` of this thread's [lo, hi).  By the whole block.
 template <int WT, int THREADS>
 __device__ __forceinline__ int64_t sum_tiles(const AttnParams& p, int64_t* part, int lo, int hi, int32_t* bits) {
     int64_t mine = 0;
@@ -167,9 +195,10 @@ __device__ __forceinline__ int64_t sum_tiles(const AttnParams& p, int64_t* part,
     return before + run - mine;   // tiles before this thread's sequences
 }
 
-template <int D, bool F8, int MT>
-__global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant__ AttnParams p, int row_blocks) {
-    using S = Shape<D, F8, MT>;
+template <int D, bool F8, int NR>
+__global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_kernel(const __grid_constant__ AttnParams p, int row_blocks) {
+    using S = Shape<D, F8, NR>;
+    constexpr int GR = S::GR, CH = S::CH;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t scan_s[kWarps + 1];
     __shared__ int at_b;
@@ -186,8 +215,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
     const int pairs = p.c.H * row_blocks;   // of a sequence
     const int64_t before = sum_tiles<S::WT, kThreads>(p, scan_s, sb0, sb1, &bits);
     const int64_t total = scan_s[kWarps] * pairs;
-    int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    share = (share + kWarps - 1) / kWarps * kWarps;
+    const int64_t share = share_of(total, gridDim.x);
     int64_t i0 = share * blockIdx.x;
     const int64_t i1 = min(total, i0 + share);
     if (blockIdx.x == 0) flag_err(p.dev_err, bits);
@@ -207,6 +235,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
     int b = at_b;
     int64_t b_first = at_before;   // tile index of sequence b's first tile
 
+    // where this lane's pieces of 32 chunks of a granule lie, here and there
+    constexpr int RS = 32 / CH > 0 ? 32 / CH : 1;    // rows that 32 chunks cover
+    const int row_l = lane / CH, c_l = lane % CH;
+    const int64_t k_step = p.c.ks[1] * S::ES * RS, v_step = p.c.vs[1] * S::ES * RS;
+    const int64_t k_lane = p.c.ks[1] * S::ES * row_l + c_l * 16, v_lane = p.c.vs[1] * S::ES * row_l + c_l * 16;
+
     while (i0 < i1) {
         const Seen seen = seen_of(p, b, &bits);
         const int n_tiles = tiles_of<S::WT>(seen);
@@ -222,8 +256,74 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
         const int h = pair / row_blocks, rb = pair % row_blocks;
         const int rows = min(S::ROWS, p.G * p.T - rb * S::ROWS), row0 = rb * S::ROWS;   // row = token G + head of the group
 
+        // This warp's tiles: s0 + warp, + 4, ...  Lane j of a batch knows where granule j % GR
+        // of tile j / GR lies and its scales; batches are read one ahead.
+        constexpr int BT = 32 / GR;
+        const int tile0 = seen.lo / S::WT + s0 + warp;
+        const int mine = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;
+        auto place_of = [&](int i) { return (tile0 + i * kWarps) * S::WT; };
+        auto page_of = [&](int batch) {   // -1: nothing to see there
+            const int i = batch * BT + lane / GR;
+            const int pos = place_of(i) + lane % GR * 16;
+            if (i >= mine || pos >= seen.hi || pos + 16 <= seen.lo) return -1;
+            const int64_t id = ld_idx(p.c.table, b * p.c.tab_s[0] + (pos / p.c.page) * p.c.tab_s[1], p.c.tab_dt);
+            if (id >= p.c.P) bits |= LAR_DEVERR_PAGE;
+            return id < 0 || id >= p.c.P ? -1 : static_cast<int>(id);
+        };
+        int id_next = page_of(0);
+        int64_t k_at = -1, v_at = -1;      // bytes from the caches' beginnings to the granule, this lane's pieces apart
+        float ks_raw = 1.f, vs_raw = 1.f;  // the scales of the batch that is being loaded
+        bool there = false;
+        auto load_batch = [&](int batch) {
+            there = id_next >= 0;
+            const int in_page = (place_of(batch * BT + lane / GR) + lane % GR * 16) % p.c.page;
+            k_at = there ? (id_next * p.c.ks[0] + in_page * p.c.ks[1] + h * p.c.ks[2]) * S::ES : -1;
+            v_at = there ? (id_next * p.c.vs[0] + in_page * p.c.vs[1] + h * p.c.vs[2]) * S::ES : -1;
+            if (F8 && there) {
+                ks_raw = __ldg(p.c.k_scale + id_next * p.c.kss[0] + h * p.c.kss[1]);
+                vs_raw = __ldg(p.c.v_scale + id_next * p.c.vss[0] + h * p.c.vss[1]);
+            }
+            id_next = page_of(batch + 1);
+        };
+        load_batch(0);
+        auto load = [&](int i) {
+            if (i < mine) {
+                if (i > 0 && i % BT == 0) load_batch(i / BT);
+                const int pos = place_of(i);
+                const unsigned dst = ring + i % S::STAGES * (2 * S::TILE);
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr) {
+                    const int src = i % BT * GR + gr, p0 = pos + gr * 16;
+                    const int64_t ka = __shfl_sync(0xffffffffu, k_at, src), va = __shfl_sync(0xffffffffu, v_at, src);
+                    const char *kp = static_cast<const char*>(p.c.k) + ka + k_lane, *vp = static_cast<const char*>(p.c.v) + va + v_lane;
+                    if (ka >= 0 && p0 >= seen.lo && p0 + 16 <= seen.hi) {
+#pragma unroll
+                        for (int j = 0; j < CH / 2; ++j) {
+                            const int row = gr * 16 + row_l + j * RS;
+                            cp16(dst + place<CH, true>(row, c_l), kp);
+                            cp16(dst + S::TILE + place<CH, false>(row, c_l), vp);
+                            kp += k_step;
+                            vp += v_step;
+                        }
+                    } else {   // zeros where there is nothing to see
+                        for (int j = 0; j < CH / 2; ++j) {
+                            const int row = gr * 16 + row_l + j * RS, at = pos + row;
+                            const bool take = ka >= 0 && at >= seen.lo && at < seen.hi;
+                            cp16_zfill(dst + place<CH, true>(row, c_l), take ? kp : static_cast<const char*>(p.c.k), take);
+                            cp16_zfill(dst + S::TILE + place<CH, false>(row, c_l), take ? vp : static_cast<const char*>(p.c.v), take);
+                            kp += k_step;
+                            vp += v_step;
+                        }
+                    }
+                }
+            }
+            cp_async_commit();   // always, so that groups are counted alike
+        };
+#pragma unroll
+        for (int i = 0; i < S::STAGES - 1; ++i) load(i);
+
         // the queries as fragments: lane (g, t4) of step ks holds dimensions
-        // (ks / CS * 4 + t4) * CD + ks % CS * 4 + {0, 1, 2, 3} of rows g and g + 8
+        // (ks / CS * 4 + t4) * CD + ks % CS * 4 + {0, 1, 2, 3} of row g
         constexpr int CD = F8 ? 16 : 8, CS = CD / 4;   // dimensions and steps of a chunk
         for (int r = warp; r < S::ROWS; r += kWarps) {
             float x[D / 32];
@@ -248,237 +348,169 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < D / 32; i += 2) {
                 const int d = (lane + (i >> 1 << 5)) * 2;
-                const int c = d / CD, ks = (c >> 2) * CS + d % CD / 4, w = (d & 3) >> 1;   // w: a0/a1 or a2/a3
+                const int c = d / CD, ks = (c >> 2) * CS + d % CD / 4, w = (d & 3) >> 1;
                 const int owner = ((r & 7) << 2) + (c & 3);
                 const unsigned v = F8 ? pack_f16x2(x[i] * mul, x[i + 1] * mul) : pack_bf16x2(x[i], x[i + 1]);
-                *reinterpret_cast<unsigned*>(qf + (((r >> 4) * S::KS + ks) * 32 + owner) * 16 + (w * 2 + ((r >> 3) & 1)) * 4) = v;
+                *reinterpret_cast<unsigned*>(qf + (((r >> 3) * S::KS + ks) * 32 + owner) * 8 + w * 4) = v;
             }
             if (lane == 0) qc[r] = p.scale * kLog2e * back;
         }
         __syncthreads();
 
-        unsigned qr[S::QREG ? MT : 1][S::QREG ? S::KS : 1][4];
+        uint2 qr[S::QREG ? NR : 1][S::QREG ? S::KS : 1];
+        auto query = [&](int n, int k) { return *reinterpret_cast<const uint2*>(qf + ((n * S::KS + k) * 32 + lane) * 8); };
         if constexpr (S::QREG) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int k = 0; k < S::KS; ++k)
-                    *reinterpret_cast<uint4*>(qr[m][k]) = *reinterpret_cast<const uint4*>(qf + ((m * S::KS + k) * 32 + lane) * 16);
+                for (int k = 0; k < S::KS; ++k) qr[n][k] = query(n, k);
         }
-        float c0[MT], c1[MT];
-        int e0[MT], e1[MT];   // one past the last place that the rows see
-        float m0[MT], m1[MT], l0[MT], l1[MT];
-        float o[MT][S::NT][4];
+        // this lane's rows: n 8 + t4 2 + {0, 1}
+        float cf[NR][2], mx[NR][2], l[NR][2];
+        int end[NR][2];   // one past the last place that the row sees
+        float o[NR][S::MT][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            c0[m] = qc[m * 16 + g];
-            c1[m] = qc[m * 16 + g + 8];
-            e0[m] = seen.own + (row0 + m * 16 + g) / p.G + 1;
-            e1[m] = seen.own + (row0 + m * 16 + g + 8) / p.G + 1;
-            m0[m] = m1[m] = -INFINITY;
-            l0[m] = l1[m] = 0.f;
+        for (int n = 0; n < NR; ++n) {
 #pragma unroll
-            for (int n = 0; n < S::NT; ++n)
+            for (int k = 0; k < 2; ++k) {
+                const int r = n * 8 + t4 * 2 + k;
+                cf[n][k] = qc[r];
+                end[n][k] = seen.own + (row0 + r) / p.G + 1;
+                mx[n][k] = kNone;
+                l[n][k] = 0.f;
+            }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[m][n][k] = 0.f;
+            for (int m = 0; m < S::MT; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[n][m][k] = 0.f;
         }
-
-        // This warp's tiles: s0 + warp, + 4, ...  Lane j of a batch knows the page and the
-        // scales of granule (16 tokens) j % GR of tile j / GR; batches are read one ahead.
-        constexpr int GR = S::WT / 16, BT = 32 / GR;
-        const int first_tile = seen.lo / S::WT;
-        const int mine = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;
-        auto place_of = [&](int i) { return (first_tile + s0 + warp + i * kWarps) * S::WT; };
-        auto page_of = [&](int batch) {   // -1: nothing to see there
-            const int i = batch * BT + lane / GR;
-            const int pos = place_of(i) + lane % GR * 16;
-            if (i >= mine || pos >= seen.hi || pos + 16 <= seen.lo) return -1;
-            const int64_t id = ld_idx(p.c.table, b * p.c.tab_s[0] + (pos / p.c.page) * p.c.tab_s[1], p.c.tab_dt);
-            if (id >= p.c.P) bits |= LAR_DEVERR_PAGE;
-            return id < 0 || id >= p.c.P ? -1 : static_cast<int>(id);
-        };
-        auto scales_of = [&](int id, float& ks, float& vs) {
-            if (F8 && id >= 0) {
-                ks = __ldg(p.c.k_scale + id * p.c.kss[0] + h * p.c.kss[1]);
-                vs = __ldg(p.c.v_scale + id * p.c.vss[0] + h * p.c.vss[1]);
-            } else {
-                ks = vs = 1.f;
-            }
-        };
-        int id0 = page_of(0), id1 = page_of(1);
-        float ks0, vs0, ks1, vs1;
-        scales_of(id0, ks0, vs0);
-        scales_of(id1, ks1, vs1);
-        int load_batch = 0, id_l0 = id0, id_l1 = id1;   // the loads run ahead of the products
-
-        auto load = [&](int i) {
-            if (i < mine) {
-                if (i / BT != load_batch) {
-                    load_batch = i / BT;
-                    id_l0 = id_l1;
-                    id_l1 = page_of(load_batch + 1);
-                }
-                const int pos = place_of(i);
-                const unsigned dst = ring + i % kStages * (2 * S::TILE);
-#pragma unroll
-                for (int gr = 0; gr < GR; ++gr) {
-                    const int id = __shfl_sync(0xffffffffu, id_l0, i % BT * GR + gr);
-                    const int in_page = (pos + gr * 16) % p.c.page;
-                    const int64_t idc = id < 0 ? 0 : id;
-                    const char* kp = static_cast<const char*>(p.c.k) + (idc * p.c.ks[0] + in_page * p.c.ks[1] + h * p.c.ks[2]) * (F8 ? 1 : 2);
-                    const char* vp = static_cast<const char*>(p.c.v) + (idc * p.c.vs[0] + in_page * p.c.vs[1] + h * p.c.vs[2]) * (F8 ? 1 : 2);
-#pragma unroll
-                    for (int j = 0; j < 16 * S::CH / 32; ++j) {
-                        const int row = (lane + j * 32) / S::CH, c = (lane + j * 32) % S::CH;
-                        const int at = pos + gr * 16 + row;
-                        const bool take = id >= 0 && at >= seen.lo && at < seen.hi;
-                        const int64_t kof = row * p.c.ks[1] * (F8 ? 1 : 2) + c * 16, vof = row * p.c.vs[1] * (F8 ? 1 : 2) + c * 16;
-                        cp16_zfill(dst + place<S::CH, true>(gr * 16 + row, c), take ? kp + kof : static_cast<const char*>(p.c.k), take);
-                        cp16_zfill(dst + S::TILE + place<S::CH, false>(gr * 16 + row, c), take ? vp + vof : static_cast<const char*>(p.c.v), take);
-                    }
-                }
-            }
-            cp_async_commit();   // always, so that groups are counted alike
-        };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) load(i);
+        float gk_l = 1.f, gv_l = 0.f, gi_l = 1.f;   // of this lane's granule: the keys' scale, log2 and inverse of the values'
 
         for (int i = 0; i < mine; ++i) {
-            if (i > 0 && i % BT == 0) {
-                const int batch = i / BT;
-                id0 = id1;
-                ks0 = ks1;
-                vs0 = vs1;
-                id1 = page_of(batch + 1);
-                scales_of(id1, ks1, vs1);
+            if (i % BT == 0) {   // the loads are at this batch already, and not at the next one
+                gk_l = ks_raw;
+                gv_l = !there ? -INFINITY : F8 ? log2f(vs_raw) : 0.f;
+                gi_l = F8 ? 1.f / vs_raw : 1.f;
             }
-            cp_async_wait<kStages - 2>();
+            cp_async_wait<S::STAGES - 2>();
             __syncwarp();
-            load(i + kStages - 1);
-            const unsigned kt = ring + i % kStages * (2 * S::TILE), vt = kt + S::TILE;
+            load(i + S::STAGES - 1);
+            const unsigned kt = ring + i % S::STAGES * (2 * S::TILE), vt = kt + S::TILE;
             const int pos = place_of(i);
 
-            float s[MT][S::WT / 8][4];
+            float s[GR][NR][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-                for (int n = 0; n < S::WT / 8; ++n)
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) s[m][n][k] = 0.f;
+                    for (int k = 0; k < 4; ++k) s[gr][n][k] = 0.f;
 #pragma unroll
-            for (int j = 0; j < S::CH / 4; ++j) {
-                unsigned qs[MT][CS][4];
+            for (int j = 0; j < CH / 4; ++j) {
+                uint2 qs[NR][CS];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int w = 0; w < CS; ++w)
-                        if constexpr (S::QREG) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) qs[m][w][k] = qr[m][j * CS + w][k];
-                        } else {
-                            *reinterpret_cast<uint4*>(qs[m][w]) =
-                                *reinterpret_cast<const uint4*>(qf + ((m * S::KS + j * CS + w) * 32 + lane) * 16);
-                        }
-#pragma unroll
-                for (int n = 0; n < S::WT / 8; ++n) {
-                    const uint4 u = lds16(kt + place<S::CH, true>(n * 8 + g, j * 4 + t4));
-                    const unsigned x[4] = {u.x, u.y, u.z, u.w};
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int w = 0; w < CS; ++w) {
-                        unsigned b0, b1;
+                        if constexpr (S::QREG) qs[n][w] = qr[n][j * CS + w];
+                        else qs[n][w] = query(n, j * CS + w);
+                    }
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr) {
+                    const uint4 u = lds16(kt + place<CH, true>(gr * 16 + g, j * 4 + t4)), v = lds16(kt + place<CH, true>(gr * 16 + g + 8, j * 4 + t4));
+                    const unsigned x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int w = 0; w < CS; ++w) {
+                        unsigned a[4];
                         if constexpr (F8) {
-                            b0 = f16_of_e4m3(static_cast<unsigned short>(x[w]));
-                            b1 = f16_of_e4m3(static_cast<unsigned short>(x[w] >> 16));
+                            a[0] = f16_of_e4m3(static_cast<unsigned short>(x[w]));
+                            a[1] = f16_of_e4m3(static_cast<unsigned short>(y[w]));
+                            a[2] = f16_of_e4m3(static_cast<unsigned short>(x[w] >> 16));
+                            a[3] = f16_of_e4m3(static_cast<unsigned short>(y[w] >> 16));
                         } else {
-                            b0 = x[2 * w];
-                            b1 = x[2 * w + 1];
+                            a[0] = x[2 * w];
+                            a[1] = y[2 * w];
+                            a[2] = x[2 * w + 1];
+                            a[3] = y[2 * w + 1];
                         }
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) mma<F8>(s[m][n], qs[m][w], b0, b1);
+                        for (int n = 0; n < NR; ++n) mma<F8>(s[gr][n], a, qs[n][w].x, qs[n][w].y);
                     }
                 }
             }
 
-            // scores in base 2, with the values' scale, and the running maximum
+            // scores in base 2 with the values' scale, against the maximum so far
             const bool inner = pos >= (p.window ? seen.own + p.T - p.window : 0) && pos + S::WT <= seen.own + 1;   // all rows see all of it
-            float inv[GR];
-            unsigned pa[MT][S::WT / 16][4], pb[F8 ? 1 : MT][F8 ? 1 : S::WT / 16][4];
-            float gk[GR], gv[GR];
+            float gk[GR], gv[GR], gi[GR];
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
                 const int src = i % BT * GR + gr;
-                gk[gr] = __shfl_sync(0xffffffffu, ks0, src);
-                const float r = __shfl_sync(0xffffffffu, vs0, src);
-                const int id = __shfl_sync(0xffffffffu, id0, src);
-                gv[gr] = id < 0 ? -INFINITY : F8 ? log2f(r) : 0.f;
-                inv[gr] = F8 ? 1.f / r : 1.f;
+                gk[gr] = __shfl_sync(0xffffffffu, gk_l, src);
+                gv[gr] = __shfl_sync(0xffffffffu, gv_l, src);
+                gi[gr] = __shfl_sync(0xffffffffu, gi_l, src);
             }
+            // element k of granule gr, row tile n: token g + 8 (k / 2), row k % 2 of the lane's
+            auto against = [&](int gr, int n, int k, float top) {
+                const float x = fmaf(s[gr][n][k], cf[n][k & 1] * gk[gr], gv[gr] - top);
+                if (inner) return x;
+                const int at = pos + gr * 16 + g + (k >> 1) * 8, e = end[n][k & 1];
+                return at >= min(e, seen.hi) || (p.window && at < e - p.window) || gv[gr] == -INFINITY ? -INFINITY : x;
+            };
+            float w[GR][NR][4];
+            float high = -INFINITY;
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float t0 = -INFINITY, t1 = -INFINITY;
+            for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-                for (int n = 0; n < S::WT / 8; ++n) {
-                    const float f0 = c0[m] * gk[n / 2], f1 = c1[m] * gk[n / 2];
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float x = fmaf(s[m][n][k], k < 2 ? f0 : f1, gv[n / 2]);
-                        if (!inner) {
-                            const int at = pos + n * 8 + t4 * 2 + (k & 1), e = k < 2 ? e0[m] : e1[m];
-                            if (at >= min(e, seen.hi) || (p.window && at < e - p.window) || gv[n / 2] == -INFINITY) x = -INFINITY;
+                        w[gr][n][k] = against(gr, n, k, mx[n][k & 1]);
+                        high = fmaxf(high, w[gr][n][k]);
+                    }
+            if (__any_sync(0xffffffffu, high > kSlack)) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float top = mx[n][r];
+#pragma unroll
+                        for (int gr = 0; gr < GR; ++gr) top = fmaxf(top, fmaxf(against(gr, n, r, 0.f), against(gr, n, r + 2, 0.f)));
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        const float f = exp2_f(mx[n][r] - top);
+                        mx[n][r] = top;
+                        l[n][r] *= f;
+#pragma unroll
+                        for (int m = 0; m < S::MT; ++m) {
+                            o[n][m][r] *= f;
+                            o[n][m][r + 2] *= f;
                         }
-                        s[m][n][k] = x;
-                        if (k < 2) t0 = fmaxf(t0, x);
-                        else t1 = fmaxf(t1, x);
-                    }
-                }
 #pragma unroll
-                for (int off = 1; off < 4; off <<= 1) {
-                    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
-                    t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
-                }
-                const bool up = t0 > m0[m] + kSlack || t1 > m1[m] + kSlack;
-                if (__any_sync(0xffffffffu, up)) {
-                    const float n0 = fmaxf(m0[m], t0), n1 = fmaxf(m1[m], t1);
-                    const float a0 = m0[m] == -INFINITY ? 0.f : exp2_f(m0[m] - n0), a1 = m1[m] == -INFINITY ? 0.f : exp2_f(m1[m] - n1);
-                    m0[m] = n0;
-                    m1[m] = n1;
-                    l0[m] *= a0;
-                    l1[m] *= a1;
-#pragma unroll
-                    for (int n = 0; n < S::NT; ++n) {
-                        o[m][n][0] *= a0;
-                        o[m][n][1] *= a0;
-                        o[m][n][2] *= a1;
-                        o[m][n][3] *= a1;
-                    }
-                }
-                const float b0 = m0[m] == -INFINITY ? 0.f : m0[m], b1 = m1[m] == -INFINITY ? 0.f : m1[m];
-#pragma unroll
-                for (int gr = 0; gr < GR; ++gr) {
-                    float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-                    for (int n = 2 * gr; n < 2 * gr + 2; ++n) {
-                        float x[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) x[k] = exp2_f(s[m][n][k] - (k < 2 ? b0 : b1));
-                        sum0 += x[0] + x[1];
-                        sum1 += x[2] + x[3];
-                        if constexpr (F8) {
-                            pa[m][gr][(n & 1) * 2] = pack_f16x2(x[0], x[1]);
-                            pa[m][gr][(n & 1) * 2 + 1] = pack_f16x2(x[2], x[3]);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const unsigned hi = pack_bf16x2(x[2 * k], x[2 * k + 1]);
-                                pa[m][gr][(n & 1) * 2 + k] = hi;
-                                pb[m][gr][(n & 1) * 2 + k] = pack_bf16x2(x[2 * k] - __uint_as_float(hi << 16), x[2 * k + 1] - __uint_as_float(hi & 0xffff0000u));
-                            }
+                        for (int gr = 0; gr < GR; ++gr) {
+                            w[gr][n][r] = against(gr, n, r, top);
+                            w[gr][n][r + 2] = against(gr, n, r + 2, top);
                         }
                     }
-                    l0[m] = fmaf(sum0, inv[gr], l0[m]);
-                    l1[m] = fmaf(sum1, inv[gr], l1[m]);
-                }
             }
+            // the weights, turned so that a lane has tokens t4 2 + {0, 1} (and + 8) of row g
+            unsigned pa[GR][NR][2], pb[F8 ? 1 : GR][F8 ? 1 : NR][2];
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float x = exp2_f(w[gr][n][2 * k]), y = exp2_f(w[gr][n][2 * k + 1]);
+                        l[n][0] = fmaf(x, gi[gr], l[n][0]);
+                        l[n][1] = fmaf(y, gi[gr], l[n][1]);
+                        if constexpr (F8) {
+                            pa[gr][n][k] = turned(pack_f16x2(x, y));
+                        } else {
+                            const unsigned hi = pack_bf16x2(x, y);
+                            pa[gr][n][k] = turned(hi);
+                            pb[gr][n][k] = turned(pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)));
+                        }
+                    }
 
             // the values.  A weight of 0 does not keep an infinity or NaN out of a sum: where a
             // tile that not all rows see all of holds one, each of the step's tokens has its
@@ -489,9 +521,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                     const uint4 u = lds16(vt + j * 16);
                     const unsigned x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        apart |= F8 ? (__vcmpeq4(x[w] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u)
-                                    : (__vcmpgeu2(x[w] & 0x7fff7fffu, 0x7f807f80u) != 0u);
+                    for (int e = 0; e < 4; ++e)
+                        apart |= F8 ? (__vcmpeq4(x[e] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u)
+                                    : (__vcmpgeu2(x[e] & 0x7fff7fffu, 0x7f807f80u) != 0u);
                 }
                 apart = __any_sync(0xffffffffu, apart);
             }
@@ -499,71 +531,68 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) {
                     const int ra = gr * 16 + t4 * 2;
-                    auto add = [&](int n, unsigned b0, unsigned b1) {
+                    auto add = [&](int m, const unsigned* a) {
                         if constexpr (!decltype(careful)::value) {
 #pragma unroll
-                            for (int m = 0; m < MT; ++m) {
-                                mma<F8>(o[m][n], pa[m][gr], b0, b1);
-                                if constexpr (!F8) mma<F8>(o[m][n], pb[m][gr], b0, b1);
+                            for (int n = 0; n < NR; ++n) {
+                                mma<F8>(o[n][m], a, pa[gr][n][0], pa[gr][n][1]);
+                                if constexpr (!F8) mma<F8>(o[n][m], a, pb[gr][n][0], pb[gr][n][1]);
                             }
                         } else {
                             for (int tk = 0; tk < p.T; ++tk) {
-                                const int end = min(seen.own + tk + 1, seen.hi), begin = p.window ? seen.own + tk + 1 - p.window : 0;
+                                const int last = min(seen.own + tk + 1, seen.hi), first = p.window ? seen.own + tk + 1 - p.window : 0;
                                 unsigned keep[2];
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     const int at = pos + ra + k * 8;
-                                    keep[k] = (at >= begin && at < end ? 0xffffu : 0u) | (at + 1 >= begin && at + 1 < end ? 0xffff0000u : 0u);
+                                    keep[k] = (at >= first && at < last ? 0xffffu : 0u) | (at + 1 >= first && at + 1 < last ? 0xffff0000u : 0u);
                                 }
+                                const unsigned v[4] = {a[0] & keep[0], a[1] & keep[0], a[2] & keep[1], a[3] & keep[1]};
 #pragma unroll
-                                for (int m = 0; m < MT; ++m) {
+                                for (int n = 0; n < NR; ++n) {
                                     float y[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma<F8>(y, pa[m][gr], b0 & keep[0], b1 & keep[1]);
-                                    if constexpr (!F8) mma<F8>(y, pb[m][gr], b0 & keep[0], b1 & keep[1]);
-                                    if (e0[m] == seen.own + tk + 1) {
-                                        o[m][n][0] += y[0];
-                                        o[m][n][1] += y[1];
-                                    }
-                                    if (e1[m] == seen.own + tk + 1) {
-                                        o[m][n][2] += y[2];
-                                        o[m][n][3] += y[3];
-                                    }
+                                    mma<F8>(y, v, pa[gr][n][0], pa[gr][n][1]);
+                                    if constexpr (!F8) mma<F8>(y, v, pb[gr][n][0], pb[gr][n][1]);
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r)
+                                        if (end[n][r] == seen.own + tk + 1) {
+                                            o[n][m][r] += y[r];
+                                            o[n][m][r + 2] += y[r + 2];
+                                        }
                                 }
                             }
                         }
                     };
 #pragma unroll
-                    for (int ci = 0; ci < (S::CH + 7) / 8; ++ci) {
+                    for (int ci = 0; ci < (CH + 7) / 8; ++ci) {
                         uint4 u[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int row = ra + (r & 1) + (r >> 1) * 8;
-                            if constexpr (S::CH == 4) {   // half a chunk a lane
-                                const uint2 w = lds8(vt + place<S::CH, false>(row, g >> 1) + (g & 1) * 8);
-                                u[r] = make_uint4(w.x, w.y, 0u, 0u);
+                            if constexpr (CH == 4) {   // half a chunk a lane
+                                const uint2 h2 = lds8(vt + place<CH, false>(row, g >> 1) + (g & 1) * 8);
+                                u[r] = make_uint4(h2.x, h2.y, 0u, 0u);
                             } else {
-                                u[r] = lds16(vt + place<S::CH, false>(row, g + ci * 8));
+                                u[r] = lds16(vt + place<CH, false>(row, g + ci * 8));
                             }
                         }
-                        constexpr int W = S::CH == 4 ? 2 : 4;
+                        // row tile m has dimensions 2 m and 2 m + 1 (of the lane's piece) in its rows g and g + 8
+                        constexpr int W = CH == 4 ? 2 : 4;
 #pragma unroll
-                        for (int w = 0; w < W; ++w) {
-                            auto word = [&](int r) { return w == 0 ? u[r].x : w == 1 ? u[r].y : w == 2 ? u[r].z : u[r].w; };
+                        for (int e = 0; e < W; ++e) {
+                            auto word = [&](int r) { return e == 0 ? u[r].x : e == 1 ? u[r].y : e == 2 ? u[r].z : u[r].w; };
                             if constexpr (F8) {
-                                unsigned x[2], y[2];
-                                x[0] = __byte_perm(word(0), word(1), 0x5140);
-                                x[1] = __byte_perm(word(0), word(1), 0x7362);
-                                y[0] = __byte_perm(word(2), word(3), 0x5140);
-                                y[1] = __byte_perm(word(2), word(3), 0x7362);
 #pragma unroll
-                                for (int d = 0; d < 4; ++d)
-                                    add((ci * W + w) * 4 + d, f16_of_e4m3(static_cast<unsigned short>(x[d >> 1] >> ((d & 1) * 16))),
-                                        f16_of_e4m3(static_cast<unsigned short>(y[d >> 1] >> ((d & 1) * 16))));
+                                for (int d = 0; d < 2; ++d) {
+                                    const unsigned x = __byte_perm(word(0), word(1), d ? 0x7362 : 0x5140), y = __byte_perm(word(2), word(3), d ? 0x7362 : 0x5140);
+                                    const unsigned a[4] = {f16_of_e4m3(static_cast<unsigned short>(x)), f16_of_e4m3(static_cast<unsigned short>(x >> 16)),
+                                                           f16_of_e4m3(static_cast<unsigned short>(y)), f16_of_e4m3(static_cast<unsigned short>(y >> 16))};
+                                    add((ci * W + e) * 2 + d, a);
+                                }
                             } else {
-#pragma unroll
-                                for (int d = 0; d < 2; ++d)
-                                    add((ci * W + w) * 2 + d, __byte_perm(word(0), word(1), d ? 0x7632 : 0x5410),
-                                        __byte_perm(word(2), word(3), d ? 0x7632 : 0x5410));
+                                const unsigned a[4] = {__byte_perm(word(0), word(1), 0x5410), __byte_perm(word(0), word(1), 0x7632),
+                                                       __byte_perm(word(2), word(3), 0x5410), __byte_perm(word(2), word(3), 0x7632)};
+                                add(ci * W + e, a);
                             }
                         }
                     }
@@ -577,66 +606,57 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
         cp_async_wait<0>();
         __syncthreads();
         float* part = reinterpret_cast<float*>(smem) + warp * S::PART;
+        constexpr int PER = CH == 4 ? 8 : CD;   // neighbouring dimensions of a lane's piece
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int off = 1; off < 4; off <<= 1) {
-                l0[m] += __shfl_xor_sync(0xffffffffu, l0[m], off);
-                l1[m] += __shfl_xor_sync(0xffffffffu, l1[m], off);
-            }
-            const int r0 = m * 16 + g, r1 = r0 + 8;
-            if (t4 == 0) {
-                part[r0] = m0[m];
-                part[r1] = m1[m];
-                part[S::ROWS + r0] = l0[m];
-                part[S::ROWS + r1] = l1[m];
-            }
-            // column tile n of lane t4 holds dimensions of the groups 2 t4 and 2 t4 + 1
-            constexpr int PER = S::CH == 4 ? 8 : F8 ? 16 : 8;   // column tiles (and neighbouring dimensions) of a group's piece
+            for (int r = 0; r < 2; ++r) {
+                const int at = n * 8 + t4 * 2 + r;
 #pragma unroll
-            for (int n = 0; n < S::NT; ++n)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int d = ((n / PER) * 8 + t4 * 2 + (k & 1)) * PER + n % PER;
-                    part[2 * S::ROWS + (k < 2 ? r0 : r1) * D + d] = o[m][n][k];
+                for (int off = 4; off < 32; off <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], off);
+                if (g == 0) {
+                    part[at] = mx[n][r];
+                    part[S::ROWS + at] = l[n][r];
                 }
-        }
+#pragma unroll
+                for (int m = 0; m < S::MT; ++m) {
+                    const int d = (m / (PER / 2) * 8 + g) * PER + m % (PER / 2) * 2;
+                    *reinterpret_cast<float2*>(part + 2 * S::ROWS + at * D + d) = make_float2(o[n][m][r], o[n][m][r + 2]);
+                }
+            }
         __syncthreads();
         const bool whole = s0 == 0 && s1 == n_tiles;
         float* ws = p.ws + (2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0)) * S::PART;
         const float* parts = reinterpret_cast<const float*>(smem);
         for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
             const int r = idx / (D / 4), d = idx % (D / 4) * 4;
-            float mx = -INFINITY, l = 0.f;
+            float top = kNone, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, parts[w * S::PART + r]);
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, parts[w * S::PART + r]);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float pm = parts[w * S::PART + r], pl = parts[w * S::PART + S::ROWS + r];
-                const float f = pm == -INFINITY ? 0.f : exp2_f(pm - mx);
-                if (pm == -INFINITY && !(pl != pl)) continue;   // saw nothing; but NaN goes on
+                const float f = exp2_f(parts[w * S::PART + r] - top);
                 const float4 x = *reinterpret_cast<const float4*>(parts + w * S::PART + 2 * S::ROWS + r * D + d);
-                const float fu = pm == -INFINITY ? 1.f : f;
-                l += fu * pl;
-                acc.x += fu * x.x;
-                acc.y += fu * x.y;
-                acc.z += fu * x.z;
-                acc.w += fu * x.w;
+                sum = fmaf(f, parts[w * S::PART + S::ROWS + r], sum);
+                acc.x = fmaf(f, x.x, acc.x);
+                acc.y = fmaf(f, x.y, acc.y);
+                acc.z = fmaf(f, x.z, acc.z);
+                acc.w = fmaf(f, x.w, acc.w);
             }
             if (whole) {
                 const int row = row0 + r, tk = row / p.G, hq = h * p.G + row % p.G;
-                const float il = l == 0.f ? 0.f : 1.f / l;
+                const float il = sum == 0.f ? 0.f : 1.f / sum;
                 const float y[4] = {acc.x * il, acc.y * il, acc.z * il, acc.w * il};
                 const int64_t at = b * p.os[0] + tk * p.os[1] + hq * p.os[2];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) st_out(p.out, at + (d + k) * p.os[3], p.o_dt, y[k]);
-                if (d == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
+                if (d == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
             } else {
                 *reinterpret_cast<float4*>(ws + 2 * S::ROWS + r * D + d) = acc;
                 if (d == 0) {
-                    ws[r] = mx;
-                    ws[S::ROWS + r] = l;
+                    ws[r] = top;
+                    ws[S::ROWS + r] = sum;
                 }
             }
         }
@@ -650,9 +670,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
 // nothing get zeros.  A block a (pair, row), its warps taking parts in turn.
 constexpr int kJoinWarps = 8;
 
-template <int D, bool F8, int MT>
+template <int D, bool F8, int NR>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(const __grid_constant__ AttnParams p, int row_blocks, int blocks) {
-    using S = Shape<D, F8, MT>;
+    using S = Shape<D, F8, NR>;
     constexpr int PER = D / 32;   // dimensions of a lane
     __shared__ int64_t scan_s[kJoinWarps + 1];
     __shared__ int64_t before_s;
@@ -680,12 +700,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(const __grid_consta
         if (tid == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = -INFINITY;
         return;
     }
-    int64_t share = (total + blocks - 1) / blocks;
-    share = (share + kWarps - 1) / kWarps * kWarps;
+    const int64_t share = share_of(total, blocks);
     const int64_t first = before_s * pairs + static_cast<int64_t>(pair) * n;
     const int64_t g0 = first / share, g1 = (first + n - 1) / share;
     if (g0 == g1) return;   // one block had all of it
-    float m = -INFINITY, l = 0.f, o[PER];
+    float m = kNone, l = 0.f, o[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) o[k] = 0.f;
     for (int64_t i = g0 + warp; i <= g1; i += kJoinWarps) {
@@ -694,13 +713,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(const __grid_consta
         float x[PER];
 #pragma unroll
         for (int k = 0; k < PER; ++k) x[k] = part[2 * S::ROWS + r * D + lane + k * 32];
-        const float nm = fmaxf(m, pm);
-        const float a = m == -INFINITY ? 0.f : exp2_f(m - nm), c = pm == -INFINITY ? 0.f : exp2_f(pm - nm);
-        const bool none = pm == -INFINITY && pl == 0.f;
-        l = fmaf(l, a, none ? 0.f : pl * (pm == -INFINITY ? 1.f : c));
+        const float top = fmaxf(m, pm), a = exp2_f(m - top), c = exp2_f(pm - top);
+        l = fmaf(l, a, pl * c);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) o[k] = fmaf(o[k], a, none ? 0.f : x[k] * (pm == -INFINITY ? 1.f : c));
-        m = nm;
+        for (int k = 0; k < PER; ++k) o[k] = fmaf(o[k], a, x[k] * c);
+        m = top;
     }
     if (lane == 0) {
         m_s[warp] = m;
@@ -709,63 +726,74 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(const __grid_consta
 #pragma unroll
     for (int k = 0; k < PER; ++k) o_s[warp][lane + k * 32] = o[k];
     __syncthreads();
-    float mx = -INFINITY, ls = 0.f;
+    float top = kNone, ls = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, m_s[w]);
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, m_s[w]);
     float f[kJoinWarps];
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-        f[w] = m_s[w] == -INFINITY ? (l_s[w] != l_s[w] ? 1.f : 0.f) : exp2_f(m_s[w] - mx);
-        ls += f[w] * l_s[w];
+        f[w] = exp2_f(m_s[w] - top);
+        ls = fmaf(f[w], l_s[w], ls);
     }
     const float il = ls == 0.f ? 0.f : 1.f / ls;
     for (int d = tid; d < D; d += threads) {
         float y = 0.f;
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) y += f[w] * o_s[w][d];
+        for (int w = 0; w < kJoinWarps; ++w) y = fmaf(f[w], o_s[w][d], y);
         st_out(p.out, at + d * p.os[3], p.o_dt, y * il);
     }
-    if (tid == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * kLn2;
+    if (tid == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = ls == 0.f ? -INFINITY : (top + log2f(ls)) * kLn2;
 }
 
-// Rows of a pair: 16, or 32 where a step has more and the registers hold their outputs
-int row_tiles(int T, int G, int D) { return T * G > 16 && D <= 128 ? 2 : 1; }
+// Tiles of 8 rows that a pair has: as many as its rows need, while registers hold their outputs
+constexpr int most_rows(int D) { return D <= 128 ? 4 : 2; }
 
-template <int D, bool F8, int MT>
+int row_tiles(int T, int G, int D) {
+    const int need = (T * G + 7) / 8;
+    return need <= 1 ? 1 : need <= 2 || most_rows(D) == 2 ? 2 : 4;
+}
+
+template <int D, bool F8, int NR>
 lar_status launch(const AttnParams& p, cudaStream_t stream) {
-    using S = Shape<D, F8, MT>;
+    using S = Shape<D, F8, NR>;
     const int row_blocks = (p.G * p.T + S::ROWS - 1) / S::ROWS;
-    auto kern = attn_kernel<D, F8, MT>;
+    auto kern = attn_kernel<D, F8, NR>;
     int sms = 0;
     const int occ = cached_occupancy(reinterpret_cast<const void*>(kern), kThreads, S::SMEM, S::SMEM, &sms);
     if (occ < 1) return LAR_ERR_LAUNCH;
+    const int64_t pairs = static_cast<int64_t>(p.B) * p.c.H * row_blocks;
+    if (pairs > (int64_t{1} << 31) - 1) return LAR_ERR_SHAPE;
     // no more blocks than the longest sequences that the table admits could fill
     const int64_t cap = static_cast<int64_t>(p.c.M) * p.c.page;
-    const int64_t most = (static_cast<int64_t>(p.B) * p.c.H * row_blocks * ((cap + S::WT - 1) / S::WT + 1) + kWarps - 1) / kWarps;
+    const int64_t most = (pairs * ((cap + S::WT - 1) / S::WT + 1) + kWarps - 1) / kWarps;
     int64_t blocks = static_cast<int64_t>(sms) * occ;
     if (blocks > kMaxBlocks) blocks = kMaxBlocks;
     if (blocks > most) blocks = most;
-    const int64_t pairs = static_cast<int64_t>(p.B) * p.c.H * row_blocks;
-    if (pairs > (int64_t{1} << 31) - 1) return LAR_ERR_SHAPE;
     const lar_status st = launch_ordered(kern, dim3(static_cast<unsigned>(blocks)), kThreads, S::SMEM, 1, stream, p, row_blocks);
     if (st != LAR_OK) return st;
-    return launch_ordered(attn_join<D, F8, MT>, dim3(static_cast<unsigned>(pairs), S::ROWS), kJoinWarps * 32, 0, 1, stream, p,
+    return launch_ordered(attn_join<D, F8, NR>, dim3(static_cast<unsigned>(pairs), S::ROWS), kJoinWarps * 32, 0, 1, stream, p,
                           row_blocks, static_cast<int>(blocks));
+}
+
+template <int D, bool F8>
+lar_status launch_rows(const AttnParams& p, cudaStream_t stream) {
+    const int nr = row_tiles(p.T, p.G, D);
+    if (nr == 1) return launch<D, F8, 1>(p, stream);
+    if constexpr (most_rows(D) == 4) {
+        if (nr == 4) return launch<D, F8, 4>(p, stream);
+    }
+    return launch<D, F8, 2>(p, stream);
 }
 
 template <int D>
 lar_status launch_d(const AttnParams& p, cudaStream_t stream) {
-    const int mt = row_tiles(p.T, p.G, D);
-    if constexpr (D <= 128) {
-        if (mt == 2) return p.c.e4m3 ? launch<D, true, 2>(p, stream) : launch<D, false, 2>(p, stream);
-    }
-    return p.c.e4m3 ? launch<D, true, 1>(p, stream) : launch<D, false, 1>(p, stream);
+    return p.c.e4m3 ? launch_rows<D, true>(p, stream) : launch_rows<D, false>(p, stream);
 }
 
 }  // namespace
 
 int64_t attn_workspace_floats(int T, int G, int D) {
-    return int64_t{2} * kMaxBlocks * 16 * row_tiles(T, G, D) * (D + 2);
+    return int64_t{2} * kMaxBlocks * 8 * row_tiles(T, G, D) * (D + 2);
 }
 
 lar_status launch_attn(const AttnParams& p, void* stream) {
