@@ -22,8 +22,9 @@
 // (fp16 reaches 2^16): no maximum is looked for, only that none is too large.
 //
 // Work.  A tile is WT tokens of one pair (sequence, key/value head, 8 NR query rows).
-// The tiles of all pairs in a row are dealt out to the blocks in equal shares, a
-// multiple of four tiles, whatever the lengths, which only the device knows: a block's
+// The tiles of all pairs in a row, each pair with kStart more for what its beginning and
+// end cost, are dealt out to the blocks in equal shares, a multiple of four, whatever the
+// lengths, which only the device knows: a block's
 // four warps take its tiles in turn, every warp with a ring of its own in shared memory
 // that no other warp waits for, its own running maximum, sum and output, joined
 // once a pair.  A pair that several blocks share leaves its parts in the workspace, and
@@ -49,11 +50,21 @@ constexpr int kMaxBlocks = 608;    // of a call: bounds the workspace
 #endif
 
 constexpr float kLn2 = 0.6931471805599453f;
+#ifndef LAR_ATTN_START
+#define LAR_ATTN_START 16
+#endif
+constexpr int kStart = LAR_ATTN_START;   // tiles that a pair's beginning and end count as
 constexpr float kSlack = 8.f;      // a weight may grow to 2^8 before the sums are scaled down
 
+#ifndef LAR_ATTN_TILE
+#define LAR_ATTN_TILE 8192
+#endif
+#ifndef LAR_ATTN_BLOCKS
+#define LAR_ATTN_BLOCKS 3
+#endif
 // Tokens of a warp's tile: 8 KB of keys and values, at least a granule of 16.
 constexpr int tile_tokens(int D, bool f8) {
-    const int t = 8192 / (2 * D * (f8 ? 1 : 2));
+    const int t = LAR_ATTN_TILE / (2 * D * (f8 ? 1 : 2));
     return t > 32 ? 32 : t < 16 ? 16 : t;
 }
 
@@ -78,7 +89,7 @@ struct Shape {
     static constexpr int BODY = kWarps * RING > JOIN ? kWarps * RING : JOIN;
     static constexpr int SMEM = BODY + QF + ROWS * 4;
     static constexpr bool QREG = D * NR <= 256;        // fragments stay in registers
-    static constexpr int BLOCKS = D * NR <= 128 ? 3 : 2;   // an SM, by registers
+    static constexpr int BLOCKS = D * NR <= 128 ? LAR_ATTN_BLOCKS : 2;   // an SM, by registers
 };
 
 __device__ __forceinline__ void cp16_zfill(unsigned dst, const void* src, bool take) {
@@ -113,11 +124,11 @@ __device__ __forceinline__ int place(int row, int c) {
     }
 }
 
-// two e4m3 codes as fp16 numbers (exact)
-__device__ __forceinline__ unsigned f16_of_e4m3(unsigned short x) {
-    unsigned y;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
-    return y;
+// four e4m3 codes as fp16 numbers (exact)
+__device__ __forceinline__ void f16_of_e4m3(unsigned x, unsigned& lo, unsigned& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
 }
 
 __device__ __forceinline__ unsigned pack_f16x2(float lo, float hi) {
@@ -163,9 +174,16 @@ __device__ __forceinline__ Seen seen_of(const AttnParams& p, int b, int32_t* bit
     return {lo, max(hi, lo), own};
 }
 
+// Tiles of a pair, and what it counts as where the work is dealt out: kStart in front of them
 template <int WT>
 __device__ __forceinline__ int tiles_of(const Seen& s) {
     return s.hi > s.lo ? (s.hi + WT - 1) / WT - s.lo / WT : 0;
+}
+
+template <int WT>
+__device__ __forceinline__ int weight_of(const Seen& s) {
+    const int n = tiles_of<WT>(s);
+    return n ? n + kStart : 0;
 }
 
 // Tiles of a block: equal shares, in whole turns of its warps
@@ -173,12 +191,12 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int64_t blocks) {
     return ((total + blocks - 1) / blocks + kWarps - 1) / kWarps * kWarps;
 }
 
-// The call's tiles a pair and row block, over all sequences, in part[THREADS / 32]; returns
+// What the sequences' pairs count as, one pair a sequence, in part[THREADS / 32]; returns
 // those before sequence `lo` of this thread's [lo, hi).  By the whole block.
 template <int WT, int THREADS>
-__device__ __forceinline__ int64_t sum_tiles(const AttnParams& p, int64_t* part, int lo, int hi, int32_t* bits) {
+__device__ __forceinline__ int64_t sum_weights(const AttnParams& p, int64_t* part, int lo, int hi, int32_t* bits) {
     int64_t mine = 0;
-    for (int b = lo; b < hi; ++b) mine += tiles_of<WT>(seen_of(p, b, bits));
+    for (int b = lo; b < hi; ++b) mine += weight_of<WT>(seen_of(p, b, bits));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t run = mine;
 #pragma unroll
@@ -213,17 +231,30 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
     // this block's share of the tiles
     const int per = (p.B + kThreads - 1) / kThreads, sb0 = min(p.B, tid * per), sb1 = min(p.B, sb0 + per);
     const int pairs = p.c.H * row_blocks;   // of a sequence
-    const int64_t before = sum_tiles<S::WT, kThreads>(p, scan_s, sb0, sb1, &bits);
+    const int64_t before = sum_weights<S::WT, kThreads>(p, scan_s, sb0, sb1, &bits);
     const int64_t total = scan_s[kWarps] * pairs;
     const int64_t share = share_of(total, gridDim.x);
     int64_t i0 = share * blockIdx.x;
     const int64_t i1 = min(total, i0 + share);
-    if (blockIdx.x == 0) flag_err(p.dev_err, bits);
+    int4* split = reinterpret_cast<int4*>(p.ws) + blockIdx.x;   // the pair that begins here and ends in another block
+    float* const parts_at = p.ws + 4 * kMaxBlocks;
+    if (tid == 0) *split = make_int4(-1, 0, 0, 0);
+    // rows of sequences that see nothing
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const Seen seen = seen_of(p, b, &bits);
+        if (seen.hi > seen.lo) continue;
+        for (int i = tid; i < p.T * p.Hq * D; i += kThreads) {
+            const int d = i % D, hq = i / D % p.Hq, tk = i / D / p.Hq;
+            st_out(p.out, b * p.os[0] + tk * p.os[1] + hq * p.os[2] + d * p.os[3], p.o_dt, 0.f);
+            if (d == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = -INFINITY;
+        }
+    }
+    flag_err(p.dev_err, bits);
     if (i0 >= i1) return;
     {
         int64_t run = before * pairs;
         for (int b = sb0; b < sb1; ++b) {
-            const int64_t n = static_cast<int64_t>(tiles_of<S::WT>(seen_of(p, b, &bits))) * pairs;
+            const int64_t n = static_cast<int64_t>(weight_of<S::WT>(seen_of(p, b, &bits))) * pairs;
             if (i0 >= run && i0 < run + n) {
                 at_b = b;
                 at_before = run;
@@ -233,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
     }
     __syncthreads();
     int b = at_b;
-    int64_t b_first = at_before;   // tile index of sequence b's first tile
+    int64_t b_first = at_before;   // where sequence b begins
 
     // where this lane's pieces of 32 chunks of a granule lie, here and there
     constexpr int RS = 32 / CH > 0 ? 32 / CH : 1;    // rows that 32 chunks cover
@@ -243,16 +274,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
 
     while (i0 < i1) {
         const Seen seen = seen_of(p, b, &bits);
-        const int n_tiles = tiles_of<S::WT>(seen);
-        if (n_tiles == 0 || i0 >= b_first + static_cast<int64_t>(n_tiles) * pairs) {
-            b_first += static_cast<int64_t>(n_tiles) * pairs;
+        const int n_tiles = tiles_of<S::WT>(seen), weight = weight_of<S::WT>(seen);
+        if (i0 >= b_first + static_cast<int64_t>(weight) * pairs) {
+            b_first += static_cast<int64_t>(weight) * pairs;
             ++b;
             continue;
         }
-        const int pair = static_cast<int>((i0 - b_first) / n_tiles);
-        const int64_t pair_first = b_first + static_cast<int64_t>(pair) * n_tiles;
-        const int s0 = static_cast<int>(i0 - pair_first);
+        const int pair = static_cast<int>((i0 - b_first) / weight);
+        const int64_t pair_first = b_first + static_cast<int64_t>(pair) * weight + kStart;
+        const int s0 = static_cast<int>(max(int64_t{0}, i0 - pair_first));
         const int s1 = static_cast<int>(min(static_cast<int64_t>(n_tiles), i1 - pair_first));
+        i0 = pair_first + n_tiles;   // on to the next pair
+        if (s1 <= s0) continue;      // its beginning alone
         const int h = pair / row_blocks, rb = pair % row_blocks;
         const int rows = min(S::ROWS, p.G * p.T - rb * S::ROWS), row0 = rb * S::ROWS;   // row = token G + head of the group
 
@@ -325,32 +358,39 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
         // the queries as fragments: lane (g, t4) of step ks holds dimensions
         // (ks / CS * 4 + t4) * CD + ks % CS * 4 + {0, 1, 2, 3} of row g
         constexpr int CD = F8 ? 16 : 8, CS = CD / 4;   // dimensions and steps of a chunk
-        for (int r = warp; r < S::ROWS; r += kWarps) {
-            float x[D / 32];
-            float top = 0.f;
-            const int row = row0 + r, tk = row / p.G, hq = h * p.G + row % p.G;
+        unsigned xq[S::ROWS / kWarps][D / 64];   // pairs of neighbours; all of a warp's rows asked for at once
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int d = (lane + (i >> 1 << 5)) * 2 + (i & 1);   // pairs of neighbours
-                x[i] = r < rows ? ld_in(p.q, b * p.qs[0] + tk * p.qs[1] + hq * p.qs[2] + d * p.qs[3], p.q_dt) : 0.f;
-                top = fmaxf(top, fabsf(x[i]));
+        for (int e = 0; e < S::ROWS / kWarps; ++e) {
+            const int r = warp + e * kWarps, row = row0 + r, tk = row / p.G, hq = h * p.G + row % p.G;
+            const unsigned short* src = static_cast<const unsigned short*>(p.q) + b * p.qs[0] + tk * p.qs[1] + hq * p.qs[2];
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const int64_t d = (lane + i * 32) * 2;
+                xq[e][i] = r >= rows ? 0u
+                           : p.q_pairs ? __ldg(reinterpret_cast<const unsigned*>(src + d))
+                                       : __ldg(src + d * p.qs[3]) | static_cast<unsigned>(__ldg(src + (d + 1) * p.qs[3])) << 16;
             }
+        }
+#pragma unroll
+        for (int e = 0; e < S::ROWS / kWarps; ++e) {
+            const int r = warp + e * kWarps;
             float mul = 1.f, back = 1.f;
             if constexpr (F8) {   // the greatest to 2^14 .. 2^15: fp16 holds what bf16 does, 2^-28 of it downwards
+                unsigned top = 0;   // bf16 magnitudes in order as whole numbers
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const int e = static_cast<int>(__float_as_uint(top) >> 23);   // biased
-                if (e > 15 && e < 240) {
-                    mul = __uint_as_float(static_cast<unsigned>(254 + 14 - e) << 23);
-                    back = __uint_as_float(static_cast<unsigned>(e - 14) << 23);
+                for (int i = 0; i < D / 64; ++i) top = max(top, max(xq[e][i] & 0x7fffu, xq[e][i] >> 16 & 0x7fffu));
+                const int x = static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7);   // biased exponent
+                if (x > 15 && x < 240) {
+                    mul = __uint_as_float(static_cast<unsigned>(254 + 14 - x) << 23);
+                    back = __uint_as_float(static_cast<unsigned>(x - 14) << 23);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < D / 32; i += 2) {
-                const int d = (lane + (i >> 1 << 5)) * 2;
+            for (int i = 0; i < D / 64; ++i) {
+                const int d = (lane + i * 32) * 2;
                 const int c = d / CD, ks = (c >> 2) * CS + d % CD / 4, w = (d & 3) >> 1;
                 const int owner = ((r & 7) << 2) + (c & 3);
-                const unsigned v = F8 ? pack_f16x2(x[i] * mul, x[i + 1] * mul) : pack_bf16x2(x[i], x[i + 1]);
+                const unsigned v = F8 ? pack_f16x2(__uint_as_float(xq[e][i] << 16) * mul, __uint_as_float(xq[e][i] & 0xffff0000u) * mul) : xq[e][i];
                 *reinterpret_cast<unsigned*>(qf + (((r >> 3) * S::KS + ks) * 32 + owner) * 8 + w * 4) = v;
             }
             if (lane == 0) qc[r] = p.scale * kLog2e * back;
@@ -423,10 +463,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
                     for (int w = 0; w < CS; ++w) {
                         unsigned a[4];
                         if constexpr (F8) {
-                            a[0] = f16_of_e4m3(static_cast<unsigned short>(x[w]));
-                            a[1] = f16_of_e4m3(static_cast<unsigned short>(y[w]));
-                            a[2] = f16_of_e4m3(static_cast<unsigned short>(x[w] >> 16));
-                            a[3] = f16_of_e4m3(static_cast<unsigned short>(y[w] >> 16));
+                            f16_of_e4m3(x[w], a[0], a[2]);
+                            f16_of_e4m3(y[w], a[1], a[3]);
                         } else {
                             a[0] = x[2 * w];
                             a[1] = y[2 * w];
@@ -585,8 +623,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
 #pragma unroll
                                 for (int d = 0; d < 2; ++d) {
                                     const unsigned x = __byte_perm(word(0), word(1), d ? 0x7362 : 0x5140), y = __byte_perm(word(2), word(3), d ? 0x7362 : 0x5140);
-                                    const unsigned a[4] = {f16_of_e4m3(static_cast<unsigned short>(x)), f16_of_e4m3(static_cast<unsigned short>(x >> 16)),
-                                                           f16_of_e4m3(static_cast<unsigned short>(y)), f16_of_e4m3(static_cast<unsigned short>(y >> 16))};
+                                    unsigned a[4];
+                                    f16_of_e4m3(x, a[0], a[1]);
+                                    f16_of_e4m3(y, a[2], a[3]);
                                     add((ci * W + e) * 2 + d, a);
                                 }
                             } else {
@@ -626,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
             }
         __syncthreads();
         const bool whole = s0 == 0 && s1 == n_tiles;
-        float* ws = p.ws + (2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0)) * S::PART;
+        if (s0 == 0 && !whole && tid == 0) *split = make_int4(b, pair, static_cast<int>((pair_first + n_tiles - 1) / share), 0);
+        float* ws = parts_at + (2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0)) * S::PART;
         const float* parts = reinterpret_cast<const float*>(smem);
         for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
             const int r = idx / (D / 4), d = idx % (D / 4) * 4;
@@ -661,88 +701,77 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
             }
         }
         __syncthreads();   // the ring and the fragments are written again
-        i0 = pair_first + s1;
     }
     flag_err(p.dev_err, bits);
 }
 
-// Adds the parts of pairs that several blocks shared; rows of sequences that see
-// nothing get zeros.  A block a (pair, row), its warps taking parts in turn.
+// Adds the parts of the pair that begins in block x and ends in another.  A block has
+// 8 rows, a warp each, or, where pairs are spread over many blocks, one row, its warps
+// taking parts in turn.
 constexpr int kJoinWarps = 8;
 
 template <int D, bool F8, int NR>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join(const __grid_constant__ AttnParams p, int row_blocks, int blocks) {
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join(const __grid_constant__ AttnParams p, int row_blocks, int by_row) {
     using S = Shape<D, F8, NR>;
     constexpr int PER = D / 32;   // dimensions of a lane
-    __shared__ int64_t scan_s[kJoinWarps + 1];
-    __shared__ int64_t before_s;
     __shared__ float m_s[kJoinWarps], l_s[kJoinWarps], o_s[kJoinWarps][D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     stream_order();
-    const int pairs = p.c.H * row_blocks, threads = kJoinWarps * 32;
-    const int b = blockIdx.x / pairs, pair = blockIdx.x % pairs, h = pair / row_blocks, row0 = pair % row_blocks * S::ROWS;
-    const int r = blockIdx.y;
-    if (row0 + r >= p.G * p.T) return;
-    int32_t bits = 0;
-    const int per = (p.B + threads - 1) / threads, sb0 = min(p.B, tid * per), sb1 = min(p.B, sb0 + per);
-    int64_t before = sum_tiles<S::WT, kJoinWarps * 32>(p, scan_s, sb0, sb1, &bits);
-    const int64_t total = scan_s[kJoinWarps] * pairs;
-    if (b >= sb0 && b < sb1) {
-        for (int i = sb0; i < b; ++i) before += tiles_of<S::WT>(seen_of(p, i, &bits));
-        before_s = before;
-    }
-    __syncthreads();
-    const int n = tiles_of<S::WT>(seen_of(p, b, &bits));
-    const int row = row0 + r, tk = row / p.G, hq = h * p.G + row % p.G;
-    const int64_t at = b * p.os[0] + tk * p.os[1] + hq * p.os[2];
-    if (n == 0) {
-        for (int d = tid; d < D; d += threads) st_out(p.out, at + d * p.os[3], p.o_dt, 0.f);
-        if (tid == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = -INFINITY;
-        return;
-    }
-    const int64_t share = share_of(total, blocks);
-    const int64_t first = before_s * pairs + static_cast<int64_t>(pair) * n;
-    const int64_t g0 = first / share, g1 = (first + n - 1) / share;
-    if (g0 == g1) return;   // one block had all of it
+    const int g0 = blockIdx.x;
+    const int4 split = reinterpret_cast<const int4*>(p.ws)[g0];
+    const int b = split.x, pair = split.y, g1 = split.z, h = pair / row_blocks, row0 = pair % row_blocks * S::ROWS;
+    const int r = by_row ? blockIdx.y : blockIdx.y * 8 + warp, row = row0 + r;
+    if (b < 0 || (by_row ? row : row0 + static_cast<int>(blockIdx.y) * 8) >= p.G * p.T) return;
+    const int step = by_row ? kJoinWarps : 1;
     float m = kNone, l = 0.f, o[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) o[k] = 0.f;
-    for (int64_t i = g0 + warp; i <= g1; i += kJoinWarps) {
-        const float* part = p.ws + (2 * i + (i == g0)) * S::PART;
-        const float pm = part[r], pl = part[S::ROWS + r];
-        float x[PER];
+    const float* const parts_at = p.ws + 4 * kMaxBlocks;
+    if (row < p.G * p.T) {
+        for (int i = g0 + (by_row ? warp : 0); i <= g1; i += step) {
+            const float* part = parts_at + (2 * static_cast<int64_t>(i) + (i == g0)) * S::PART;
+            const float pm = part[r], pl = part[S::ROWS + r];
+            float x[PER];
 #pragma unroll
-        for (int k = 0; k < PER; ++k) x[k] = part[2 * S::ROWS + r * D + lane + k * 32];
-        const float top = fmaxf(m, pm), a = exp2_f(m - top), c = exp2_f(pm - top);
-        l = fmaf(l, a, pl * c);
+            for (int k = 0; k < PER; ++k) x[k] = part[2 * S::ROWS + r * D + lane + k * 32];
+            const float top = fmaxf(m, pm), a = exp2_f(m - top), c = exp2_f(pm - top);
+            l = fmaf(l, a, pl * c);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) o[k] = fmaf(o[k], a, x[k] * c);
+            for (int k = 0; k < PER; ++k) o[k] = fmaf(o[k], a, x[k] * c);
+            m = top;
+        }
+    }
+    const int tk = row / p.G, hq = h * p.G + row % p.G;
+    const int64_t at = b * p.os[0] + tk * p.os[1] + hq * p.os[2];
+    if (by_row) {
+        if (lane == 0) {
+            m_s[warp] = m;
+            l_s[warp] = l;
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) o_s[warp][lane + k * 32] = o[k];
+        __syncthreads();
+        if (warp != 0) return;
+        float top = kNone;
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, m_s[w]);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) o[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f = exp2_f(m_s[w] - top);
+            l = fmaf(f, l_s[w], l);
+#pragma unroll
+            for (int k = 0; k < PER; ++k) o[k] = fmaf(f, o_s[w][lane + k * 32], o[k]);
+        }
         m = top;
     }
-    if (lane == 0) {
-        m_s[warp] = m;
-        l_s[warp] = l;
-    }
+    if (row >= p.G * p.T) return;
+    const float il = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) o_s[warp][lane + k * 32] = o[k];
-    __syncthreads();
-    float top = kNone, ls = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, m_s[w]);
-    float f[kJoinWarps];
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        f[w] = exp2_f(m_s[w] - top);
-        ls = fmaf(f[w], l_s[w], ls);
-    }
-    const float il = ls == 0.f ? 0.f : 1.f / ls;
-    for (int d = tid; d < D; d += threads) {
-        float y = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) y = fmaf(f[w], o_s[w][d], y);
-        st_out(p.out, at + d * p.os[3], p.o_dt, y * il);
-    }
-    if (tid == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = ls == 0.f ? -INFINITY : (top + log2f(ls)) * kLn2;
+    for (int k = 0; k < PER; ++k) st_out(p.out, at + (lane + k * 32) * p.os[3], p.o_dt, o[k] * il);
+    if (lane == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Tiles of 8 rows that a pair has: as many as its rows need, while registers hold their outputs
@@ -765,14 +794,15 @@ lar_status launch(const AttnParams& p, cudaStream_t stream) {
     if (pairs > (int64_t{1} << 31) - 1) return LAR_ERR_SHAPE;
     // no more blocks than the longest sequences that the table admits could fill
     const int64_t cap = static_cast<int64_t>(p.c.M) * p.c.page;
-    const int64_t most = (pairs * ((cap + S::WT - 1) / S::WT + 1) + kWarps - 1) / kWarps;
+    const int64_t most = (pairs * ((cap + S::WT - 1) / S::WT + 1 + kStart) + kWarps - 1) / kWarps;
     int64_t blocks = static_cast<int64_t>(sms) * occ;
     if (blocks > kMaxBlocks) blocks = kMaxBlocks;
     if (blocks > most) blocks = most;
     const lar_status st = launch_ordered(kern, dim3(static_cast<unsigned>(blocks)), kThreads, S::SMEM, 1, stream, p, row_blocks);
     if (st != LAR_OK) return st;
-    return launch_ordered(attn_join<D, F8, NR>, dim3(static_cast<unsigned>(pairs), S::ROWS), kJoinWarps * 32, 0, 1, stream, p,
-                          row_blocks, static_cast<int>(blocks));
+    const int by_row = blocks >= kJoinWarps * pairs;
+    return launch_ordered(attn_join<D, F8, NR>, dim3(static_cast<unsigned>(blocks), by_row ? S::ROWS : NR), kJoinWarps * 32, 0, 1,
+                          stream, p, row_blocks, by_row);
 }
 
 template <int D, bool F8>
@@ -793,7 +823,7 @@ lar_status launch_d(const AttnParams& p, cudaStream_t stream) {
 }  // namespace
 
 int64_t attn_workspace_floats(int T, int G, int D) {
-    return int64_t{2} * kMaxBlocks * 8 * row_tiles(T, G, D) * (D + 2);
+    return int64_t{4} * kMaxBlocks + int64_t{2} * kMaxBlocks * 8 * row_tiles(T, G, D) * (D + 2);
 }
 
 lar_status launch_attn(const AttnParams& p, void* stream) {

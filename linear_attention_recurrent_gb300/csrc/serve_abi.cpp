@@ -234,7 +234,8 @@ lar_status attn_decode(const lar_tensor* q, const lar_tensor* k_cache, const lar
     if (workspace->stride[0] != 1) return LAR_ERR_STRIDE;
     if (reinterpret_cast<uintptr_t>(workspace->data) % 16) return LAR_ERR_ALIGN;
     p.ws = static_cast<float*>(workspace->data);
-    p.q = q->data; p.q_dt = q->dtype;
+    p.q = q->data;
+    p.q_pairs = p.qs[3] == 1 && reinterpret_cast<uintptr_t>(q->data) % 4 == 0 && !((p.qs[0] | p.qs[1] | p.qs[2]) & 1);
     p.out = out->data; p.o_dt = out->dtype;
     p.scale = scale;
     p.window = window;

@@ -43,7 +43,8 @@ struct AppendParams {
 struct AttnParams {
     CacheParams c;
     int B, T, Hq, G;                                // G = Hq / H
-    const void* q; int64_t qs[4]; int q_dt;
+    const void* q; int64_t qs[4];                   // bf16
+    int q_pairs;                                    // 4-byte accesses of two dimensions fit q
     void* out; int64_t os[4]; int o_dt;
     float* lse; int64_t ls[3];                      // [B, T, Hq] or NULL
     float* ws;                                      // partial sums of blocks that share a pair
