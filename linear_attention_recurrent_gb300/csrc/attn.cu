@@ -56,6 +56,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kStart = LAR_ATTN_START;   // tiles that a pair's beginning and end count as
 constexpr float kSlack = 8.f;      // a weight may grow to 2^8 before the sums are scaled down
 
+#ifndef LAR_ATTN_QREG
+#define LAR_ATTN_QREG 256
+#endif
+#ifndef LAR_ATTN_BLOCKS2
+#define LAR_ATTN_BLOCKS2 2
+#endif
 #ifndef LAR_ATTN_TILE
 #define LAR_ATTN_TILE 8192
 #endif
@@ -88,8 +94,8 @@ struct Shape {
     static constexpr int JOIN = kWarps * PART * 4;
     static constexpr int BODY = kWarps * RING > JOIN ? kWarps * RING : JOIN;
     static constexpr int SMEM = BODY + QF + ROWS * 4;
-    static constexpr bool QREG = D * NR <= 256;        // fragments stay in registers
-    static constexpr int BLOCKS = D * NR <= 128 ? LAR_ATTN_BLOCKS : 2;   // an SM, by registers
+    static constexpr bool QREG = D * NR <= LAR_ATTN_QREG;        // fragments stay in registers
+    static constexpr int BLOCKS = D * NR <= 128 ? LAR_ATTN_BLOCKS : D * NR <= 256 ? LAR_ATTN_BLOCKS2 : 2;   // an SM, by registers
 };
 
 __device__ __forceinline__ void cp16_zfill(unsigned dst, const void* src, bool take) {
@@ -100,17 +106,9 @@ __device__ __forceinline__ void cp16(unsigned dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds16(unsigned a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-
-__device__ __forceinline__ uint2 lds8(unsigned a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
+// Plain loads, so that the compiler may ask for them early (never past a wait, which clobbers memory)
+__device__ __forceinline__ uint4 lds16(const unsigned char* a) { return *reinterpret_cast<const uint4*>(a); }
+__device__ __forceinline__ uint2 lds8(const unsigned char* a) { return *reinterpret_cast<const uint2*>(a); }
 
 // Where chunk c of a tile's row lies: the rows that a warp reads at once fall on
 // different banks.  Rows of 64 bytes share a line of 128 in pairs.
@@ -148,12 +146,12 @@ __device__ __forceinline__ unsigned turned(unsigned x) {
 template <bool F8>
 __device__ __forceinline__ void mma(float* d, const unsigned* a, unsigned b0, unsigned b1) {
     if constexpr (F8)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -214,7 +212,7 @@ __device__ __forceinline__ int64_t sum_weights(const AttnParams& p, int64_t* par
 }
 
 template <int D, bool F8, int NR>
-__global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_kernel(const __grid_constant__ AttnParams p, int row_blocks) {
+__global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_kernel(const __grid_constant__ AttnParams p, int row_blocks, int by_row) {
     using S = Shape<D, F8, NR>;
     constexpr int GR = S::GR, CH = S::CH;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -224,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
     unsigned char* qf = smem + S::BODY;
     float* qc = reinterpret_cast<float*>(qf + S::QF);   // what a row's products are multiplied by
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    const unsigned ring = static_cast<unsigned>(__cvta_generic_to_shared(smem)) + warp * S::RING;
+    unsigned char* const ring = smem + warp * S::RING;
+    const unsigned ring_a = static_cast<unsigned>(__cvta_generic_to_shared(ring));
     stream_order();
     int32_t bits = 0;
 
@@ -236,13 +235,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
     const int64_t share = share_of(total, gridDim.x);
     int64_t i0 = share * blockIdx.x;
     const int64_t i1 = min(total, i0 + share);
-    int4* split = reinterpret_cast<int4*>(p.ws) + blockIdx.x;   // the pair that begins here and ends in another block
+    // Pairs that end in another block than they begin in: one a block at most, or, where pairs
+    // are few, by pair.
+    int4* const split = reinterpret_cast<int4*>(p.ws);
     float* const parts_at = p.ws + 4 * kMaxBlocks;
-    if (tid == 0) *split = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !by_row) split[blockIdx.x].x = -1;
     // rows of sequences that see nothing
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const Seen seen = seen_of(p, b, &bits);
         if (seen.hi > seen.lo) continue;
+        if (by_row && tid < pairs) split[b * pairs + tid].x = -1;
         for (int i = tid; i < p.T * p.Hq * D; i += kThreads) {
             const int d = i % D, hq = i / D % p.Hq, tk = i / D / p.Hq;
             st_out(p.out, b * p.os[0] + tk * p.os[1] + hq * p.os[2] + d * p.os[3], p.o_dt, 0.f);
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
             if (i < mine) {
                 if (i > 0 && i % BT == 0) load_batch(i / BT);
                 const int pos = place_of(i);
-                const unsigned dst = ring + i % S::STAGES * (2 * S::TILE);
+                const unsigned dst = ring_a + i % S::STAGES * (2 * S::TILE);
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) {
                     const int src = i % BT * GR + gr, p0 = pos + gr * 16;
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
             cp_async_wait<S::STAGES - 2>();
             __syncwarp();
             load(i + S::STAGES - 1);
-            const unsigned kt = ring + i % S::STAGES * (2 * S::TILE), vt = kt + S::TILE;
+            const unsigned char *kt = ring + i % S::STAGES * (2 * S::TILE), *vt = kt + S::TILE;
             const int pos = place_of(i);
 
             float s[GR][NR][4];
@@ -665,7 +667,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
             }
         __syncthreads();
         const bool whole = s0 == 0 && s1 == n_tiles;
-        if (s0 == 0 && !whole && tid == 0) *split = make_int4(b, pair, static_cast<int>((pair_first + n_tiles - 1) / share), 0);
+        if (s0 == 0 && tid == 0 && (by_row || !whole))
+            split[by_row ? b * pairs + pair : blockIdx.x] =
+                make_int4(whole ? -1 : b, pair, static_cast<int>((pair_first + n_tiles - 1) / share), blockIdx.x);
         float* ws = parts_at + (2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0)) * S::PART;
         const float* parts = reinterpret_cast<const float*>(smem);
         for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
@@ -705,73 +709,95 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
     flag_err(p.dev_err, bits);
 }
 
-// Adds the parts of the pair that begins in block x and ends in another.  A block has
-// 8 rows, a warp each, or, where pairs are spread over many blocks, one row, its warps
-// taking parts in turn.
+// Adds the parts of a pair that begins in one block and ends in another.  A block has
+// 8 rows, a warp each, or, where pairs are spread over many blocks, 64 dimensions of one
+// row, its half-warps taking parts in turn.
 constexpr int kJoinWarps = 8;
+constexpr int kSlice = 64;
 
 template <int D, bool F8, int NR>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(const __grid_constant__ AttnParams p, int row_blocks, int by_row) {
     using S = Shape<D, F8, NR>;
-    constexpr int PER = D / 32;   // dimensions of a lane
-    __shared__ float m_s[kJoinWarps], l_s[kJoinWarps], o_s[kJoinWarps][D];
+    constexpr int GROUPS = kJoinWarps * 2;
+    __shared__ float top_s[kJoinWarps], sum_s[kJoinWarps], f_s[kMaxBlocks];
+    __shared__ float4 o_s[GROUPS][kSlice / 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     stream_order();
-    const int g0 = blockIdx.x;
-    const int4 split = reinterpret_cast<const int4*>(p.ws)[g0];
-    const int b = split.x, pair = split.y, g1 = split.z, h = pair / row_blocks, row0 = pair % row_blocks * S::ROWS;
+    const int4 split = reinterpret_cast<const int4*>(p.ws)[blockIdx.x];
+    const int b = split.x, pair = split.y, g1 = split.z, g0 = split.w, h = pair / row_blocks, row0 = pair % row_blocks * S::ROWS;
+    if (b < 0) return;
+    const float* const parts_at = p.ws + 4 * kMaxBlocks;
+    auto part_of = [&](int i) { return parts_at + (2 * static_cast<int64_t>(i) + (i == g0)) * S::PART; };
     const int r = by_row ? blockIdx.y : blockIdx.y * 8 + warp, row = row0 + r;
-    if (b < 0 || (by_row ? row : row0 + static_cast<int>(blockIdx.y) * 8) >= p.G * p.T) return;
-    const int step = by_row ? kJoinWarps : 1;
+    if (row >= p.G * p.T) return;   // a block's, or a warp's
+    const int tk = row / p.G, hq = h * p.G + row % p.G;
+    const int64_t at = b * p.os[0] + tk * p.os[1] + hq * p.os[2];
+    float* const lse = p.lse ? p.lse + b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2] : nullptr;
+    if (by_row) {
+        float m = kNone, l = 0.f;
+        for (int i = g0 + tid; i <= g1; i += kJoinWarps * 32) m = fmaxf(m, part_of(i)[r]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (lane == 0) top_s[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, top_s[w]);
+        for (int i = g0 + tid; i <= g1; i += kJoinWarps * 32) {
+            const float* part = part_of(i);
+            const float f = exp2_f(part[r] - m);
+            f_s[i - g0] = f;
+            l = fmaf(f, part[S::ROWS + r], l);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (lane == 0) sum_s[warp] = l;
+        __syncthreads();
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) l += sum_s[w];
+        const int grp = tid / (kSlice / 4), q = tid % (kSlice / 4), d = blockIdx.z * kSlice + q * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = g0 + grp; i <= g1; i += GROUPS) {
+            const float4 x = *reinterpret_cast<const float4*>(part_of(i) + 2 * S::ROWS + r * D + d);
+            const float f = f_s[i - g0];
+            acc.x = fmaf(f, x.x, acc.x);
+            acc.y = fmaf(f, x.y, acc.y);
+            acc.z = fmaf(f, x.z, acc.z);
+            acc.w = fmaf(f, x.w, acc.w);
+        }
+        o_s[grp][q] = acc;
+        __syncthreads();
+        if (tid < kSlice) {
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < GROUPS; ++w) y += reinterpret_cast<const float*>(o_s[w])[tid];
+            st_out(p.out, at + (blockIdx.z * kSlice + tid) * p.os[3], p.o_dt, y * (l == 0.f ? 0.f : 1.f / l));
+        }
+        if (tid == 0 && blockIdx.z == 0 && lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        return;
+    }
+    constexpr int PER = D / 32;   // dimensions of a lane
     float m = kNone, l = 0.f, o[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) o[k] = 0.f;
-    const float* const parts_at = p.ws + 4 * kMaxBlocks;
-    if (row < p.G * p.T) {
-        for (int i = g0 + (by_row ? warp : 0); i <= g1; i += step) {
-            const float* part = parts_at + (2 * static_cast<int64_t>(i) + (i == g0)) * S::PART;
-            const float pm = part[r], pl = part[S::ROWS + r];
-            float x[PER];
+#pragma unroll 2
+    for (int i = g0; i <= g1; ++i) {
+        const float* part = part_of(i);
+        const float pm = part[r], pl = part[S::ROWS + r];
+        float x[PER];
 #pragma unroll
-            for (int k = 0; k < PER; ++k) x[k] = part[2 * S::ROWS + r * D + lane + k * 32];
-            const float top = fmaxf(m, pm), a = exp2_f(m - top), c = exp2_f(pm - top);
-            l = fmaf(l, a, pl * c);
+        for (int k = 0; k < PER; ++k) x[k] = part[2 * S::ROWS + r * D + lane + k * 32];
+        const float top = fmaxf(m, pm), a = exp2_f(m - top), c = exp2_f(pm - top);
+        l = fmaf(l, a, pl * c);
 #pragma unroll
-            for (int k = 0; k < PER; ++k) o[k] = fmaf(o[k], a, x[k] * c);
-            m = top;
-        }
-    }
-    const int tk = row / p.G, hq = h * p.G + row % p.G;
-    const int64_t at = b * p.os[0] + tk * p.os[1] + hq * p.os[2];
-    if (by_row) {
-        if (lane == 0) {
-            m_s[warp] = m;
-            l_s[warp] = l;
-        }
-#pragma unroll
-        for (int k = 0; k < PER; ++k) o_s[warp][lane + k * 32] = o[k];
-        __syncthreads();
-        if (warp != 0) return;
-        float top = kNone;
-        l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, m_s[w]);
-#pragma unroll
-        for (int k = 0; k < PER; ++k) o[k] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-            const float f = exp2_f(m_s[w] - top);
-            l = fmaf(f, l_s[w], l);
-#pragma unroll
-            for (int k = 0; k < PER; ++k) o[k] = fmaf(f, o_s[w][lane + k * 32], o[k]);
-        }
+        for (int k = 0; k < PER; ++k) o[k] = fmaf(o[k], a, x[k] * c);
         m = top;
     }
-    if (row >= p.G * p.T) return;
     const float il = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int k = 0; k < PER; ++k) st_out(p.out, at + (lane + k * 32) * p.os[3], p.o_dt, o[k] * il);
-    if (lane == 0 && p.lse) p.lse[b * p.ls[0] + tk * p.ls[1] + hq * p.ls[2]] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (lane == 0 && lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Tiles of 8 rows that a pair has: as many as its rows need, while registers hold their outputs
@@ -798,10 +824,10 @@ lar_status launch(const AttnParams& p, cudaStream_t stream) {
     int64_t blocks = static_cast<int64_t>(sms) * occ;
     if (blocks > kMaxBlocks) blocks = kMaxBlocks;
     if (blocks > most) blocks = most;
-    const lar_status st = launch_ordered(kern, dim3(static_cast<unsigned>(blocks)), kThreads, S::SMEM, 1, stream, p, row_blocks);
-    if (st != LAR_OK) return st;
     const int by_row = blocks >= kJoinWarps * pairs;
-    return launch_ordered(attn_join<D, F8, NR>, dim3(static_cast<unsigned>(blocks), by_row ? S::ROWS : NR), kJoinWarps * 32, 0, 1,
+    const lar_status st = launch_ordered(kern, dim3(static_cast<unsigned>(blocks)), kThreads, S::SMEM, 1, stream, p, row_blocks, by_row);
+    if (st != LAR_OK) return st;
+    return launch_ordered(attn_join<D, F8, NR>, dim3(static_cast<unsigned>(by_row ? pairs : blocks), by_row ? S::ROWS : NR, by_row ? D / kSlice : 1), kJoinWarps * 32, 0, 1,
                           stream, p, row_blocks, by_row);
 }
 
