@@ -9,25 +9,37 @@
 // from a table of 32 steps, and the rest, at most 1/64, from a polynomial: good to 2^-30 of
 // the weight, or 2^-40 of the greatest.
 //
-// Thresholds.  The key at which a prefix has k tokens, or p of the weight, is found 11 bits
-// at a time: sums a bin in shared memory, added over the blocks of a cluster.  Ties at the
-// threshold are kept from the lowest index on.
-//
-// A row is a cluster's, every warp owning a contiguous stretch of the vocabulary.
+// Work.  A row is a cluster's, every warp owning a contiguous stretch of the vocabulary.
+// One pass finds the greatest logit.  Then
+//   top-k: the k-th of the threads' own maxima is a bound that k logits reach, and hardly
+//     more (1.4 k where k is half as many as the threads are); the logits from it on go to
+//     one block, which finds all cuts, and the token, among them.
+//   top-p alone: the weights are added up in bins of their exponent, 11 bits at once; the
+//     logits of the one bin that the cut falls into go to one block.
+//   neither: the weights of each warp's stretch are added up.
+// Where no list is left, the warp whose stretch holds the threshold reads it again.  Lists
+// that grow past their room (equal logits, sorted ones) are replaced by passes over the
+// row that narrow the key down 11 bits at a time.  Ties at a cut are kept from the lowest
+// index on.
+#include <type_traits>
+
 #include "layer_common.cuh"
 #include "serve_params.h"
 
 namespace lar {
 
+int cached_occupancy(const void* kern, int threads, size_t smem, size_t smem_max, int* sms_out);
+
 namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kStep = 256;       // tokens of a warp's step, 8 a lane
 constexpr int kBits = 11;        // of a key, looked at in one go
+constexpr int kList = 2048;      // room for logits around a cut
 constexpr int kBins = 1 << kBits;
 constexpr u64 kOne = 1ull << 39;  // weight of the greatest logit
 
@@ -139,12 +151,20 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
     return v;
 }
 
+// A logit of a list: greater first, lower indices first
+__device__ __forceinline__ u64 entry_of(unsigned key, int i) { return static_cast<u64>(key) << 32 | (0xffffffffu - static_cast<unsigned>(i)); }
+__device__ __forceinline__ unsigned entry_key(u64 e) { return static_cast<unsigned>(e >> 32); }
+__device__ __forceinline__ int entry_index(u64 e) { return static_cast<int>(0xffffffffu - static_cast<unsigned>(e)); }
+
 struct Shared {
     u64 pow[32];
     u64 warp[kWarps];
-    u64 peer[2][2][kMaxCluster];   // exchanges in turn; two values each
+    u64 peer[2][kMaxCluster];      // exchanges in turn
     u64 found[4];
+    u64 list[kList], all[kList];   // this block's, and in block 0 the cluster's
     unsigned lo[kBins], hi[kBins];
+    unsigned maxima[kMaxCluster * kThreads];   // block 0: of the cluster's threads
+    unsigned count;
     float scale_hi, scale_lo;
 };
 
@@ -154,44 +174,154 @@ struct Block {
     int tid, lane, warp;
     int turn = 0;
 
-    // Sum (or greatest) of every thread's v over the cluster, and of the ranks before this
-    // block; warp sums stay in s.warp.
-    __device__ __forceinline__ u64 sum(u64 v, u64* before) {
-        v = warp_sum(v);
-        __syncthreads();   // s.warp is read no more
+    template <typename F>
+    __device__ __forceinline__ u64 over(u64 v, u64 start, F join, u64* before) {
         if (lane == 0) s.warp[warp] = v;
         __syncthreads();
         if (warp == 0) {
-            const u64 own = warp_sum(lane < kWarps ? s.warp[lane] : 0ull);
-            if (lane < size) st_peer_u64(&s.peer[turn][0][rank], lane, own);
+            u64 own = lane < kWarps ? s.warp[lane] : start;
+#pragma unroll
+            for (int off = kWarps / 2; off > 0; off >>= 1) own = join(own, __shfl_xor_sync(0xffffffffu, own, off));
+            if (lane < size) st_peer_u64(&s.peer[turn][rank], lane, own);
         }
         __syncwarp();
         cluster_sync();
-        u64 all = 0, b = 0;
+        u64 all = start, b = start;
         for (unsigned r = 0; r < size; ++r) {
             if (r == rank) b = all;
-            all += s.peer[turn][0][r];
+            all = join(all, s.peer[turn][r]);
         }
         turn ^= 1;
         if (before) *before = b;
         return all;
     }
 
+    // Sum of every thread's v over the cluster, and of the ranks before this block; the warps'
+    // sums stay in s.warp.
+    __device__ __forceinline__ u64 sum(u64 v, u64* before) {
+        v = warp_sum(v);
+        __syncthreads();   // s.warp is read no more
+        return over(v, 0ull, [](u64 a, u64 b) { return a + b; }, before);
+    }
+
     __device__ __forceinline__ u64 greatest(u64 v) {
         v = warp_max(v);
         __syncthreads();
+        return over(v, 0ull, [](u64 a, u64 b) { return a > b ? a : b; }, nullptr);
+    }
+
+    // The same over this block alone
+    __device__ __forceinline__ u64 own_sum(u64 v) {
+        v = warp_sum(v);
+        __syncthreads();
         if (lane == 0) s.warp[warp] = v;
         __syncthreads();
-        if (warp == 0) {
-            const u64 own = warp_max(lane < kWarps ? s.warp[lane] : 0ull);
-            if (lane < size) st_peer_u64(&s.peer[turn][0][rank], lane, own);
+        u64 all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) all += s.warp[w];
+        return all;
+    }
+
+    // A bin's share of a sum
+    __device__ __forceinline__ void add(unsigned bin, u64 w) {
+        const unsigned wl = static_cast<unsigned>(w), old = atomicAdd(&s.lo[bin], wl);
+        const unsigned wh = static_cast<unsigned>(w >> 32) + (old + wl < old ? 1u : 0u);
+        if (wh) atomicAdd(&s.hi[bin], wh);
+    }
+
+    __device__ __forceinline__ void clear_bins() {
+        for (int i = tid; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
+        __syncthreads();
+    }
+
+    // The highest bin down to which the bins' sums reach `target`, in s.found: bin, the sum
+    // above it, its own.  CL: bins of all the cluster's blocks, to all of them.
+    template <bool CL>
+    __device__ __forceinline__ void find_bin(u64 target) {
+        const unsigned n = CL ? size : 1, me = CL ? rank : 0;
+        if (CL) {
+            __syncwarp();
+            cluster_sync();
+        } else {
+            __syncthreads();
+        }
+        const int slice = kBins / static_cast<int>(n), per = slice / kThreads > 0 ? slice / kThreads : 1;
+        const int base = kBins - 1 - static_cast<int>(me) * slice;   // this block's highest bin
+        u64 bins[kBins / kThreads];
+        u64 mine = 0;
+#pragma unroll
+        for (int e = 0; e < kBins / kThreads; ++e) {
+            bins[e] = 0;
+            const int q = tid * per + e;
+            if (e < per && q < slice) {
+                if (CL) {
+                    for (unsigned r = 0; r < n; ++r) {
+                        unsigned l, h;
+                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(l) : "r"(peer_addr(&s.lo[base - q], r)));
+                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h) : "r"(peer_addr(&s.hi[base - q], r)));
+                        bins[e] += static_cast<u64>(h) << 32 | l;
+                    }
+                } else {
+                    bins[e] = static_cast<u64>(s.hi[base - q]) << 32 | s.lo[base - q];
+                }
+            }
+            mine += bins[e];
+        }
+        u64 run = 0;
+        if (CL) sum(mine, &run);
+        else own_sum(mine);
+        for (int w = 0; w < warp; ++w) run += s.warp[w];
+        run += warp_scan(mine, lane) - mine;
+        if (run < target && run + mine >= target) {   // one thread
+            int at = -1;
+            u64 got = 0;
+#pragma unroll
+            for (int e = 0; e < kBins / kThreads; ++e)
+                if (at < 0) {
+                    if (run + bins[e] >= target) {
+                        at = e;
+                        got = bins[e];
+                    } else {
+                        run += bins[e];
+                    }
+                }
+            for (unsigned r = 0; r < n; ++r) {
+                const unsigned to = CL ? r : rank;
+                st_peer_u64(&s.found[1], to, static_cast<u64>(base - tid * per - at));
+                st_peer_u64(&s.found[2], to, run);
+                st_peer_u64(&s.found[3], to, got);
+            }
         }
         __syncwarp();
-        cluster_sync();
-        u64 all = 0;
-        for (unsigned r = 0; r < size; ++r) all = max(all, s.peer[turn][0][r]);
-        turn ^= 1;
-        return all;
+        if (CL) cluster_sync();
+        else __syncthreads();
+    }
+
+    // The greatest key in [lo, hi] down to which the sums of f reach `target` (which they do):
+    // s.found[2] is the sum above it, s.found[3] its own.  each(g) calls g(key, i, x) for
+    // the values in question.
+    template <bool CL, typename E, typename F>
+    __device__ __forceinline__ unsigned find_key(unsigned lo, unsigned hi, u64 target, E each, F f) {
+        u64 above = 0;
+        while (true) {
+            int shift = 0;
+            while (((hi - lo) >> shift) >= kBins) ++shift;
+            clear_bins();
+            each([&](unsigned key, int i, float x) {
+                if (key < lo || key > hi) return;
+                const u64 w = f(key, i, x);
+                if (w) add((key - lo) >> shift, w);
+            });
+            find_bin<CL>(target - above);
+            above += s.found[2];
+            lo += static_cast<unsigned>(s.found[1]) << shift;
+            hi = lo + min(hi - lo, (1u << shift) - 1);
+            if (shift == 0) break;
+        }
+        __syncthreads();
+        if (tid == 0) s.found[2] = above;
+        __syncthreads();
+        return lo;
     }
 };
 
@@ -225,12 +355,14 @@ __device__ __forceinline__ u64 part_of(float u, u64 T) {
     return whole + (UP && rest ? 1u : 0u);
 }
 
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p) {
-    __shared__ Shared s;
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_constant__ SampleParams p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    Shared& s = *reinterpret_cast<Shared*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Block c{s, cluster_rank(), cluster_size(), tid, lane, warp};
     cluster_arrive();
     if (tid < 32) s.pow[tid] = kPow[tid];
+    if (tid == 0) s.count = 0;
     stream_order();
     const int b = blockIdx.y / p.T, t = blockIdx.y % p.T;
     Row row;
@@ -247,29 +379,25 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         for (int st = s0; st < s1; ++st) row.eight(st * kStep + lane * 8, f);
     };
 
-    // the greatest logit and its lowest index, and how many are above -infinity
-    u64 top = 0;
-    unsigned some = 0;
-    each([&](int i, float x) {
-        const u64 v = static_cast<u64>(key_of(x)) << 32 | (0xffffffffu - static_cast<unsigned>(i));
-        top = v > top ? v : top;
-        some += x > -INFINITY;
-    });
-    cluster_wait();   // every block runs: its memory may be written
-    top = c.greatest(top);
-    const u64 N = c.sum(some, nullptr);
-    const int first = static_cast<int>(0xffffffffu - static_cast<unsigned>(top));
-    const unsigned top_key = static_cast<unsigned>(top >> 32);
-    const float greatest = of_key(top_key);
-
     const float temp = p.temp ? __ldg(p.temp + b * p.temp_s) : 1.f;
     const float top_p = p.top_p ? __ldg(p.top_p + b * p.tp_s) : 1.f;
     const float min_p = p.min_p ? __ldg(p.min_p + b * p.mp_s) : 0.f;
     int64_t k = p.top_k ? ld_idx(p.top_k, b * p.tk_s, p.tk_dt) : 0;
-    if (k < 0) k = 0;
+    if (k < 0 || k >= row.V) k = 0;
     const float u = __ldg(p.u + b * p.us[0] + t * p.us[1]);
-    const bool none = N == 0;
     const bool single = !(temp > 0.f) || k == 1 || !(top_p > 0.f) || min_p > 1.f;
+    const bool by_k = k > 0 && !single;
+
+    // the greatest logit
+    float most = -INFINITY;
+#pragma unroll 4
+    for (int st = s0; st < s1; ++st) row.eight(st * kStep + lane * 8, [&](int, float x) { most = fmaxf(most, x); });
+    cluster_wait();   // every block runs: its memory may be written
+    if (by_k)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(&s.maxima[c.rank * kThreads + tid], 0)), "r"(key_of(most)) : "memory");
+    const unsigned top_key = static_cast<unsigned>(c.greatest(key_of(most)));
+    const float greatest = of_key(top_key);
+    const bool none = top_key == kLeast;
 
     auto put = [&](int64_t v) {
         const int64_t o = b * p.ts[0] + t * p.ts[1];
@@ -281,16 +409,21 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         if (!p.probs) return;
         float* out = p.probs + b * p.ps[0] + t * p.ps[1];
         const int lo = max(0, s0 * kStep - row.off), hi = min(row.V, s1 * kStep - row.off);
+#pragma unroll 4
         for (int i = lo + lane; i < hi; i += 32) out[i * p.ps[2]] = f(i);
     };
     if (none || single) {
+        int first = row.V;
+        if (!none) {
+            each([&](int i, float x) { if (x == greatest) first = min(first, i); });
+            first = static_cast<int>(0xffffffffu - static_cast<unsigned>(c.greatest(0xffffffffu - static_cast<unsigned>(first))));
+        }
         if (c.rank == 0 && tid == 0) {
             put(none ? -1 : first);
             if (none) flag_err(p.dev_err, LAR_DEVERR_PROBS);
         }
         put_probs([&](int i) { return !none && i == first ? 1.f : 0.f; });
-        cluster_sync();   // no block leaves while another may still write to it
-        return;
+        return;   // every exchange is behind a barrier that all have passed
     }
 
     if (tid == 0) {
@@ -304,26 +437,195 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     sc.hi = s.scale_hi;
     sc.lo = s.scale_lo;
     sc.infinite = greatest == INFINITY;
+    const u64 least = min_p > 0.f ? part_of<true>(min_p, kOne) : 0ull;
 
-    Cut cut = {kLeast, row.V};   // keep everything above -infinity (its weight is 0)
+    Cut cut = {kLeast, row.V};   // everything above -infinity (whose weight is 0)
     auto kept = [&](int i, unsigned key) { return key > cut.key || (key == cut.key && i < cut.limit); };
+    auto weight = [&](int i, float x) {   // of the draw
+        if (!kept(i, key_of(x))) return u64{0};
+        const u64 w = sc.weight(x, s.pow);
+        return w >= least ? w : u64{0};
+    };
+    auto of_row = [&](auto g) {
+        each([&](int i, float x) {
+            const unsigned key = key_of(x);
+            if (kept(i, key)) g(key, i, x);
+        });
+    };
+    const auto one = [](unsigned, int, float) { return u64{1}; };
+    const auto by_weight = [&](unsigned, int, float x) { return sc.weight(x, s.pow); };
 
-    // The first index (in order) with  sum of f up to it > target;  in s.found[0] of every block.
-    auto select = [&](u64 before, u64 target, auto f) {
-        // s.warp holds this block's warp sums of f, `before` the sum of the blocks before
-        if (tid == 0) s.found[0] = ~0ull;
-        u64 start = before;
-        for (int w = 0; w < warp; ++w) start += s.warp[w];
-        const u64 own = s.warp[warp];
+    // Logits that `want` says go into this block's list; how many the cluster's blocks have,
+    // and, if they all fit, they are in block 0's s.all (after a barrier).
+    auto collect = [&](auto want) {
+        each([&](int i, float x) {
+            const unsigned key = key_of(x);
+            if (!want(key, i, x)) return;
+            const unsigned at = atomicAdd(&s.count, 1u);
+            if (at < kList) s.list[at] = entry_of(key, i);
+        });
+        __syncthreads();
+        const unsigned mine = s.count;
+        u64 before;
+        const u64 n = c.sum(tid == 0 ? mine : 0u, &before);
+        if (n <= kList)
+            for (unsigned i = tid; i < mine; i += kThreads) st_peer_u64(&s.all[before + i], 0, s.list[i]);
+        __syncwarp();
         cluster_sync();
-        if (start <= target && target < start + own) {   // one warp of the cluster
+        return n;
+    };
+    u64 n_list = 0;
+    auto of_list = [&](auto g) {
+        for (unsigned i = tid; i < n_list; i += kThreads) {
+            const unsigned key = entry_key(s.all[i]);
+            const int at = entry_index(s.all[i]);
+            if (kept(at, key)) g(key, at, of_key(key));
+        }
+    };
+    // The cut behind the first values whose sum of f reaches `target`, each() holding all down to it.
+    auto cut_by = [&](auto cl, u64 target, auto each_of, auto f) {
+        constexpr bool CL = decltype(cl)::value;
+        const unsigned key = c.template find_key<CL>(cut.key, top_key, target, each_of, f);
+        const u64 above = s.found[2], at = s.found[3], w1 = f(key, 0, of_key(key));
+        const u64 n = (target - above + w1 - 1) / w1;   // of the equal ones, this many
+        int limit = cut.key == key ? cut.limit : row.V;
+        __syncthreads();
+        if (n * w1 < at) {
+            const unsigned last = c.template find_key<CL>(
+                0xffffffffu - static_cast<unsigned>(row.V), 0xffffffffu, n,
+                [&](auto g) { each_of([&](unsigned q, int i, float x) { if (q == key) g(0xffffffffu - static_cast<unsigned>(i), i, x); }); }, one);
+            limit = static_cast<int>(0xffffffffu - last) + 1;
+        }
+        cut = {key, limit};
+    };
+    using Whole = std::true_type;
+    using Alone = std::false_type;
+
+    u64 total = 0;
+    bool drawn = false;
+    u64 mine = 0;
+    bool summed = false;
+    if (by_k) {
+        unsigned bound = kLeast;
+        if (k <= static_cast<int64_t>(c.size) * kThreads) {
+            if (c.rank == 0) {
+                const unsigned n = c.size * kThreads;
+                bound = c.template find_key<false>(kLeast, top_key, static_cast<u64>(k),
+                                                   [&](auto g) { for (unsigned i = tid; i < n; i += kThreads) g(s.maxima[i], 0, 0.f); }, one);
+                if (tid < static_cast<int>(c.size)) st_peer_u64(&s.found[0], tid, bound);
+            }
+            __syncwarp();
+            cluster_sync();
+            bound = static_cast<unsigned>(s.found[0]);
+        }
+        n_list = bound == kLeast && row.V > kList ? kList + 1 : collect([&](unsigned key, int, float) { return key >= bound; });
+        if (n_list <= kList) {
+            if (c.rank == 0) {
+                cut_by(Alone{}, static_cast<u64>(k), of_list, one);
+                if (top_p < 1.f) {
+                    u64 w = 0;
+                    of_list([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });
+                    cut_by(Alone{}, part_of<true>(top_p, c.own_sum(w)), of_list, by_weight);
+                }
+                u64 w = 0;
+                of_list([&](unsigned, int i, float x) { w += weight(i, x); });
+                total = c.own_sum(w);
+                u64 target = part_of<false>(u, total);
+                if (target >= total) target = total - 1;
+                const unsigned at = c.template find_key<false>(
+                    0xffffffffu - static_cast<unsigned>(row.V), 0xffffffffu, target + 1,
+                    [&](auto g) { of_list([&](unsigned, int i, float x) { g(0xffffffffu - static_cast<unsigned>(i), i, x); }); },
+                    [&](unsigned, int i, float x) { return weight(i, x); });
+                if (tid == 0) put(static_cast<int64_t>(0xffffffffu - at));
+                if (p.probs) {
+                    if (tid < static_cast<int>(c.size)) {
+                        st_peer_u64(&s.found[0], tid, static_cast<u64>(cut.key) << 32 | static_cast<unsigned>(cut.limit));
+                        st_peer_u64(&s.found[1], tid, total);
+                    }
+                    __syncwarp();
+                }
+            }
+            drawn = true;
+            if (p.probs) {
+                __syncwarp();
+                cluster_sync();
+                cut = {static_cast<unsigned>(s.found[0] >> 32), static_cast<int>(static_cast<unsigned>(s.found[0]))};
+                total = s.found[1];
+            }
+        } else {
+            cut_by(Whole{}, static_cast<u64>(k), of_row, one);
+        }
+    }
+    if (!drawn && top_p < 1.f) {
+        bool done = false;
+        if (!by_k) {
+            // bins of the exponent, from 0 at the greatest (the highest bin) to -42
+            auto bin_of = [&](float x) {
+                if (0.5f * x == sc.half_max) return kBins - 1;
+                float y, e;
+                sc.exponent(x, y, e);
+                return y >= -42.f ? kBins - 1 - static_cast<int>(y * (-kBins / 42.01f)) : -1;
+            };
+            c.clear_bins();
+            u64 w = 0;
+            each([&](int, float x) {
+                const u64 v = sc.weight(x, s.pow);
+                if (v) c.add(static_cast<unsigned>(bin_of(x)), v);
+                w += v;
+            });
+            const u64 all = c.sum(w, nullptr), target = part_of<true>(top_p, all);
+            c.template find_bin<true>(target);
+            const int bin = static_cast<int>(s.found[1]);
+            const u64 above = s.found[2];
+            __syncthreads();
+            n_list = collect([&](unsigned, int i, float x) {
+                const int q = bin_of(x);
+                if (q > bin) {
+                    const u64 v = sc.weight(x, s.pow);
+                    mine += v >= least ? v : 0;
+                }
+                return q == bin;
+            });
+            if (n_list <= kList) {
+                if (c.rank == 0) {
+                    cut_by(Alone{}, target - above, of_list, by_weight);
+                    if (tid < static_cast<int>(c.size))
+                        st_peer_u64(&s.found[0], tid, static_cast<u64>(cut.key) << 32 | static_cast<unsigned>(cut.limit));
+                }
+                __syncwarp();
+                cluster_sync();
+                cut = {static_cast<unsigned>(s.found[0] >> 32), static_cast<int>(static_cast<unsigned>(s.found[0]))};
+                // each warp its own of the list's
+                for (unsigned i = lane; i < s.count; i += 32) {
+                    const int at = entry_index(s.list[i]), st = (at + row.off) / kStep;
+                    if (st >= s0 && st < s1) mine += weight(at, of_key(entry_key(s.list[i])));
+                }
+                done = summed = true;
+            }
+        }
+        if (!done) {
+            mine = 0;
+            u64 w = 0;
+            of_row([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });
+            const u64 all = c.sum(w, nullptr);
+            cut_by(Whole{}, part_of<true>(top_p, all), of_row, by_weight);
+        }
+    }
+    if (!drawn) {
+        if (!summed) each([&](int i, float x) { mine += weight(i, x); });
+        u64 start;
+        total = c.sum(mine, &start);
+        u64 target = part_of<false>(u, total);
+        if (target >= total) target = total - 1;
+        for (int w = 0; w < warp; ++w) start += s.warp[w];
+        if (start <= target && target < start + s.warp[warp]) {   // one warp of the cluster
             for (int st = s0; st < s1; ++st) {
                 u64 w8[8];
                 int idx = -1;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w8[e] = 0;
                 const int i0 = st * kStep + lane * 8 - row.off;
-                row.eight(st * kStep + lane * 8, [&](int i, float x) { w8[i - i0] = f(i, x); });
+                row.eight(st * kStep + lane * 8, [&](int i, float x) { w8[i - i0] = weight(i, x); });
                 u64 sum8 = 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum8 += w8[e];
@@ -337,121 +639,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                 const unsigned has = __ballot_sync(0xffffffffu, idx >= 0);
                 if (has) {
                     idx = __shfl_sync(0xffffffffu, idx, __ffs(has) - 1);
-                    if (lane < c.size) st_peer_u64(&s.found[0], lane, static_cast<u64>(idx));
+                    if (lane == 0) put(idx);
                     break;
                 }
                 start += __shfl_sync(0xffffffffu, incl, 31);
             }
         }
-        __syncwarp();
-        cluster_sync();
-    };
-
-    // The cut at which the sum of f over a prefix reaches `target` (which the whole sum
-    // does); `each_is` is what a token with the cut's own key adds.
-    auto find_cut = [&](u64 target, auto f, auto of_one) {
-        unsigned lo = cut.key, hi = top_key;
-        u64 above = 0, at = 0;
-        while (true) {
-            int shift = 0;
-            while (((hi - lo) >> shift) >= kBins) ++shift;
-            for (int i = tid; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
-            __syncthreads();
-            each([&](int i, float x) {
-                const unsigned key = key_of(x);
-                if (key < lo || key > hi || !kept(i, key)) return;
-                const u64 w = f(x);
-                if (w == 0) return;
-                const unsigned bin = (key - lo) >> shift, wl = static_cast<unsigned>(w);
-                const unsigned old = atomicAdd(&s.lo[bin], wl);
-                const unsigned wh = static_cast<unsigned>(w >> 32) + (old + wl < old ? 1u : 0u);
-                if (wh) atomicAdd(&s.hi[bin], wh);
-            });
-            __syncwarp();
-            cluster_sync();
-            // this block's bins, from the top: a thread `per` of them
-            const int slice = kBins / static_cast<int>(c.size), per = (slice + kThreads - 1) / kThreads;
-            const int base = kBins - 1 - static_cast<int>(c.rank) * slice;   // its highest bin
-            u64 bins[kBins / kThreads];
-            u64 mine = 0;
-#pragma unroll
-            for (int e = 0; e < kBins / kThreads; ++e) {
-                bins[e] = 0;
-                const int q = tid * per + e;
-                if (e < per && q < slice) {
-                    for (unsigned r = 0; r < c.size; ++r) {
-                        unsigned l, h;
-                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(l) : "r"(peer_addr(&s.lo[base - q], r)));
-                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h) : "r"(peer_addr(&s.hi[base - q], r)));
-                        bins[e] += static_cast<u64>(h) << 32 | l;
-                    }
-                }
-                mine += bins[e];
-            }
-            u64 before;
-            c.sum(mine, &before);
-            u64 run = above + before;
-            for (int w = 0; w < warp; ++w) run += s.warp[w];
-            run += warp_scan(mine, lane) - mine;
-            if (run < target && run + mine >= target) {   // one thread of the cluster
-                int e = 0;
-                while (run + bins[e] < target) run += bins[e++];
-                u64 got = 0;
-#pragma unroll
-                for (int q = 0; q < kBins / kThreads; ++q)
-                    if (q == e) got = bins[q];
-                for (unsigned r = 0; r < c.size; ++r) {
-                    st_peer_u64(&s.found[1], r, static_cast<u64>(base - tid * per - e));
-                    st_peer_u64(&s.found[2], r, run);
-                    st_peer_u64(&s.found[3], r, got);
-                }
-            }
-            __syncwarp();
-            cluster_sync();
-            above = s.found[2];
-            at = s.found[3];
-            lo += static_cast<unsigned>(s.found[1]) << shift;
-            hi = min(hi, lo + ((1u << shift) - 1));
-            if (shift == 0) break;
-        }
-        const u64 one = of_one(of_key(lo));
-        const u64 n = (target - above + one - 1) / one;   // ties kept
-        int limit = cut.key == lo ? cut.limit : row.V;
-        if (n * one < at) {   // not all: the index behind the n-th
-            unsigned same = 0;
-            each([&](int i, float x) { same += key_of(x) == lo && i < limit; });
-            u64 before;
-            c.sum(same, &before);
-            const int lim = limit;
-            select(before, n - 1, [&](int i, float x) { return static_cast<u64>(key_of(x) == lo && i < lim); });
-            limit = static_cast<int>(s.found[0]) + 1;
-        }
-        cut = {lo, limit};
-    };
-
-    if (k > 0 && static_cast<u64>(k) < N)
-        find_cut(static_cast<u64>(k), [](float) { return 1ull; }, [](float) { return 1ull; });
-    if (top_p < 1.f) {
-        u64 mine = 0;
-        each([&](int i, float x) { if (kept(i, key_of(x))) mine += sc.weight(x, s.pow); });
-        const u64 all = c.sum(mine, nullptr);
-        const u64 target = part_of<true>(top_p, all);
-        find_cut(target, [&](float x) { return sc.weight(x, s.pow); }, [&](float x) { return sc.weight(x, s.pow); });
     }
-    const u64 least = min_p > 0.f ? part_of<true>(min_p, kOne) : 0ull;
-
-    auto weight = [&](int i, float x) {
-        if (!kept(i, key_of(x))) return u64{0};
-        const u64 w = sc.weight(x, s.pow);
-        return w >= least ? w : u64{0};
-    };
-    u64 mine = 0, before;
-    each([&](int i, float x) { mine += weight(i, x); });
-    const u64 total = c.sum(mine, &before);
-    u64 target = part_of<false>(u, total);
-    if (target >= total) target = total - 1;
-    select(before, target, weight);
-    if (c.rank == 0 && tid == 0) put(static_cast<int64_t>(s.found[0]));
     if (p.probs) {
         const float inv = 1.f / (static_cast<float>(total) * 0x1p-39f);
         put_probs([&](int i) {
@@ -469,15 +663,20 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 }  // namespace
 
 lar_status launch_sample(const SampleParams& p, void* stream) {
-    // a block a few thousand tokens, at most 8 (the portable cluster)
+    // a block a few thousand tokens, at most 8 (the portable cluster), and no more blocks
+    // than the device holds at once while rows are long enough to make up for that
+    int sms = 0;
+    const int occ = cached_occupancy(reinterpret_cast<const void*>(sample_kernel), kThreads, sizeof(Shared), sizeof(Shared), &sms);
+    if (occ < 1) return LAR_ERR_LAUNCH;
+    const int64_t rows = static_cast<int64_t>(p.B) * p.T;
     int size = 1;
-    while (size < kMaxCluster && static_cast<int64_t>(size) * 4096 < p.V) size *= 2;
+    while (size < kMaxCluster && static_cast<int64_t>(size) * 2048 < p.V && 2 * size * rows <= static_cast<int64_t>(sms) * occ) size *= 2;
     SampleParams q = p;
     // rows are the grid's y: as many at once as that admits
     const int most = 65535 / p.T;
     for (int64_t b = 0; b < p.B; b += most) {
         q.B = static_cast<int>(p.B - b < most ? p.B - b : most);
-        const lar_status st = launch_ordered(sample_kernel, dim3(size, q.B * p.T), kThreads, 0, size, static_cast<cudaStream_t>(stream), q);
+        const lar_status st = launch_ordered(sample_kernel, dim3(size, q.B * p.T), kThreads, sizeof(Shared), size, static_cast<cudaStream_t>(stream), q);
         if (st != LAR_OK) return st;
         const int64_t es = p.x_dt == LAR_F32 ? 4 : 2;
         q.x = static_cast<const char*>(q.x) + most * p.xs[0] * es;
