@@ -11,8 +11,8 @@
 //
 // Work.  A row is a cluster's, every warp owning a contiguous stretch of the vocabulary.
 // One pass finds the greatest logit.  Then
-//   top-k: the k-th of the threads' own maxima is a bound that k logits reach, and hardly
-//     more (1.4 k where k is half as many as the threads are); the logits from it on go to
+//   top-k: the k-th of the threads' own maxima (two a thread) is a bound that k logits reach,
+//     and hardly more (1.4 k where k is half as many as there are maxima); the logits from it on go to
 //     one block, which finds all cuts, and the token, among them.
 //   top-p alone: the weights are added up in bins of their exponent, 11 bits at once; the
 //     logits of the one bin that the cut falls into go to one block.
@@ -39,18 +39,17 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kStep = 256;       // tokens of a warp's step, 8 a lane
 constexpr int kBits = 11;        // of a key, looked at in one go
-constexpr int kList = 2048;      // room for logits around a cut
+constexpr int kList = 2048;      // room for logits around a cut, all and a block's
+constexpr int kOwn = 1024;
 constexpr int kBins = 1 << kBits;
 constexpr u64 kOne = 1ull << 39;  // weight of the greatest logit
 
-// 2^(39 + j / 32), to the nearest whole number
-__constant__ u64 kPow[32] = {
-    549755813888ull, 561793898668ull, 574095583180ull, 586666639507ull, 599512966123ull, 612640590662ull,
-    626055672747ull, 639764506879ull, 653773525390ull, 668089301461ull, 682718552210ull, 697668141836ull,
-    712945084849ull, 728556549354ull, 744509860419ull, 760812503507ull, 777472127994ull, 794496550755ull,
-    811893759832ull, 829671918182ull, 847839367509ull, 866404632174ull, 885376423200ull, 904763642353ull,
-    924575386327ull, 944820951003ull, 965509835819ull, 986651748221ull, 1008256608221ull, 1030334553053ull,
-    1052895941925ull, 1075951360882ull};
+// 2^(31 + j / 32), to the nearest whole number
+__constant__ unsigned kPow[32] = {
+    2147483648u, 2194507417u, 2242560872u, 2291666561u, 2341847524u, 2393127307u, 2445529972u, 2499080105u,
+    2553802834u, 2609723834u, 2666869345u, 2725266179u, 2784941738u, 2845924021u, 2908241642u, 2971923842u,
+    3037000500u, 3103502151u, 3171459999u, 3240905930u, 3311872529u, 3384393094u, 3458501653u, 3534232978u,
+    3611622603u, 3690706840u, 3771522796u, 3854108391u, 3938502376u, 4024744348u, 4112874773u, 4202935003u};
 
 // A logit as it is ordered: NaN is -infinity, and -0 is 0.
 __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
@@ -66,33 +65,65 @@ __device__ __forceinline__ float of_key(unsigned k) {
 
 constexpr unsigned kLeast = 0x007fffffu;   // key of -infinity
 
+constexpr float kRound = 12582912.f;   // 1.5 2^23: a sum with it is rounded to a whole number
+
 struct Scale {
     float half_max;     // max / 2: differences of halves do not overflow
     float hi, lo;       // 2 log2(e) / temperature
     bool infinite;      // max is +infinity
 
-    // (x - max) log2(e) / temperature as y + e
-    __device__ __forceinline__ void exponent(float x, float& y, float& e) const {
-        const float a = 0.5f * x, d = a - half_max, t = d - a;
-        const float de = (a - (d - t)) + (-half_max - t);
-        y = d * hi;
-        e = fmaf(d, hi, -y) + fmaf(d, lo, de * hi);
+    // (x - max) log2(e) / temperature as y + e, two at once.  The difference is exact: its
+    // error is a float (two-sum).
+    __device__ __forceinline__ void exponents(f32x2 x, f32x2& y, f32x2& e) const {
+        const f32x2 m = pack2(-half_max, -half_max), minus = pack2(-1.f, -1.f), h = pack2(hi, hi);
+        const f32x2 a = mul2(x, pack2(0.5f, 0.5f)), d = add2(a, m), t = fma2(a, minus, d);
+        const f32x2 de = add2(fma2(fma2(t, minus, d), minus, a), fma2(t, minus, m));
+        y = mul2(d, h);
+        e = fma2(d, pack2(lo, lo), fma2(de, h, fma2(d, h, mul2(y, minus))));
     }
 
-    __device__ __forceinline__ u64 weight(float x, const u64* pow) const {
-        if (0.5f * x == half_max) return kOne;
-        if (infinite) return 0;
-        float y, e;
-        exponent(x, y, e);
-        if (!(y >= -41.f)) return 0;
-        const float r32 = rintf(y * 32.f);
-        const int j = static_cast<int>(r32), down = -(j >> 5);
-        const float f = fmaf(r32, -1.f / 32, y) + e;
-        // 2^f - 1 by ln 2, its powers over the factorials
-        const float g = f * fmaf(f, fmaf(f, fmaf(f, 9.618129e-3f, 5.550411e-2f), 0.24022651f), 0.69314718f);
-        const u64 t = pow[j & 31];
-        const u64 w = t + static_cast<u64>(static_cast<long long>(__float2int_rn(g * (static_cast<float>(t) * 0.125f))) << 3);
-        return down > 0 ? (w + (1ull << (down - 1))) >> down : w;
+    __device__ __forceinline__ void exponent(float x, float& y, float& e) const {
+        f32x2 yy, ee;
+        float z;
+        exponents(pack2(x, x), yy, ee);
+        unpack2(yy, y, z);
+        unpack2(ee, e, z);
+    }
+
+    // Weights of two logits, in 2^-39: 2^y by whole number, 32nd and the rest
+    __device__ __forceinline__ void weights(float x0, float x1, const uint2* pow, u64& w0, u64& w1) const {
+        f32x2 y, e;
+        exponents(pack2(x0, x1), y, e);
+        const f32x2 big = pack2(kRound, kRound), minus = pack2(-1.f, -1.f);
+        const f32x2 r = fma2(y, pack2(32.f, 32.f), big);
+        const f32x2 f = add2(fma2(add2(r, mul2(big, minus)), pack2(-1.f / 32, -1.f / 32), y), e);
+        // 2^f - 1: ln 2, its powers over the factorials
+        f32x2 g = fma2(f, pack2(9.618129e-3f, 9.618129e-3f), pack2(5.550411e-2f, 5.550411e-2f));
+        g = fma2(f, g, pack2(0.24022651f, 0.24022651f));
+        g = fma2(f, g, pack2(0.69314718f, 0.69314718f));
+        g = mul2(f, g);
+        float y0, y1, r0, r1, g0, g1;
+        unpack2(y, y0, y1);
+        unpack2(r, r0, r1);
+        unpack2(g, g0, g1);
+        w0 = scaled(x0, y0, r0, g0, pow);
+        w1 = scaled(x1, y1, r1, g1, pow);
+    }
+
+    __device__ __forceinline__ u64 scaled(float x, float y, float r, float g, const uint2* pow) const {
+        const int j = static_cast<int>(__float_as_uint(r) - __float_as_uint(kRound));
+        const uint2 t = pow[j & 31];
+        const unsigned m = t.x + static_cast<unsigned>(__float2int_rn(g * __uint_as_float(t.y)));
+        // m 2^8 2^(j / 32), rounded
+        const u64 v = ((static_cast<u64>(m) << 9 >> min(63, -(j >> 5))) + 1) >> 1;
+        const u64 w = y >= -41.f && !infinite ? v : 0ull;
+        return 0.5f * x == half_max ? kOne : w;
+    }
+
+    __device__ __forceinline__ u64 weight(float x, const uint2* pow) const {
+        u64 a, b;
+        weights(x, x, pow, a, b);
+        return a;
     }
 };
 
@@ -105,7 +136,20 @@ struct Row {
 
     __device__ __forceinline__ float at(int i) const { return clean(ld_in(x, i * xs, dt)); }
 
-    // f(i, x) for elements [j - off, j - off + 8), j a multiple of 8, if they are there
+    // elements [j - off, j - off + 8), j a multiple of 8; -infinity where there is none
+    __device__ __forceinline__ void eight_of(int j, float* a) const {
+        const int i = j - off;
+        if (xs == 1 && i >= 0 && i + 8 <= V) {
+            ld8<true>(x, i, dt, a);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a[k] = clean(a[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a[k] = i + k >= 0 && i + k < V ? at(i + k) : -INFINITY;
+        }
+    }
+
+    // f(i, x) for them, if they are there
     template <typename F>
     __device__ __forceinline__ void eight(int j, F f) const {
         const int i = j - off;
@@ -157,13 +201,16 @@ __device__ __forceinline__ unsigned entry_key(u64 e) { return static_cast<unsign
 __device__ __forceinline__ int entry_index(u64 e) { return static_cast<int>(0xffffffffu - static_cast<unsigned>(e)); }
 
 struct Shared {
-    u64 pow[32];
+    uint2 pow[32];                 // a whole number, and as a float
     u64 warp[kWarps];
     u64 peer[2][kMaxCluster];      // exchanges in turn
     u64 found[4];
-    u64 list[kList], all[kList];   // this block's, and in block 0 the cluster's
+    u64 list[kOwn];                // this block's
+    union {                        // block 0: the cluster's; before that its threads' maxima
+        u64 all[kList];
+        unsigned maxima[2 * kMaxCluster * kThreads];
+    };
     unsigned lo[kBins], hi[kBins];
-    unsigned maxima[kMaxCluster * kThreads];   // block 0: of the cluster's threads
     unsigned count;
     float scale_hi, scale_lo;
 };
@@ -361,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Block c{s, cluster_rank(), cluster_size(), tid, lane, warp};
     cluster_arrive();
-    if (tid < 32) s.pow[tid] = kPow[tid];
+    if (tid < 32) s.pow[tid] = make_uint2(kPow[tid], __float_as_uint(static_cast<float>(kPow[tid])));
     if (tid == 0) s.count = 0;
     stream_order();
     const int b = blockIdx.y / p.T, t = blockIdx.y % p.T;
@@ -388,13 +435,24 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     const bool single = !(temp > 0.f) || k == 1 || !(top_p > 0.f) || min_p > 1.f;
     const bool by_k = k > 0 && !single;
 
-    // the greatest logit
-    float most = -INFINITY;
+    // the greatest logit, and two maxima a thread
+    float most0 = -INFINITY, most1 = -INFINITY;
 #pragma unroll 4
-    for (int st = s0; st < s1; ++st) row.eight(st * kStep + lane * 8, [&](int, float x) { most = fmaxf(most, x); });
+    for (int st = s0; st < s1; ++st) {
+        float x[8];
+        row.eight_of(st * kStep + lane * 8, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            most0 = fmaxf(most0, x[e]);
+            most1 = fmaxf(most1, x[e + 4]);
+        }
+    }
     cluster_wait();   // every block runs: its memory may be written
-    if (by_k)
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(&s.maxima[c.rank * kThreads + tid], 0)), "r"(key_of(most)) : "memory");
+    if (by_k) {
+        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(peer_addr(&s.maxima[2 * (c.rank * kThreads + tid)], 0)),
+                     "r"(key_of(most0)), "r"(key_of(most1)) : "memory");
+    }
+    const float most = fmaxf(most0, most1);
     const unsigned top_key = static_cast<unsigned>(c.greatest(key_of(most)));
     const float greatest = of_key(top_key);
     const bool none = top_key == kLeast;
@@ -446,6 +504,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         const u64 w = sc.weight(x, s.pow);
         return w >= least ? w : u64{0};
     };
+    // f(x) has the weights of all the warp's logits, by lanes' eights
+    auto each_weight = [&](auto f) {
+        for (int st = s0; st < s1; ++st) {
+            float x[8];
+            row.eight_of(st * kStep + lane * 8, x);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                u64 a, b;
+                sc.weights(x[e], x[e + 1], s.pow, a, b);
+                f(x[e], a);
+                f(x[e + 1], b);
+            }
+        }
+    };
     auto of_row = [&](auto g) {
         each([&](int i, float x) {
             const unsigned key = key_of(x);
@@ -462,12 +534,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
             const unsigned key = key_of(x);
             if (!want(key, i, x)) return;
             const unsigned at = atomicAdd(&s.count, 1u);
-            if (at < kList) s.list[at] = entry_of(key, i);
+            if (at < kOwn) s.list[at] = entry_of(key, i);
         });
         __syncthreads();
         const unsigned mine = s.count;
         u64 before;
-        const u64 n = c.sum(tid == 0 ? mine : 0u, &before);
+        const u64 n = c.sum(tid != 0 ? 0u : mine <= kOwn ? mine : kList + 1, &before);
         if (n <= kList)
             for (unsigned i = tid; i < mine; i += kThreads) st_peer_u64(&s.all[before + i], 0, s.list[i]);
         __syncwarp();
@@ -507,9 +579,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     bool summed = false;
     if (by_k) {
         unsigned bound = kLeast;
-        if (k <= static_cast<int64_t>(c.size) * kThreads) {
+        if (k <= static_cast<int64_t>(c.size) * 2 * kThreads) {
             if (c.rank == 0) {
-                const unsigned n = c.size * kThreads;
+                const unsigned n = c.size * 2 * kThreads;
                 bound = c.template find_key<false>(kLeast, top_key, static_cast<u64>(k),
                                                    [&](auto g) { for (unsigned i = tid; i < n; i += kThreads) g(s.maxima[i], 0, 0.f); }, one);
                 if (tid < static_cast<int>(c.size)) st_peer_u64(&s.found[0], tid, bound);
@@ -568,8 +640,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
             };
             c.clear_bins();
             u64 w = 0;
-            each([&](int, float x) {
-                const u64 v = sc.weight(x, s.pow);
+            each_weight([&](float x, u64 v) {
                 if (v) c.add(static_cast<unsigned>(bin_of(x)), v);
                 w += v;
             });
@@ -612,7 +683,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         }
     }
     if (!drawn) {
-        if (!summed) each([&](int i, float x) { mine += weight(i, x); });
+        if (!summed) {
+            if (cut.key == kLeast) each_weight([&](float, u64 v) { mine += v >= least ? v : 0ull; });
+            else each([&](int i, float x) { mine += weight(i, x); });
+        }
         u64 start;
         total = c.sum(mine, &start);
         u64 target = part_of<false>(u, total);
