@@ -34,7 +34,10 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kThreads = 256;
+#ifndef LAR_SAMPLE_THREADS
+#define LAR_SAMPLE_THREADS 512
+#endif
+constexpr int kThreads = LAR_SAMPLE_THREADS;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kStep = 256;       // tokens of a warp's step, 8 a lane
@@ -208,7 +211,7 @@ struct Shared {
     u64 list[kOwn];                // this block's
     union {                        // block 0: the cluster's; before that its threads' maxima
         u64 all[kList];
-        unsigned maxima[2 * kMaxCluster * kThreads];
+        unsigned maxima[2 * kList];
     };
     unsigned lo[kBins], hi[kBins];
     unsigned count;
@@ -292,24 +295,25 @@ struct Block {
         } else {
             __syncthreads();
         }
+        constexpr int E = kBins / kThreads;   // bins of a thread, at most
         const int slice = kBins / static_cast<int>(n), per = slice / kThreads > 0 ? slice / kThreads : 1;
-        const int base = kBins - 1 - static_cast<int>(me) * slice;   // this block's highest bin
-        u64 bins[kBins / kThreads];
+        const int base = kBins - static_cast<int>(me) * slice - per * (tid + 1);   // this thread's lowest bin
+        u64 bins[E];   // from its highest down
         u64 mine = 0;
 #pragma unroll
-        for (int e = 0; e < kBins / kThreads; ++e) {
+        for (int e = 0; e < E; ++e) {
             bins[e] = 0;
-            const int q = tid * per + e;
-            if (e < per && q < slice) {
+            const int q = base + per - 1 - e;
+            if (e < per && tid * per < slice) {
                 if (CL) {
                     for (unsigned r = 0; r < n; ++r) {
                         unsigned l, h;
-                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(l) : "r"(peer_addr(&s.lo[base - q], r)));
-                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h) : "r"(peer_addr(&s.hi[base - q], r)));
+                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(l) : "r"(peer_addr(&s.lo[q], r)));
+                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h) : "r"(peer_addr(&s.hi[q], r)));
                         bins[e] += static_cast<u64>(h) << 32 | l;
                     }
                 } else {
-                    bins[e] = static_cast<u64>(s.hi[base - q]) << 32 | s.lo[base - q];
+                    bins[e] = static_cast<u64>(s.hi[q]) << 32 | s.lo[q];
                 }
             }
             mine += bins[e];
@@ -323,7 +327,7 @@ struct Block {
             int at = -1;
             u64 got = 0;
 #pragma unroll
-            for (int e = 0; e < kBins / kThreads; ++e)
+            for (int e = 0; e < E; ++e)
                 if (at < 0) {
                     if (run + bins[e] >= target) {
                         at = e;
@@ -334,7 +338,7 @@ struct Block {
                 }
             for (unsigned r = 0; r < n; ++r) {
                 const unsigned to = CL ? r : rank;
-                st_peer_u64(&s.found[1], to, static_cast<u64>(base - tid * per - at));
+                st_peer_u64(&s.found[1], to, static_cast<u64>(base + per - 1 - at));
                 st_peer_u64(&s.found[2], to, run);
                 st_peer_u64(&s.found[3], to, got);
             }
@@ -402,7 +406,7 @@ __device__ __forceinline__ u64 part_of(float u, u64 T) {
     return whole + (UP && rest ? 1u : 0u);
 }
 
-__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const __grid_constant__ SampleParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared& s = *reinterpret_cast<Shared*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -448,11 +452,25 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         }
     }
     cluster_wait();   // every block runs: its memory may be written
-    if (by_k) {
-        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(peer_addr(&s.maxima[2 * (c.rank * kThreads + tid)], 0)),
-                     "r"(key_of(most0)), "r"(key_of(most1)) : "memory");
-    }
     const float most = fmaxf(most0, most1);
+    // maxima of as many groups of logits as there is room for: two a thread, one, or one of two threads
+    const int groups = min(2 * static_cast<int>(c.size) * kThreads, 2 * kList);
+    if (by_k) {
+        const int id = static_cast<int>(c.rank) * kThreads + tid;
+        const float both = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        auto push = [&](int at, float x) {
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(&s.maxima[at], 0)), "r"(key_of(x)) : "memory");
+        };
+        const int all = static_cast<int>(c.size) * kThreads;
+        if (2 * all <= groups) {
+            push(id, most0);
+            push(id + all, most1);
+        } else if (all <= groups) {
+            push(id, most);
+        } else if (tid % 2 == 0) {
+            push(id / 2, both);
+        }
+    }
     const unsigned top_key = static_cast<unsigned>(c.greatest(key_of(most)));
     const float greatest = of_key(top_key);
     const bool none = top_key == kLeast;
@@ -575,13 +593,37 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
 
     u64 total = 0;
     bool drawn = false;
-    u64 mine = 0;
-    bool summed = false;
+    // The token, among block 0's list
+    auto draw_of_list = [&] {
+        u64 w = 0;
+        of_list([&](unsigned, int i, float x) { w += weight(i, x); });
+        total = c.own_sum(w);
+        u64 target = part_of<false>(u, total);
+        if (target >= total) target = total - 1;
+        const unsigned at = c.template find_key<false>(
+            0xffffffffu - static_cast<unsigned>(row.V), 0xffffffffu, target + 1,
+            [&](auto g) { of_list([&](unsigned, int i, float x) { g(0xffffffffu - static_cast<unsigned>(i), i, x); }); },
+            [&](unsigned, int i, float x) { return weight(i, x); });
+        if (tid == 0) put(static_cast<int64_t>(0xffffffffu - at));
+    };
+    // Block 0's cut and sum, to all blocks
+    auto tell_all = [&] {
+        if (tid < static_cast<int>(c.size)) {
+            st_peer_u64(&s.found[0], tid, static_cast<u64>(cut.key) << 32 | static_cast<unsigned>(cut.limit));
+            st_peer_u64(&s.found[1], tid, total);
+        }
+    };
+    auto hear = [&] {
+        __syncwarp();
+        cluster_sync();
+        cut = {static_cast<unsigned>(s.found[0] >> 32), static_cast<int>(static_cast<unsigned>(s.found[0]))};
+        total = s.found[1];
+    };
     if (by_k) {
         unsigned bound = kLeast;
-        if (k <= static_cast<int64_t>(c.size) * 2 * kThreads) {
+        if (k <= groups) {
             if (c.rank == 0) {
-                const unsigned n = c.size * 2 * kThreads;
+                const unsigned n = groups;
                 bound = c.template find_key<false>(kLeast, top_key, static_cast<u64>(k),
                                                    [&](auto g) { for (unsigned i = tid; i < n; i += kThreads) g(s.maxima[i], 0, 0.f); }, one);
                 if (tid < static_cast<int>(c.size)) st_peer_u64(&s.found[0], tid, bound);
@@ -599,31 +641,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
                     of_list([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });
                     cut_by(Alone{}, part_of<true>(top_p, c.own_sum(w)), of_list, by_weight);
                 }
-                u64 w = 0;
-                of_list([&](unsigned, int i, float x) { w += weight(i, x); });
-                total = c.own_sum(w);
-                u64 target = part_of<false>(u, total);
-                if (target >= total) target = total - 1;
-                const unsigned at = c.template find_key<false>(
-                    0xffffffffu - static_cast<unsigned>(row.V), 0xffffffffu, target + 1,
-                    [&](auto g) { of_list([&](unsigned, int i, float x) { g(0xffffffffu - static_cast<unsigned>(i), i, x); }); },
-                    [&](unsigned, int i, float x) { return weight(i, x); });
-                if (tid == 0) put(static_cast<int64_t>(0xffffffffu - at));
-                if (p.probs) {
-                    if (tid < static_cast<int>(c.size)) {
-                        st_peer_u64(&s.found[0], tid, static_cast<u64>(cut.key) << 32 | static_cast<unsigned>(cut.limit));
-                        st_peer_u64(&s.found[1], tid, total);
-                    }
-                    __syncwarp();
-                }
+                draw_of_list();
+                if (p.probs) tell_all();
             }
             drawn = true;
-            if (p.probs) {
-                __syncwarp();
-                cluster_sync();
-                cut = {static_cast<unsigned>(s.found[0] >> 32), static_cast<int>(static_cast<unsigned>(s.found[0]))};
-                total = s.found[1];
-            }
+            if (p.probs) hear();
         } else {
             cut_by(Whole{}, static_cast<u64>(k), of_row, one);
         }
@@ -631,13 +653,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     if (!drawn && top_p < 1.f) {
         bool done = false;
         if (!by_k) {
-            // bins of the exponent, from 0 at the greatest (the highest bin) to -42
-            auto bin_of = [&](float x) {
-                if (0.5f * x == sc.half_max) return kBins - 1;
-                float y, e;
-                sc.exponent(x, y, e);
-                return y >= -42.f ? kBins - 1 - static_cast<int>(y * (-kBins / 42.01f)) : -1;
-            };
+            // bins of equal widths over the logits that weigh anything
+            const float low = fmaxf(greatest - 29.2f * temp, -3e38f), to_bin = (kBins - 1) / (greatest - low);   // 2^-42
+            auto bin_of = [&](float x) { return min(kBins - 1, max(0, static_cast<int>((x - low) * to_bin))); };
             c.clear_bins();
             u64 w = 0;
             each_weight([&](float x, u64 v) {
@@ -649,33 +667,26 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
             const int bin = static_cast<int>(s.found[1]);
             const u64 above = s.found[2];
             __syncthreads();
-            n_list = collect([&](unsigned, int i, float x) {
-                const int q = bin_of(x);
-                if (q > bin) {
-                    const u64 v = sc.weight(x, s.pow);
-                    mine += v >= least ? v : 0;
-                }
-                return q == bin;
-            });
+            // all that may be kept, or, where that is too much, the cut's bin alone
+            n_list = collect([&](unsigned, int, float x) { return bin_of(x) >= bin; });
+            const bool few = n_list <= kList;
+            if (!few) {
+                if (tid == 0) s.count = 0;
+                __syncthreads();
+                n_list = collect([&](unsigned, int, float x) { return bin_of(x) == bin; });
+            }
             if (n_list <= kList) {
                 if (c.rank == 0) {
-                    cut_by(Alone{}, target - above, of_list, by_weight);
-                    if (tid < static_cast<int>(c.size))
-                        st_peer_u64(&s.found[0], tid, static_cast<u64>(cut.key) << 32 | static_cast<unsigned>(cut.limit));
+                    cut_by(Alone{}, few ? target : target - above, of_list, by_weight);
+                    if (few) draw_of_list();
+                    if (!few || p.probs) tell_all();
                 }
-                __syncwarp();
-                cluster_sync();
-                cut = {static_cast<unsigned>(s.found[0] >> 32), static_cast<int>(static_cast<unsigned>(s.found[0]))};
-                // each warp its own of the list's
-                for (unsigned i = lane; i < s.count; i += 32) {
-                    const int at = entry_index(s.list[i]), st = (at + row.off) / kStep;
-                    if (st >= s0 && st < s1) mine += weight(at, of_key(entry_key(s.list[i])));
-                }
-                done = summed = true;
+                drawn = few;
+                done = true;
+                if (!few || p.probs) hear();   // else the other blocks may be gone: nothing is sent to them
             }
         }
         if (!done) {
-            mine = 0;
             u64 w = 0;
             of_row([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });
             const u64 all = c.sum(w, nullptr);
@@ -683,40 +694,71 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         }
     }
     if (!drawn) {
-        if (!summed) {
-            if (cut.key == kLeast) each_weight([&](float, u64 v) { mine += v >= least ? v : 0ull; });
-            else each([&](int i, float x) { mine += weight(i, x); });
+        u64 mine = 0, start;
+        if (cut.key == kLeast) {
+            each_weight([&](float, u64 v) { mine += v >= least ? v : 0ull; });
+        } else {
+            const float at = of_key(cut.key);
+            for (int st = s0; st < s1; ++st) {
+                float x[8], high = -INFINITY;
+                row.eight_of(st * kStep + lane * 8, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) high = fmaxf(high, x[e]);
+                if (!(high >= at)) continue;   // nothing kept here
+                const int i0 = st * kStep + lane * 8 - row.off;
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    u64 a, b;
+                    sc.weights(x[e], x[e + 1], s.pow, a, b);
+                    mine += kept(i0 + e, key_of(x[e])) && a >= least ? a : 0ull;
+                    mine += kept(i0 + e + 1, key_of(x[e + 1])) && b >= least ? b : 0ull;
+                }
+            }
         }
-        u64 start;
         total = c.sum(mine, &start);
         u64 target = part_of<false>(u, total);
         if (target >= total) target = total - 1;
-        for (int w = 0; w < warp; ++w) start += s.warp[w];
-        if (start <= target && target < start + s.warp[warp]) {   // one warp of the cluster
-            for (int st = s0; st < s1; ++st) {
-                u64 w8[8];
-                int idx = -1;
+        // the one warp of the cluster whose stretch holds it; its block goes through that, 8
+        // neighbours a thread
+        int owner = -1;
+        for (int w = 0; w < kWarps; ++w) {
+            const u64 own = s.warp[w];
+            if (start <= target && target < start + own) {
+                owner = w;
+                break;
+            }
+            start += own;
+        }
+        if (owner >= 0) {
+            const int o_me = static_cast<int>(c.rank) * kWarps + owner, end = first_step(o_me + 1) * kStep;
+            for (int j0 = first_step(o_me) * kStep; j0 < end; j0 += kThreads * 8) {
+                const int j = j0 + tid * 8, i0 = j - row.off;
+                u64 w8[8], sum8 = 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w8[e] = 0;
-                const int i0 = st * kStep + lane * 8 - row.off;
-                row.eight(st * kStep + lane * 8, [&](int i, float x) { w8[i - i0] = weight(i, x); });
-                u64 sum8 = 0;
+                if (j < end) row.eight(j, [&](int i, float x) { w8[i - i0] = weight(i, x); });
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum8 += w8[e];
                 const u64 incl = warp_scan(sum8, lane);
-                u64 run = start + incl - sum8;
+                __syncthreads();   // s.warp is read no more
+                if (lane == 31) s.warp[warp] = incl;
+                __syncthreads();
+                u64 run = start + incl - sum8, all = start;
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w == warp) run += all - start;
+                    all += s.warp[w];
+                }
+                if (run <= target && target < run + sum8) {   // one thread
+                    int idx = -1;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    run += w8[e];
-                    if (idx < 0 && run > target) idx = i0 + e;
+                    for (int e = 0; e < 8; ++e) {
+                        run += w8[e];
+                        if (idx < 0 && run > target) idx = i0 + e;
+                    }
+                    put(idx);
                 }
-                const unsigned has = __ballot_sync(0xffffffffu, idx >= 0);
-                if (has) {
-                    idx = __shfl_sync(0xffffffffu, idx, __ffs(has) - 1);
-                    if (lane == 0) put(idx);
-                    break;
-                }
-                start += __shfl_sync(0xffffffffu, incl, 31);
+                if (target < all) break;
+                start = all;
             }
         }
     }

@@ -64,6 +64,17 @@ def test_filters(B, T, V, dtype, cuda_device):
     check(cuda_device, x, u, False, top_k=k * 50, top_p=0.9 + 0.1 * p)
 
 
+@pytest.mark.parametrize("B,V", [(1, 131072), (1, 32000), (40, 20000)])
+def test_cuts_without_probabilities(B, V, cuda_device):
+    """Calls that write a token alone: blocks end as soon as nothing is asked of them, while
+    one of them finds the token in its list."""
+    x, u, g = rows(60 + B, B, 1, V)
+    for i in range(4):
+        check(cuda_device, x, u, False, top_p=torch.full((B,), 0.9 if i % 2 else 0.9999))
+        check(cuda_device, x, u, False, top_k=torch.full((B,), 5 + 300 * i))
+        check(cuda_device, x, u, False, top_k=torch.full((B,), 700), top_p=torch.full((B,), 0.6))
+
+
 def test_ties(cuda_device):
     """Few different logits: prefixes that end inside a run of equal ones keep the lowest
     indices, wherever blocks and warps part them."""
