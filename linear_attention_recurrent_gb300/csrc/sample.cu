@@ -3,26 +3,26 @@
 //
 // Order and weights.  Logits are ordered by the bits of their fp32 value (a key that rises
 // with it), equal ones by index; each filter keeps a prefix of that order.  A weight
-// exp((x - max) / temperature) is a whole number of 2^-39: a token has to be the one that
-// exact sums give, and whole numbers add up exactly in any order, at the rate of 32-bit
-// adds, where fp64 is slow on this part.  Its argument is kept in two floats, 2^n comes
-// from a table of 32 steps, and the rest, at most 1/64, from a polynomial: good to 2^-30 of
-// the weight, or 2^-40 of the greatest.
+// exp((x - max) / temperature) is a whole number of 2^-(63 - log2 V): a token has to be the
+// one that exact sums give, and whole numbers add up exactly in any order, at the rate of
+// 32-bit adds, where fp64 is slow on this part.  Its argument is kept in two floats, 2^n
+// comes from a table of 32 steps, and the rest, at most 1/64, from a polynomial: good to
+// 2^-30 of the weight.
 //
 // Work.  A row is a cluster's, every warp owning a contiguous stretch of the vocabulary.
 // One pass finds the greatest logit.  Then
 //   top-k: the k-th of the threads' own maxima (two a thread) is a bound that k logits reach,
-//     and hardly more (1.4 k where k is half as many as there are maxima); the logits from it on go to
-//     one block, which finds all cuts, and the token, among them.
-//   top-p alone: the weights are added up in bins of their exponent, 11 bits at once; the
-//     logits of the one bin that the cut falls into go to one block.
+//     and hardly more (1.4 k where k is half as many as there are maxima); the logits from
+//     it on go to one block, which finds all cuts, and the token, among them.
+//   top-p alone: logits are counted in bins, which say in which one the cut lies if every bin
+//     weighs its middle; one more pass has all exact sums and takes that bin (or, where they
+//     are few, all above it as well) to one block.  Sums that place the cut elsewhere after
+//     all are rare, and left to the passes below.
 //   neither: the weights of each warp's stretch are added up.
-// Where no list is left, the warp whose stretch holds the threshold reads it again.  Lists
+// Where no list is left, the block whose stretch holds the threshold reads it again.  Lists
 // that grow past their room (equal logits, sorted ones) are replaced by passes over the
 // row that narrow the key down 11 bits at a time.  Ties at a cut are kept from the lowest
 // index on.
-#include <type_traits>
-
 #include "layer_common.cuh"
 #include "serve_params.h"
 
@@ -42,10 +42,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kStep = 256;       // tokens of a warp's step, 8 a lane
 constexpr int kBits = 11;        // of a key, looked at in one go
-constexpr int kList = 2048;      // room for logits around a cut, all and a block's
-constexpr int kOwn = 1024;
+constexpr int kList = 2048;      // room for logits around a cut
 constexpr int kBins = 1 << kBits;
-constexpr u64 kOne = 1ull << 39;  // weight of the greatest logit
+constexpr int kSmall = 256;      // entries that are compared with one another
 
 // 2^(31 + j / 32), to the nearest whole number
 __constant__ unsigned kPow[32] = {
@@ -73,7 +72,10 @@ constexpr float kRound = 12582912.f;   // 1.5 2^23: a sum with it is rounded to 
 struct Scale {
     float half_max;     // max / 2: differences of halves do not overflow
     float hi, lo;       // 2 log2(e) / temperature
+    int up;             // the greatest weighs 2^up
     bool infinite;      // max is +infinity
+
+    __device__ __forceinline__ u64 one() const { return 1ull << up; }
 
     // (x - max) log2(e) / temperature as y + e, two at once.  The difference is exact: its
     // error is a float (two-sum).
@@ -85,18 +87,20 @@ struct Scale {
         e = fma2(d, pack2(lo, lo), fma2(de, h, fma2(d, h, mul2(y, minus))));
     }
 
-    __device__ __forceinline__ void exponent(float x, float& y, float& e) const {
-        f32x2 yy, ee;
-        float z;
-        exponents(pack2(x, x), yy, ee);
-        unpack2(yy, y, z);
-        unpack2(ee, e, z);
-    }
-
-    // Weights of two logits, in 2^-39: 2^y by whole number, 32nd and the rest
+    // Weights of two logits (NaN and -infinity weigh nothing): 2^y by whole number, 32nd and
+    // the rest
     __device__ __forceinline__ void weights(float x0, float x1, const uint2* pow, u64& w0, u64& w1) const {
+        if (infinite) {
+            w0 = x0 == INFINITY ? one() : 0ull;
+            w1 = x1 == INFINITY ? one() : 0ull;
+            return;
+        }
         f32x2 y, e;
         exponents(pack2(x0, x1), y, e);
+        float y0, y1, r0, r1, g0, g1;
+        unpack2(y, y0, y1);
+        const float least = static_cast<float>(-2 - up);   // from there on a weight is 0
+        y = pack2(fmaxf(y0, least), fmaxf(y1, least));
         const f32x2 big = pack2(kRound, kRound), minus = pack2(-1.f, -1.f);
         const f32x2 r = fma2(y, pack2(32.f, 32.f), big);
         const f32x2 f = add2(fma2(add2(r, mul2(big, minus)), pack2(-1.f / 32, -1.f / 32), y), e);
@@ -105,22 +109,21 @@ struct Scale {
         g = fma2(f, g, pack2(0.24022651f, 0.24022651f));
         g = fma2(f, g, pack2(0.69314718f, 0.69314718f));
         g = mul2(f, g);
-        float y0, y1, r0, r1, g0, g1;
-        unpack2(y, y0, y1);
         unpack2(r, r0, r1);
         unpack2(g, g0, g1);
-        w0 = scaled(x0, y0, r0, g0, pow);
-        w1 = scaled(x1, y1, r1, g1, pow);
+        w0 = scaled(r0, g0, pow);
+        w1 = scaled(r1, g1, pow);
     }
 
-    __device__ __forceinline__ u64 scaled(float x, float y, float r, float g, const uint2* pow) const {
-        const int j = static_cast<int>(__float_as_uint(r) - __float_as_uint(kRound));
+    // r has the 32nds in its low bits, as a whole number
+    __device__ __forceinline__ u64 scaled(float r, float g, const uint2* pow) const {
+        const int j = static_cast<int>(__float_as_uint(r));   // kRound's own low 22 bits are 0
         const uint2 t = pow[j & 31];
         const unsigned m = t.x + static_cast<unsigned>(__float2int_rn(g * __uint_as_float(t.y)));
-        // m 2^8 2^(j / 32), rounded
-        const u64 v = ((static_cast<u64>(m) << 9 >> min(63, -(j >> 5))) + 1) >> 1;
-        const u64 w = y >= -41.f && !infinite ? v : 0ull;
-        return 0.5f * x == half_max ? kOne : w;
+        const int down = 63 - up + (static_cast<int>(__float_as_uint(kRound)) >> 5) - (j >> 5);
+        u64 w;
+        asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(static_cast<u64>(m) << 32), "r"(down));   // by 64 and more: 0
+        return w;
     }
 
     __device__ __forceinline__ u64 weight(float x, const uint2* pow) const {
@@ -139,16 +142,14 @@ struct Row {
 
     __device__ __forceinline__ float at(int i) const { return clean(ld_in(x, i * xs, dt)); }
 
-    // elements [j - off, j - off + 8), j a multiple of 8; -infinity where there is none
+    // elements [j - off, j - off + 8) as they are, j a multiple of 8; -infinity where there is none
     __device__ __forceinline__ void eight_of(int j, float* a) const {
         const int i = j - off;
         if (xs == 1 && i >= 0 && i + 8 <= V) {
             ld8<true>(x, i, dt, a);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) a[k] = clean(a[k]);
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) a[k] = i + k >= 0 && i + k < V ? at(i + k) : -INFINITY;
+            for (int k = 0; k < 8; ++k) a[k] = i + k >= 0 && i + k < V ? ld_in(x, (i + k) * xs, dt) : -INFINITY;
         }
     }
 
@@ -208,13 +209,15 @@ struct Shared {
     u64 warp[kWarps];
     u64 peer[2][kMaxCluster];      // exchanges in turn
     u64 found[4];
-    u64 list[kOwn];                // this block's
+    alignas(16) unsigned lo[kBins];
+    alignas(16) unsigned hi[kBins];
+    u64 list[kList];                // this block's
     union {                        // block 0: the cluster's; before that its threads' maxima
         u64 all[kList];
         unsigned maxima[2 * kList];
     };
-    unsigned lo[kBins], hi[kBins];
-    unsigned count;
+    u64 small[kSmall], small_w[kSmall];
+    unsigned count, small_n;
     float scale_hi, scale_lo;
 };
 
@@ -224,19 +227,22 @@ struct Block {
     int tid, lane, warp;
     int turn = 0;
 
+    // Joins every thread's v over the cluster, and over the ranks before this block; the warps'
+    // own stay in s.warp.
     template <typename F>
-    __device__ __forceinline__ u64 over(u64 v, u64 start, F join, u64* before) {
+    __device__ __forceinline__ u64 over(u64 v, F join, u64* before) {
+        __syncthreads();   // s.warp is read no more
         if (lane == 0) s.warp[warp] = v;
         __syncthreads();
         if (warp == 0) {
-            u64 own = lane < kWarps ? s.warp[lane] : start;
+            u64 own = lane < kWarps ? s.warp[lane] : 0ull;
 #pragma unroll
             for (int off = kWarps / 2; off > 0; off >>= 1) own = join(own, __shfl_xor_sync(0xffffffffu, own, off));
             if (lane < size) st_peer_u64(&s.peer[turn][rank], lane, own);
         }
         __syncwarp();
         cluster_sync();
-        u64 all = start, b = start;
+        u64 all = 0, b = 0;
         for (unsigned r = 0; r < size; ++r) {
             if (r == rank) b = all;
             all = join(all, s.peer[turn][r]);
@@ -246,18 +252,23 @@ struct Block {
         return all;
     }
 
-    // Sum of every thread's v over the cluster, and of the ranks before this block; the warps'
-    // sums stay in s.warp.
     __device__ __forceinline__ u64 sum(u64 v, u64* before) {
-        v = warp_sum(v);
-        __syncthreads();   // s.warp is read no more
-        return over(v, 0ull, [](u64 a, u64 b) { return a + b; }, before);
+        return over(warp_sum(v), [](u64 a, u64 b) { return a + b; }, before);
     }
 
     __device__ __forceinline__ u64 greatest(u64 v) {
-        v = warp_max(v);
+        return over(warp_max(v), [](u64 a, u64 b) { return a > b ? a : b; }, nullptr);
+    }
+
+    __device__ __forceinline__ unsigned own_least(unsigned v) {
+        v = __reduce_min_sync(0xffffffffu, v);
         __syncthreads();
-        return over(v, 0ull, [](u64 a, u64 b) { return a > b ? a : b; }, nullptr);
+        if (lane == 0) s.warp[warp] = v;
+        __syncthreads();
+        u64 all = s.warp[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) all = s.warp[w] < all ? s.warp[w] : all;
+        return static_cast<unsigned>(all);
     }
 
     // The same over this block alone
@@ -280,14 +291,16 @@ struct Block {
     }
 
     __device__ __forceinline__ void clear_bins() {
-        for (int i = tid; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
+        for (int i = tid; i < kBins / 4; i += kThreads)
+            reinterpret_cast<uint4*>(s.lo)[i] = reinterpret_cast<uint4*>(s.hi)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
     }
 
-    // The highest bin down to which the bins' sums reach `target`, in s.found: bin, the sum
-    // above it, its own.  CL: bins of all the cluster's blocks, to all of them.
-    template <bool CL>
-    __device__ __forceinline__ void find_bin(u64 target) {
+    // The highest bin down to which the bins' sums, as `value` takes them, reach `target_of`
+    // (the whole sum), in s.found: bin, the sum above it, its own.  CL: bins of all the
+    // cluster's blocks, to all of them.
+    template <bool CL, typename V, typename T>
+    __device__ __forceinline__ void find_bin(V value, T target_of) {
         const unsigned n = CL ? size : 1, me = CL ? rank : 0;
         if (CL) {
             __syncwarp();
@@ -315,12 +328,12 @@ struct Block {
                 } else {
                     bins[e] = static_cast<u64>(s.hi[q]) << 32 | s.lo[q];
                 }
+                bins[e] = value(q, bins[e]);
             }
             mine += bins[e];
         }
         u64 run = 0;
-        if (CL) sum(mine, &run);
-        else own_sum(mine);
+        const u64 target = target_of(CL ? sum(mine, &run) : own_sum(mine));
         for (int w = 0; w < warp; ++w) run += s.warp[w];
         run += warp_scan(mine, lane) - mine;
         if (run < target && run + mine >= target) {   // one thread
@@ -354,7 +367,7 @@ struct Block {
     template <bool CL, typename E, typename F>
     __device__ __forceinline__ unsigned find_key(unsigned lo, unsigned hi, u64 target, E each, F f) {
         u64 above = 0;
-        while (true) {
+        for (int round = 0; round < 3; ++round) {   // 32 bits, 11 at a time
             int shift = 0;
             while (((hi - lo) >> shift) >= kBins) ++shift;
             clear_bins();
@@ -363,7 +376,7 @@ struct Block {
                 const u64 w = f(key, i, x);
                 if (w) add((key - lo) >> shift, w);
             });
-            find_bin<CL>(target - above);
+            find_bin<CL>([](int, u64 v) { return v; }, [&](u64) { return target - above; });
             above += s.found[2];
             lo += static_cast<unsigned>(s.found[1]) << shift;
             hi = lo + min(hi - lo, (1u << shift) - 1);
@@ -372,6 +385,50 @@ struct Block {
         __syncthreads();
         if (tid == 0) s.found[2] = above;
         __syncthreads();
+        return lo;
+    }
+
+    // By this block alone: of values with places in [lo, hi], no two the same, the one at which
+    // the sums of the weights from the highest place down reach `target` (which they do).
+    // each(g) calls g(place, weight).
+    template <typename E>
+    __device__ __forceinline__ u64 find_place(u64 lo, u64 hi, u64 target, E each) {
+        u64 above = 0;
+        for (int round = 0; round < 6; ++round) {   // 64 bits, 11 at a time
+            const int shift = max(0, 64 - kBits - __clzll(static_cast<long long>(hi - lo)));
+            clear_bins();
+            each([&](u64 at, u64 w) {
+                if (at >= lo && at <= hi && w) add(static_cast<unsigned>((at - lo) >> shift), w);
+            });
+            find_bin<false>([](int, u64 v) { return v; }, [&](u64) { return target - above; });
+            above += s.found[2];
+            lo += s.found[1] << shift;
+            const u64 wide = (1ull << shift) - 1;
+            hi = hi - lo < wide ? hi : lo + wide;
+            if (shift == 0) break;
+            // few in the bin: each is compared with all
+            if (tid == 0) s.small_n = 0;
+            __syncthreads();
+            each([&](u64 at, u64 w) {
+                if (at < lo || at > hi || !w) return;
+                const unsigned n = atomicAdd(&s.small_n, 1u);
+                if (n < kSmall) {
+                    s.small[n] = at;
+                    s.small_w[n] = w;
+                }
+            });
+            __syncthreads();
+            const int n = static_cast<int>(s.small_n);
+            if (n > kSmall) continue;
+            if (tid < n) {
+                const u64 at = s.small[tid];
+                u64 run = above;
+                for (int i = 0; i < n; ++i) run += s.small[i] >= at ? s.small_w[i] : 0ull;
+                if (run >= target && run - s.small_w[tid] < target) s.found[0] = at;   // one thread
+            }
+            __syncthreads();
+            return s.found[0];
+        }
         return lo;
     }
 };
@@ -452,6 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         }
     }
     cluster_wait();   // every block runs: its memory may be written
+    most0 += 0.f;   // -0 is 0
+    most1 += 0.f;
     const float most = fmaxf(most0, most1);
     // maxima of as many groups of logits as there is room for: two a thread, one, or one of two threads
     const int groups = min(2 * static_cast<int>(c.size) * kThreads, 2 * kList);
@@ -504,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
 
     if (tid == 0) {
         const double q = 2.0 * 1.4426950408889634074 / static_cast<double>(temp);
-        s.scale_hi = static_cast<float>(q);
+        s.scale_hi = q < 3e38 ? static_cast<float>(q) : 3e38f;
         s.scale_lo = q < 3e38 ? static_cast<float>(q - static_cast<double>(s.scale_hi)) : 0.f;
     }
     __syncthreads();
@@ -513,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     sc.hi = s.scale_hi;
     sc.lo = s.scale_lo;
     sc.infinite = greatest == INFINITY;
-    const u64 least = min_p > 0.f ? part_of<true>(min_p, kOne) : 0ull;
+    sc.up = 63 - (32 - __clz(row.V - 1));   // so that V of the greatest sum up to 2^63
+    const u64 least = min_p > 0.f ? part_of<true>(min_p, sc.one()) : 0ull;
 
     Cut cut = {kLeast, row.V};   // everything above -infinity (whose weight is 0)
     auto kept = [&](int i, unsigned key) { return key > cut.key || (key == cut.key && i < cut.limit); };
@@ -522,17 +582,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         const u64 w = sc.weight(x, s.pow);
         return w >= least ? w : u64{0};
     };
-    // f(x) has the weights of all the warp's logits, by lanes' eights
+    // f(i, x, w): all of the warp's logits with their weights; i may lie outside the row, where
+    // the weight is 0
     auto each_weight = [&](auto f) {
         for (int st = s0; st < s1; ++st) {
             float x[8];
             row.eight_of(st * kStep + lane * 8, x);
+            const int i0 = st * kStep + lane * 8 - row.off;
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 u64 a, b;
                 sc.weights(x[e], x[e + 1], s.pow, a, b);
-                f(x[e], a);
-                f(x[e + 1], b);
+                f(i0 + e, x[e], a);
+                f(i0 + e + 1, x[e + 1], b);
             }
         }
     };
@@ -545,19 +607,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     const auto one = [](unsigned, int, float) { return u64{1}; };
     const auto by_weight = [&](unsigned, int, float x) { return sc.weight(x, s.pow); };
 
-    // Logits that `want` says go into this block's list; how many the cluster's blocks have,
-    // and, if they all fit, they are in block 0's s.all (after a barrier).
-    auto collect = [&](auto want) {
-        each([&](int i, float x) {
-            const unsigned key = key_of(x);
-            if (!want(key, i, x)) return;
-            const unsigned at = atomicAdd(&s.count, 1u);
-            if (at < kOwn) s.list[at] = entry_of(key, i);
-        });
+    auto to_list = [&](unsigned key, int i) {
+        const unsigned at = atomicAdd(&s.count, 1u);
+        if (at < kList) s.list[at] = entry_of(key, i);
+    };
+    // How many logits the cluster's lists have; if they all fit, they are in block 0's s.all
+    auto gather = [&] {
         __syncthreads();
         const unsigned mine = s.count;
         u64 before;
-        const u64 n = c.sum(tid != 0 ? 0u : mine <= kOwn ? mine : kList + 1, &before);
+        const u64 n = c.sum(tid != 0 ? 0u : mine <= kList ? mine : kList + 1, &before);
         if (n <= kList)
             for (unsigned i = tid; i < mine; i += kThreads) st_peer_u64(&s.all[before + i], 0, s.list[i]);
         __syncwarp();
@@ -565,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         return n;
     };
     u64 n_list = 0;
+    unsigned list_low = kLeast;   // no key of the list lies below
     auto of_list = [&](auto g) {
         for (unsigned i = tid; i < n_list; i += kThreads) {
             const unsigned key = entry_key(s.all[i]);
@@ -572,24 +632,28 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
             if (kept(at, key)) g(key, at, of_key(key));
         }
     };
-    // The cut behind the first values whose sum of f reaches `target`, each() holding all down to it.
-    auto cut_by = [&](auto cl, u64 target, auto each_of, auto f) {
-        constexpr bool CL = decltype(cl)::value;
-        const unsigned key = c.template find_key<CL>(cut.key, top_key, target, each_of, f);
+    // The cut behind the first logits whose sum of f reaches `target`: among block 0's list, and
+    // among the whole row
+    auto cut_list = [&](u64 target, auto f) {
+        const u64 at = c.find_place(entry_of(list_low, 0x7fffffff), entry_of(top_key, 0), target,
+                                    [&](auto g) { of_list([&](unsigned key, int i, float x) { g(entry_of(key, i), f(key, i, x)); }); });
+        __syncthreads();
+        cut = {entry_key(at), entry_index(at) + 1};
+    };
+    auto cut_row = [&](u64 target, auto f) {
+        const unsigned key = c.template find_key<true>(cut.key, top_key, target, of_row, f);
         const u64 above = s.found[2], at = s.found[3], w1 = f(key, 0, of_key(key));
         const u64 n = (target - above + w1 - 1) / w1;   // of the equal ones, this many
         int limit = cut.key == key ? cut.limit : row.V;
         __syncthreads();
         if (n * w1 < at) {
-            const unsigned last = c.template find_key<CL>(
+            const unsigned last = c.template find_key<true>(
                 0xffffffffu - static_cast<unsigned>(row.V), 0xffffffffu, n,
-                [&](auto g) { each_of([&](unsigned q, int i, float x) { if (q == key) g(0xffffffffu - static_cast<unsigned>(i), i, x); }); }, one);
+                [&](auto g) { of_row([&](unsigned q, int i, float x) { if (q == key) g(0xffffffffu - static_cast<unsigned>(i), i, x); }); }, one);
             limit = static_cast<int>(0xffffffffu - last) + 1;
         }
         cut = {key, limit};
     };
-    using Whole = std::true_type;
-    using Alone = std::false_type;
 
     u64 total = 0;
     bool drawn = false;
@@ -600,11 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         total = c.own_sum(w);
         u64 target = part_of<false>(u, total);
         if (target >= total) target = total - 1;
-        const unsigned at = c.template find_key<false>(
-            0xffffffffu - static_cast<unsigned>(row.V), 0xffffffffu, target + 1,
-            [&](auto g) { of_list([&](unsigned, int i, float x) { g(0xffffffffu - static_cast<unsigned>(i), i, x); }); },
-            [&](unsigned, int i, float x) { return weight(i, x); });
-        if (tid == 0) put(static_cast<int64_t>(0xffffffffu - at));
+        const u64 most_i = 0xffffffffull, least_i = most_i - static_cast<unsigned>(row.V);
+        const u64 at = c.find_place(least_i, most_i, target + 1,
+                                    [&](auto g) { of_list([&](unsigned, int i, float x) { g(most_i - static_cast<unsigned>(i), weight(i, x)); }); });
+        if (tid == 0) put(static_cast<int64_t>(most_i - at));
     };
     // Block 0's cut and sum, to all blocks
     auto tell_all = [&] {
@@ -619,100 +682,156 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         cut = {static_cast<unsigned>(s.found[0] >> 32), static_cast<int>(static_cast<unsigned>(s.found[0]))};
         total = s.found[1];
     };
+    bool summed = false;   // the warps' sums of what the draw is among
+    u64 mine = 0;
     if (by_k) {
         unsigned bound = kLeast;
         if (k <= groups) {
             if (c.rank == 0) {
-                const unsigned n = groups;
-                bound = c.template find_key<false>(kLeast, top_key, static_cast<u64>(k),
-                                                   [&](auto g) { for (unsigned i = tid; i < n; i += kThreads) g(s.maxima[i], 0, 0.f); }, one);
-                if (tid < static_cast<int>(c.size)) st_peer_u64(&s.found[0], tid, bound);
+                // the k-th maximum, or a little less: one look at the bins between the least and the greatest
+                unsigned low = 0xffffffffu;
+                for (int i = tid; i < groups; i += kThreads) low = min(low, s.maxima[i]);
+                low = c.own_least(low);
+                const int shift = max(0, 32 - kBits - __clz(static_cast<int>(top_key - low)));
+                c.clear_bins();
+                for (int i = tid; i < groups; i += kThreads) atomicAdd(&s.lo[(s.maxima[i] - low) >> shift], 1u);
+                c.template find_bin<false>([](int, u64 v) { return v; }, [&](u64) { return static_cast<u64>(k); });
+                if (tid < static_cast<int>(c.size)) st_peer_u64(&s.found[0], tid, low + (s.found[1] << shift));
             }
             __syncwarp();
             cluster_sync();
             bound = static_cast<unsigned>(s.found[0]);
         }
-        n_list = bound == kLeast && row.V > kList ? kList + 1 : collect([&](unsigned key, int, float) { return key >= bound; });
+        n_list = kList + 1;
+        if (bound > kLeast || row.V <= kList) {
+            const float least_x = of_key(bound);
+            for (int st = s0; st < s1; ++st) {
+                float x[8], high = -INFINITY;
+                row.eight_of(st * kStep + lane * 8, x);
+                const int i0 = st * kStep + lane * 8 - row.off;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) high = fmaxf(high, x[e]);
+                if (!(high >= least_x)) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (clean(x[e]) >= least_x && i0 + e >= 0 && i0 + e < row.V) to_list(key_of(clean(x[e])), i0 + e);
+            }
+            n_list = gather();
+        }
+        list_low = bound;
         if (n_list <= kList) {
             if (c.rank == 0) {
-                cut_by(Alone{}, static_cast<u64>(k), of_list, one);
+                cut_list(static_cast<u64>(k), one);
                 if (top_p < 1.f) {
                     u64 w = 0;
                     of_list([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });
-                    cut_by(Alone{}, part_of<true>(top_p, c.own_sum(w)), of_list, by_weight);
+                    cut_list(part_of<true>(top_p, c.own_sum(w)), by_weight);
                 }
                 draw_of_list();
                 if (p.probs) tell_all();
             }
             drawn = true;
-            if (p.probs) hear();
+            if (p.probs) hear();   // else the other blocks may be gone: nothing is sent to them
         } else {
-            cut_by(Whole{}, static_cast<u64>(k), of_row, one);
+            cut_row(static_cast<u64>(k), one);
         }
     }
     if (!drawn && top_p < 1.f) {
         bool done = false;
         if (!by_k) {
             // bins of equal widths over the logits that weigh anything
-            const float low = fmaxf(greatest - 29.2f * temp, -3e38f), to_bin = (kBins - 1) / (greatest - low);   // 2^-42
+            const float low = fmaxf(greatest - 0.6931472f * (sc.up + 1) * temp, -3e38f), to_bin = (kBins - 1) / (greatest - low);
             auto bin_of = [&](float x) { return min(kBins - 1, max(0, static_cast<int>((x - low) * to_bin))); };
             c.clear_bins();
-            u64 w = 0;
-            each_weight([&](float x, u64 v) {
-                if (v) c.add(static_cast<unsigned>(bin_of(x)), v);
-                w += v;
-            });
-            const u64 all = c.sum(w, nullptr), target = part_of<true>(top_p, all);
-            c.template find_bin<true>(target);
-            const int bin = static_cast<int>(s.found[1]);
-            const u64 above = s.found[2];
-            __syncthreads();
-            // all that may be kept, or, where that is too much, the cut's bin alone
-            n_list = collect([&](unsigned, int, float x) { return bin_of(x) >= bin; });
-            const bool few = n_list <= kList;
-            if (!few) {
-                if (tid == 0) s.count = 0;
-                __syncthreads();
-                n_list = collect([&](unsigned, int, float x) { return bin_of(x) == bin; });
+#pragma unroll 2
+            for (int st = s0; st < s1; ++st) {
+                float x[8];
+                row.eight_of(st * kStep + lane * 8, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (x[e] >= low) atomicAdd(&s.lo[bin_of(x[e])], 1u);
             }
-            if (n_list <= kList) {
+            const float width = 1.f / to_bin;
+            c.template find_bin<true>([&](int q, u64 n) { return n ? n * sc.weight(fminf(greatest, low + (q + 0.5f) * width), s.pow) : 0ull; },
+                                      [&](u64 all) { return max(u64{1}, part_of<true>(top_p, all)); });
+            const int bin = static_cast<int>(s.found[1]);
+            // How many lie in and above it, and in the 3, 7 and 17 bins around it: a bin's middle is up
+            // to 0.8 % off, so the cut may lie in a neighbour.  The list takes all of them or, where
+            // they are too many, the widest of these windows that fits.
+            u64 n = 0;
+            {
+                unsigned part[4] = {0, 0, 0, 0};
+                for (int q = max(0, bin - 8) + tid; q < kBins; q += kThreads) {
+                    const unsigned v = s.lo[q];
+                    if (q >= bin - 3) part[0] = min(part[0] + min(v, kList + 1u), kList + 1u);
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        if (abs(q - bin) <= (e == 0 ? 1 : e == 1 ? 3 : 8)) part[e + 1] += min(v, kList + 1u);
+                }
+                // 16 bits a number: of a block kList + 1 at most
+#pragma unroll
+                for (int e = 0; e < 4; ++e) n |= min(c.own_sum(part[e]), kList + u64{1}) << (16 * e);
+            }
+            n = c.sum(tid == 0 ? n : 0ull, nullptr);
+            const bool few = (n & 0xffff) <= kList;
+            const int around = (n >> 48) <= kList ? 8 : (n >> 32 & 0xffff) <= kList ? 3 : (n >> 16 & 0xffff) <= kList ? 1 : 0;
+            const int from = few ? bin - 3 : bin - around, to = few ? kBins : bin + around;
+            // exact sums: of all, of the bins above the list's, of those
+            u64 all = 0, above = 0, own = 0;
+            each_weight([&](int i, float x, u64 w) {
+                all += w;
+                if (w == 0) return;
+                const int q = bin_of(x);
+                if (q < from) return;
+                if (q > to) {
+                    above += w;
+                    mine += w >= least ? w : 0ull;
+                } else {
+                    own += w;
+                    to_list(key_of(clean(x)), i);
+                }
+            });
+            all = c.sum(all, nullptr);
+            above = c.sum(above, nullptr);
+            own = c.sum(own, nullptr);
+            n_list = gather();
+            list_low = key_of(clean(low));
+            const u64 target = part_of<true>(top_p, all);
+            if (n_list <= kList && above < target && target <= above + own) {
                 if (c.rank == 0) {
-                    cut_by(Alone{}, few ? target : target - above, of_list, by_weight);
+                    cut_list(target - above, by_weight);
                     if (few) draw_of_list();
                     if (!few || p.probs) tell_all();
                 }
-                drawn = few;
                 done = true;
-                if (!few || p.probs) hear();   // else the other blocks may be gone: nothing is sent to them
+                drawn = few;
+                if (!few || p.probs) hear();
+                if (!few) {
+                    // each warp its own of the lists'
+                    for (unsigned i = lane; i < s.count; i += 32) {
+                        const int at = entry_index(s.list[i]), st = (at + row.off) / kStep;
+                        if (st >= s0 && st < s1) mine += weight(at, of_key(entry_key(s.list[i])));
+                    }
+                    summed = true;
+                }
             }
         }
         if (!done) {
             u64 w = 0;
             of_row([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });
             const u64 all = c.sum(w, nullptr);
-            cut_by(Whole{}, part_of<true>(top_p, all), of_row, by_weight);
+            cut_row(part_of<true>(top_p, all), by_weight);
         }
     }
     if (!drawn) {
-        u64 mine = 0, start;
-        if (cut.key == kLeast) {
-            each_weight([&](float, u64 v) { mine += v >= least ? v : 0ull; });
-        } else {
-            const float at = of_key(cut.key);
-            for (int st = s0; st < s1; ++st) {
-                float x[8], high = -INFINITY;
-                row.eight_of(st * kStep + lane * 8, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) high = fmaxf(high, x[e]);
-                if (!(high >= at)) continue;   // nothing kept here
-                const int i0 = st * kStep + lane * 8 - row.off;
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    u64 a, b;
-                    sc.weights(x[e], x[e + 1], s.pow, a, b);
-                    mine += kept(i0 + e, key_of(x[e])) && a >= least ? a : 0ull;
-                    mine += kept(i0 + e + 1, key_of(x[e + 1])) && b >= least ? b : 0ull;
-                }
+        u64 start;
+        if (!summed) {
+            mine = 0;
+            if (cut.key == kLeast) {
+                if (least) each_weight([&](int, float, u64 w) { mine += w >= least ? w : 0ull; });
+                else each_weight([&](int, float, u64 w) { mine += w; });
+            } else {
+                each_weight([&](int i, float x, u64 w) { mine += w >= least && kept(i, key_of(clean(x))) ? w : 0ull; });
             }
         }
         total = c.sum(mine, &start);
@@ -763,16 +882,33 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         }
     }
     if (p.probs) {
-        const float inv = 1.f / (static_cast<float>(total) * 0x1p-39f);
-        put_probs([&](int i) {
-            const float x = row.at(i);
-            if (!kept(i, key_of(x)) || (least && sc.weight(x, s.pow) < least)) return 0.f;
-            if (0.5f * x == sc.half_max) return inv;
-            if (sc.infinite) return 0.f;
-            float y, e;
-            sc.exponent(x, y, e);
-            return y >= -200.f ? exp2_f(y) * fmaf(e, 0.69314718f, 1.f) * inv : 0.f;
-        });
+        float* out = p.probs + b * p.ps[0] + t * p.ps[1];
+        const float inv = 1.f / ldexpf(static_cast<float>(total), -sc.up);
+        const bool all = cut.key == kLeast && !least;
+        const int lo = max(0, s0 * kStep - row.off), hi = min(row.V, s1 * kStep - row.off);
+        // neighbours on neighbouring lanes, four steps at once
+        for (int i0 = lo + lane; i0 < hi; i0 += 128) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = i0 + e * 32 < hi ? row.at(i0 + e * 32) : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                f32x2 y, er;
+                float v[2], q[2];
+                sc.exponents(pack2(x[e], x[e + 1]), y, er);
+                unpack2(y, v[0], v[1]);
+                unpack2(er, q[0], q[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int i = i0 + (e + k) * 32;
+                    const float z = x[e + k];
+                    float r = v[k] >= -200.f ? exp2_f(v[k]) * fmaf(q[k], 0.69314718f, 1.f) * inv : 0.f;
+                    if (sc.infinite) r = z == INFINITY ? inv : 0.f;
+                    if (!all && (!kept(i, key_of(z)) || (least && sc.weight(z, s.pow) < least))) r = 0.f;
+                    if (i < hi) out[i * p.ps[2]] = r;
+                }
+            }
+        }
     }
 }
 
