@@ -208,6 +208,7 @@ struct Shared {
     uint2 pow[32];                 // a whole number, and as a float
     u64 warp[kWarps];
     u64 peer[2][kMaxCluster];      // exchanges in turn
+    u64 warp4[4][kWarps], peer4[2][4][kMaxCluster];
     u64 found[4];
     alignas(16) unsigned lo[kBins];
     alignas(16) unsigned hi[kBins];
@@ -242,10 +243,13 @@ struct Block {
         }
         __syncwarp();
         cluster_sync();
-        u64 all = 0, b = 0;
-        for (unsigned r = 0; r < size; ++r) {
+        u64 of[kMaxCluster], all = 0, b = 0;
+#pragma unroll
+        for (unsigned r = 0; r < kMaxCluster; ++r) of[r] = r < size ? s.peer[turn][r] : 0ull;
+#pragma unroll
+        for (unsigned r = 0; r < kMaxCluster; ++r) {
             if (r == rank) b = all;
-            all = join(all, s.peer[turn][r]);
+            all = join(all, of[r]);
         }
         turn ^= 1;
         if (before) *before = b;
@@ -254,6 +258,30 @@ struct Block {
 
     __device__ __forceinline__ u64 sum(u64 v, u64* before) {
         return over(warp_sum(v), [](u64 a, u64 b) { return a + b; }, before);
+    }
+
+    // Four sums at once
+    __device__ __forceinline__ void sums(u64 (&v)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = warp_sum(v[e]);
+            if (lane == 0) s.warp4[e][warp] = v[e];
+        }
+        __syncthreads();
+        if (warp < 4) {
+            u64 own = lane < kWarps ? s.warp4[warp][lane] : 0ull;
+            own = warp_sum(own);
+            if (lane < size) st_peer_u64(&s.peer4[turn][warp][rank], lane, own);
+        }
+        __syncwarp();
+        cluster_sync();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = 0;
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r) v[e] += r < size ? s.peer4[turn][e][r] : 0ull;
+        }
+        turn ^= 1;
     }
 
     __device__ __forceinline__ u64 greatest(u64 v) {
@@ -319,12 +347,17 @@ struct Block {
             const int q = base + per - 1 - e;
             if (e < per && tid * per < slice) {
                 if (CL) {
-                    for (unsigned r = 0; r < n; ++r) {
-                        unsigned l, h;
-                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(l) : "r"(peer_addr(&s.lo[q], r)));
-                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h) : "r"(peer_addr(&s.hi[q], r)));
-                        bins[e] += static_cast<u64>(h) << 32 | l;
+                    unsigned l[kMaxCluster], h[kMaxCluster];   // all asked for at once
+#pragma unroll
+                    for (unsigned r = 0; r < kMaxCluster; ++r) {
+                        l[r] = h[r] = 0;
+                        if (r < n) {
+                            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(l[r]) : "r"(peer_addr(&s.lo[q], r)));
+                            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h[r]) : "r"(peer_addr(&s.hi[q], r)));
+                        }
                     }
+#pragma unroll
+                    for (unsigned r = 0; r < kMaxCluster; ++r) bins[e] += static_cast<u64>(h[r]) << 32 | l[r];
                 } else {
                     bins[e] = static_cast<u64>(s.hi[q]) << 32 | s.lo[q];
                 }
@@ -423,6 +456,7 @@ struct Block {
             if (tid < n) {
                 const u64 at = s.small[tid];
                 u64 run = above;
+#pragma unroll 8
                 for (int i = 0; i < n; ++i) run += s.small[i] >= at ? s.small_w[i] : 0ull;
                 if (run >= target && run - s.small_w[tid] < target) s.found[0] = at;   // one thread
             }
@@ -584,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     };
     // f(i, x, w): all of the warp's logits with their weights; i may lie outside the row, where
     // the weight is 0
-    auto each_weight = [&](auto f) {
+    auto each_weight2 = [&](auto f) {   // f(i, x, x', w, w') of neighbours
         for (int st = s0; st < s1; ++st) {
             float x[8];
             row.eight_of(st * kStep + lane * 8, x);
@@ -593,10 +627,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
             for (int e = 0; e < 8; e += 2) {
                 u64 a, b;
                 sc.weights(x[e], x[e + 1], s.pow, a, b);
-                f(i0 + e, x[e], a);
-                f(i0 + e + 1, x[e + 1], b);
+                f(i0 + e, x[e], x[e + 1], a, b);
             }
         }
+    };
+    auto each_weight = [&](auto f) {
+        each_weight2([&](int i, float x0, float x1, u64 w0, u64 w1) {
+            f(i, x0, w0);
+            f(i + 1, x1, w1);
+        });
     };
     auto of_row = [&](auto g) {
         each([&](int i, float x) {
@@ -624,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         return n;
     };
     u64 n_list = 0;
-    unsigned list_low = kLeast;   // no key of the list lies below
+    unsigned list_low = kLeast, list_high = top_key;   // no key of the list lies outside
     auto of_list = [&](auto g) {
         for (unsigned i = tid; i < n_list; i += kThreads) {
             const unsigned key = entry_key(s.all[i]);
@@ -635,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     // The cut behind the first logits whose sum of f reaches `target`: among block 0's list, and
     // among the whole row
     auto cut_list = [&](u64 target, auto f) {
-        const u64 at = c.find_place(entry_of(list_low, 0x7fffffff), entry_of(top_key, 0), target,
+        const u64 at = c.find_place(entry_of(list_low, 0x7fffffff), entry_of(list_high, 0), target,
                                     [&](auto g) { of_list([&](unsigned key, int i, float x) { g(entry_of(key, i), f(key, i, x)); }); });
         __syncthreads();
         cut = {entry_key(at), entry_index(at) + 1};
@@ -758,44 +797,42 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
             // How many lie in and above it, and in the 3, 7 and 17 bins around it: a bin's middle is up
             // to 0.8 % off, so the cut may lie in a neighbour.  The list takes all of them or, where
             // they are too many, the widest of these windows that fits.
-            u64 n = 0;
-            {
-                unsigned part[4] = {0, 0, 0, 0};
-                for (int q = max(0, bin - 8) + tid; q < kBins; q += kThreads) {
-                    const unsigned v = s.lo[q];
-                    if (q >= bin - 3) part[0] = min(part[0] + min(v, kList + 1u), kList + 1u);
+            u64 n[4] = {0, 0, 0, 0};
+            for (int q = max(0, bin - 8) + tid; q < kBins; q += kThreads) {
+                const unsigned v = s.lo[q];
+                if (q >= bin - 3) n[0] += v;
 #pragma unroll
-                    for (int e = 0; e < 3; ++e)
-                        if (abs(q - bin) <= (e == 0 ? 1 : e == 1 ? 3 : 8)) part[e + 1] += min(v, kList + 1u);
-                }
-                // 16 bits a number: of a block kList + 1 at most
-#pragma unroll
-                for (int e = 0; e < 4; ++e) n |= min(c.own_sum(part[e]), kList + u64{1}) << (16 * e);
+                for (int e = 0; e < 3; ++e)
+                    if (abs(q - bin) <= (e == 0 ? 1 : e == 1 ? 3 : 8)) n[e + 1] += v;
             }
-            n = c.sum(tid == 0 ? n : 0ull, nullptr);
-            const bool few = (n & 0xffff) <= kList;
-            const int around = (n >> 48) <= kList ? 8 : (n >> 32 & 0xffff) <= kList ? 3 : (n >> 16 & 0xffff) <= kList ? 1 : 0;
-            const int from = few ? bin - 3 : bin - around, to = few ? kBins : bin + around;
-            // exact sums: of all, of the bins above the list's, of those
-            u64 all = 0, above = 0, own = 0;
-            each_weight([&](int i, float x, u64 w) {
-                all += w;
-                if (w == 0) return;
-                const int q = bin_of(x);
-                if (q < from) return;
-                if (q > to) {
-                    above += w;
-                    mine += w >= least ? w : 0ull;
-                } else {
-                    own += w;
-                    to_list(key_of(clean(x)), i);
+            c.sums(n);
+            const bool few = n[0] <= kList;
+            const int around = n[3] <= kList ? 8 : n[2] <= kList ? 3 : n[1] <= kList ? 1 : 0;
+            const float from = low + (few ? bin - 3 : bin - around) * width, to = few ? INFINITY : low + (bin + around + 1) * width;
+            // exact sums: of all, of what lies above the list's, of those
+            u64 got[4] = {0, 0, 0, 0};
+            each_weight2([&](int i, float x0, float x1, u64 w0, u64 w1) {
+                got[0] += w0 + w1;
+                if (!(fmaxf(x0, x1) >= from)) return;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = e ? x1 : x0;
+                    const u64 w = e ? w1 : w0;
+                    if (!(x >= from) || w == 0) continue;
+                    if (x > to) {
+                        got[1] += w;
+                        mine += w >= least ? w : 0ull;
+                    } else {
+                        got[2] += w;
+                        to_list(key_of(clean(x)), i + e);
+                    }
                 }
             });
-            all = c.sum(all, nullptr);
-            above = c.sum(above, nullptr);
-            own = c.sum(own, nullptr);
+            c.sums(got);
+            const u64 all = got[0], above = got[1], own = got[2];
             n_list = gather();
-            list_low = key_of(clean(low));
+            list_low = key_of(clean(from));
+            if (!few) list_high = key_of(clean(to));
             const u64 target = part_of<true>(top_p, all);
             if (n_list <= kList && above < target && target <= above + own) {
                 if (c.rank == 0) {
@@ -885,28 +922,43 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         float* out = p.probs + b * p.ps[0] + t * p.ps[1];
         const float inv = 1.f / ldexpf(static_cast<float>(total), -sc.up);
         const bool all = cut.key == kLeast && !least;
-        const int lo = max(0, s0 * kStep - row.off), hi = min(row.V, s1 * kStep - row.off);
-        // neighbours on neighbouring lanes, four steps at once
-        for (int i0 = lo + lane; i0 < hi; i0 += 128) {
-            float x[4];
+        // Eight neighbours a lane are worked out, and written by neighbouring lanes: rows of
+        // odd sizes have no 16-byte borders in common with what is read.
+        float* const mine8 = reinterpret_cast<float*>(s.lo) + warp * kStep;   // the bins are done with
+        static_assert(kWarps * kStep * sizeof(float) <= sizeof(s.lo) + sizeof(s.hi), "");
+        for (int st = s0; st < s1; ++st) {
+            float x[8];
+            row.eight_of(st * kStep + lane * 8, x);
+            const int i0 = st * kStep - row.off;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = i0 + e * 32 < hi ? row.at(i0 + e * 32) : -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
+            for (int e = 0; e < 8; e += 2) {
                 f32x2 y, er;
-                float v[2], q[2];
                 sc.exponents(pack2(x[e], x[e + 1]), y, er);
+                er = fma2(er, pack2(0.69314718f, 0.69314718f), pack2(1.f, 1.f));
+                float v[2], q[2];
                 unpack2(y, v[0], v[1]);
                 unpack2(er, q[0], q[1]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int i = i0 + (e + k) * 32;
-                    const float z = x[e + k];
-                    float r = v[k] >= -200.f ? exp2_f(v[k]) * fmaf(q[k], 0.69314718f, 1.f) * inv : 0.f;
-                    if (sc.infinite) r = z == INFINITY ? inv : 0.f;
-                    if (!all && (!kept(i, key_of(z)) || (least && sc.weight(z, s.pow) < least))) r = 0.f;
-                    if (i < hi) out[i * p.ps[2]] = r;
+                for (int k = 0; k < 2; ++k) x[e + k] = v[k] >= -200.f ? exp2_f(v[k]) * inv * q[k] : sc.infinite && x[e + k] == INFINITY ? inv : 0.f;
+            }
+            if (!all) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = i0 + lane * 8 + e;
+                    if (!(x[e] > 0.f) || i < 0 || i >= row.V) continue;
+                    const float z = row.at(i);
+                    if (!kept(i, key_of(z)) || (least && sc.weight(z, s.pow) < least)) x[e] = 0.f;
                 }
+            }
+            __syncwarp();
+            float4* to = reinterpret_cast<float4*>(mine8 + lane * 8);
+            to[0] = make_float4(x[0], x[1], x[2], x[3]);
+            to[1] = make_float4(x[4], x[5], x[6], x[7]);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = i0 + e * 32 + lane;
+                if (i >= 0 && i < row.V) out[i * p.ps[2]] = mine8[e * 32 + lane];
             }
         }
     }
