@@ -12,8 +12,10 @@
 // magnitude is taken first.  Scales are powers of two, so that a page whose scale grows
 // later is rescaled without loss but for codes that leave the normal range.
 //
-// Jobs are a warp's where they are small (a step of T <= 16 tokens) and a block's where
-// they are whole pages; the queries, which belong to no page, are blocks of their own.
+// Steps of T <= 16 tokens: a warp has a job, and the queries are blocks of their own.
+// Prompts: a block has the new tokens of a page for some heads and their queries, a thread
+// a token's 16 dimensions, whose angles it works out once for all of them; the greatest
+// magnitudes come first, and the second look at keys and values finds them in L1 or L2.
 #include <cuda_fp8.h>
 
 #include "layer_common.cuh"
@@ -23,7 +25,13 @@ namespace lar {
 
 namespace {
 
-constexpr int kThreads = 256;
+#ifndef LAR_APPEND_MIN
+#define LAR_APPEND_MIN 2
+#endif
+#ifndef LAR_APPEND_THREADS
+#define LAR_APPEND_THREADS 256
+#endif
+constexpr int kThreads = LAR_APPEND_THREADS;
 constexpr int kELo = -64, kEHi = 64;   // exponents of a scale
 
 // f / 2 pi in units of 2^-64 turns, whole turns dropped: f = m 2^e, m of 24 bits, times
@@ -108,6 +116,39 @@ __device__ __forceinline__ void angles_of(const AppendParams& p, const unsigned 
     }
 }
 
+__device__ __forceinline__ void turn(const AppendParams& p, const Unit& un, const Angles& a, float* x) {
+    if (un.pair < 0) return;
+    if (p.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[2 * i], v = x[2 * i + 1];
+            x[2 * i] = fmaf(u, a.c[i], -(v * a.s[i]));
+            x[2 * i + 1] = fmaf(v, a.c[i], u * a.s[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[i], v = x[i + 8];
+            x[i] = fmaf(u, a.c[i], -(v * a.s[i]));
+            x[i + 8] = fmaf(v, a.c[i], u * a.s[i]);
+        }
+    }
+}
+
+// A unit of a bf16 row as it lies: asked for now, looked at later
+struct Raw {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void* base, int64_t row, const Unit& un) {
+        const unsigned short* p = static_cast<const unsigned short*>(base) + row;
+        a = __ldg(reinterpret_cast<const uint4*>(p + un.d0));
+        b = __ldg(reinterpret_cast<const uint4*>(p + un.d1));
+    }
+    __device__ __forceinline__ void widen(float* x) const {
+        unpack8(a, x);
+        unpack8(b, x + 8);
+    }
+};
+
 // The unit's values, rotated: x[0..8) at d0, x[8..16) at d1
 template <bool FAST>
 __device__ __forceinline__ void load_unit(const AppendParams& p, const unsigned long long* steps, const void* base, int64_t row, int64_t ds,
@@ -115,22 +156,7 @@ __device__ __forceinline__ void load_unit(const AppendParams& p, const unsigned 
     if constexpr (FAST) {
         ld8<true>(base, row + un.d0, dt, x);
         ld8<true>(base, row + un.d1, dt, x + 8);
-        if (un.pair < 0) return;
-        if (p.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = x[2 * i], v = x[2 * i + 1];
-                x[2 * i] = fmaf(u, a.c[i], -(v * a.s[i]));
-                x[2 * i + 1] = fmaf(v, a.c[i], u * a.s[i]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = x[i], v = x[i + 8];
-                x[i] = fmaf(u, a.c[i], -(v * a.s[i]));
-                x[i + 8] = fmaf(v, a.c[i], u * a.s[i]);
-            }
-        }
+        turn(p, un, a, x);
     } else {
         for (int i = 0; i < 16; ++i) {
             const int d = un.d0 + i;
@@ -182,145 +208,266 @@ __device__ __forceinline__ int last_at_most(int n, int64_t want, F key) {
     return lo;
 }
 
-// One job: the tokens of a call that fall into page `j` (of the touched ones) of sequence
-// n, for head h, by THR threads of which this is `me`.
-template <bool F8, bool FAST, int THR>
-__device__ __forceinline__ void kv_job(const AppendParams& p, const unsigned long long* steps, unsigned* top_s, int n, int j, int h, int me,
-                                       int32_t* bits) {
+template <bool FAST>
+__device__ __forceinline__ void put_query(const AppendParams& p, int64_t row, const Unit& un, const float* x) {
+    if constexpr (FAST) {
+        st8(p.q_out, row + un.d0, p.o_dt, x);
+        st8(p.q_out, row + un.d1, p.o_dt, x + 8);
+    } else {
+        for (int i = 0; i < 16; ++i) st_out(p.q_out, row + (un.d0 + i) * p.os[3], p.o_dt, x[i]);
+    }
+}
+
+// The new tokens of a call that fall into page `j` (of the touched ones) of sequence n
+struct Job {
+    int tok, cnt;        // first token's place in the arrays (of a sequence where T is fixed), their number
+    int place;           // of the first
+    int first;           // its row in the page
+    int64_t id;          // the page; -1: none
+};
+
+// false: no tokens there
+__device__ __forceinline__ bool job_of(const AppendParams& p, int n, int j, Job& job, int32_t* bits) {
     int begin, len;
     span(p, n, &begin, &len, bits);
     const int64_t start = length_of(p, n);
-    if (start < 0 || len == 0) return;
+    if (start < 0 || len == 0) return false;
     const int page = p.c.page;
     const int64_t pg = start / page + j;                                // page of the sequence
     const int64_t lo = max(start, pg * page), hi = min(start + len, (pg + 1) * page);
-    if (lo >= hi) return;
+    if (lo >= hi) return false;
+    job.tok = begin + static_cast<int>(lo - start);
+    job.cnt = static_cast<int>(hi - lo);
+    job.place = static_cast<int>(lo);
+    job.first = static_cast<int>(lo - pg * page);
+    job.id = -1;
     if (pg >= p.c.M) {
         *bits |= LAR_DEVERR_SEQLEN;
-        return;
+    } else {
+        job.id = ld_idx(p.c.table, n * p.c.tab_s[0] + pg * p.c.tab_s[1], p.c.tab_dt);
+        if (job.id >= p.c.P) {
+            *bits |= LAR_DEVERR_PAGE;
+            job.id = -1;
+        }
     }
-    const int64_t id = ld_idx(p.c.table, n * p.c.tab_s[0] + pg * p.c.tab_s[1], p.c.tab_dt);
-    if (id >= p.c.P) *bits |= LAR_DEVERR_PAGE;
-    if (id < 0 || id >= p.c.P) return;
-    const int first = static_cast<int>(lo - pg * page), cnt = static_cast<int>(hi - lo), t0 = static_cast<int>(lo - start);
-    const int UN = p.c.D / 16, tasks = cnt * UN;
-    const int64_t kq = p.cu ? 0 : n * p.ks[0], vq = p.cu ? 0 : n * p.vs[0];
+    return true;
+}
+
+__device__ __forceinline__ void raise(float& top, const float* x) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (fabsf(x[e]) < INFINITY) top = fmaxf(top, fabsf(x[e]));
+}
+
+// The scale of a (page, head) whose new values have the greatest magnitude `top`: no less
+// than that of `first` tokens that stand before them, whose codes follow it.  Written by
+// thread 0 of the THR threads that share the job; returned inverted.
+template <int THR>
+__device__ __forceinline__ float rescale(const AppendParams& p, bool values, const Job& job, int h, float top, int me) {
+    float* at = values ? p.c.v_scale + job.id * p.c.vss[0] + h * p.c.vss[1] : p.c.k_scale + job.id * p.c.kss[0] + h * p.c.kss[1];
+    const float was = job.first ? *at : 0.f, need = pow2(scale_exponent(top)), now = was > need ? was : need;
+    if (job.first && now > was) {
+        const float f = was / now;
+        unsigned char* pg = static_cast<unsigned char*>(values ? p.c.v : p.c.k) + job.id * (values ? p.c.vs[0] : p.c.ks[0]) + h * (values ? p.c.vs[2] : p.c.ks[2]);
+        const int64_t step = values ? p.c.vs[1] : p.c.ks[1];
+        const int UN = p.c.D / 16;
+        for (int i = me; i < job.first * UN; i += THR) {
+            uint4* to = reinterpret_cast<uint4*>(pg + i / UN * step + i % UN * 16);
+            const uint4 old = *to;
+            const unsigned in[4] = {old.x, old.y, old.z, old.w};
+            unsigned out[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    __nv_fp8_e4m3 c;
+                    c.__x = static_cast<__nv_fp8_storage_t>(in[e] >> (8 * b));
+                    x[b] = static_cast<float>(c);
+                }
+                out[e] = codes4(x, f);
+            }
+            *to = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+    }
+    if (THR > 32) __syncthreads();   // all have read the old scale
+    else __syncwarp();
+    if (me == 0) *at = now;
+    return 1.f / now;
+}
+
+template <bool F8>
+__device__ __forceinline__ void put_unit(const AppendParams& p, bool values, const Job& job, int h, int t, const Unit& un, const float* x, float inv) {
+    const int64_t row = values ? job.id * p.c.vs[0] + (job.first + t) * p.c.vs[1] + h * p.c.vs[2]
+                               : job.id * p.c.ks[0] + (job.first + t) * p.c.ks[1] + h * p.c.ks[2];
+    void* base = values ? p.c.v : p.c.k;
+    if constexpr (F8) {
+        unsigned char* to = static_cast<unsigned char*>(base) + row;
+        const uint2 a = make_uint2(codes4(x, inv), codes4(x + 4, inv)), b = make_uint2(codes4(x + 8, inv), codes4(x + 12, inv));
+        if (un.d1 == un.d0 + 8) {
+            *reinterpret_cast<uint4*>(to + un.d0) = make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            *reinterpret_cast<uint2*>(to + un.d0) = a;
+            *reinterpret_cast<uint2*>(to + un.d1) = b;
+        }
+    } else {
+        st8(base, row + un.d0, LAR_BF16, x);
+        st8(base, row + un.d1, LAR_BF16, x + 8);
+    }
+}
+
+// A step's job for one head, by a warp
+template <bool F8, bool FAST>
+__device__ __forceinline__ void step_job(const AppendParams& p, const unsigned long long* steps, int n, int j, int h, int me, int32_t* bits) {
+    Job job;
+    if (!job_of(p, n, j, job, bits) || job.id < 0) return;
+    const int UN = p.c.D / 16, tasks = job.cnt * UN;
     float kx[16], vx[16];
-    float ktop = 0.f, vtop = 0.f;
     auto take = [&](int i) {
         const int t = i / UN, u = i % UN;
         const Unit ku = unit_of<FAST>(p, u, true), vu = {u * 16, u * 16 + 8, -1};
-        const int tok = begin + t0 + t, place = static_cast<int>(lo) + t;
         Angles a;
-        angles_of<FAST>(p, steps, ku, place, a);
-        load_unit<FAST>(p, steps, p.k, kq + tok * p.ks[1] + h * p.ks[2], p.ks[3], p.k_dt, ku, a, place, true, kx);
-        load_unit<FAST>(p, steps, p.v, vq + tok * p.vs[1] + h * p.vs[2], p.vs[3], p.v_dt, vu, a, place, false, vx);
+        angles_of<FAST>(p, steps, ku, job.place + t, a);
+        load_unit<FAST>(p, steps, p.k, n * p.ks[0] + (job.tok + t) * p.ks[1] + h * p.ks[2], p.ks[3], p.k_dt, ku, a, job.place + t, true, kx);
+        load_unit<FAST>(p, steps, p.v, n * p.vs[0] + (job.tok + t) * p.vs[1] + h * p.vs[2], p.vs[3], p.v_dt, vu, a, job.place + t, false, vx);
     };
     float kinv = 1.f, vinv = 1.f;
     if constexpr (F8) {
-        for (int i = me; i < tasks; i += THR) {
+        float ktop = 0.f, vtop = 0.f;
+        for (int i = me; i < tasks; i += 32) {
             take(i);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                if (fabsf(kx[e]) < INFINITY) ktop = fmaxf(ktop, fabsf(kx[e]));
-                if (fabsf(vx[e]) < INFINITY) vtop = fmaxf(vtop, fabsf(vx[e]));
-            }
+            raise(ktop, kx);
+            raise(vtop, vx);
         }
-        unsigned kt = __reduce_max_sync(0xffffffffu, __float_as_uint(ktop)), vt = __reduce_max_sync(0xffffffffu, __float_as_uint(vtop));
-        if constexpr (THR > 32) {
-            if (me < 2) top_s[me] = 0u;
-            __syncthreads();
-            if (me % 32 == 0) {
-                atomicMax(&top_s[0], kt);
-                atomicMax(&top_s[1], vt);
-            }
-            __syncthreads();
-            kt = top_s[0];
-            vt = top_s[1];
-        }
-        float* kscale = p.c.k_scale + id * p.c.kss[0] + h * p.c.kss[1];
-        float* vscale = p.c.v_scale + id * p.c.vss[0] + h * p.c.vss[1];
-        const float kold = first ? *kscale : 0.f, vold = first ? *vscale : 0.f;
-        const float kne = pow2(scale_exponent(__uint_as_float(kt))), vne = pow2(scale_exponent(__uint_as_float(vt)));
-        const float know = kold > kne ? kold : kne, vnow = vold > vne ? vold : vne;
-        kinv = 1.f / know;
-        vinv = 1.f / vnow;
-        // what stands before them, at the new scale
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const float was = w ? vold : kold, now = w ? vnow : know;
-            if (first == 0 || !(now > was)) continue;
-            const float f = was / now;
-            unsigned char* pgp = static_cast<unsigned char*>(w ? p.c.v : p.c.k) + id * (w ? p.c.vs[0] : p.c.ks[0]) + h * (w ? p.c.vs[2] : p.c.ks[2]);
-            for (int i = me; i < first * UN; i += THR) {
-                uint4* at = reinterpret_cast<uint4*>(pgp + i / UN * (w ? p.c.vs[1] : p.c.ks[1]) + i % UN * 16);
-                const uint4 old = *at;
-                const unsigned in[4] = {old.x, old.y, old.z, old.w};
-                unsigned out[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x[4];
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        __nv_fp8_e4m3 c;
-                        c.__x = static_cast<__nv_fp8_storage_t>(in[e] >> (8 * b));
-                        x[b] = static_cast<float>(c);
-                    }
-                    out[e] = codes4(x, f);
-                }
-                *at = make_uint4(out[0], out[1], out[2], out[3]);
-            }
-        }
-        if constexpr (THR > 32) __syncthreads();
-        else __syncwarp();
-        if (me == 0) {
-            *kscale = know;
-            *vscale = vnow;
-        }
+        ktop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(ktop)));
+        vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
+        kinv = rescale<32>(p, false, job, h, ktop, me);
+        vinv = rescale<32>(p, true, job, h, vtop, me);
     }
-    const bool kept = F8 && tasks <= THR;   // still in registers
-    for (int i = me; i < tasks; i += THR) {
+    const bool kept = F8 && tasks <= 32;   // still in registers
+    for (int i = me; i < tasks; i += 32) {
         if (!kept) take(i);
-        const int t = i / UN, u = i % UN;
-        const Unit ku = unit_of<FAST>(p, u, true);
-        const int64_t krow = id * p.c.ks[0] + (first + t) * p.c.ks[1] + h * p.c.ks[2];
-        const int64_t vrow = id * p.c.vs[0] + (first + t) * p.c.vs[1] + h * p.c.vs[2];
-        if constexpr (F8) {
-            unsigned char *kc = static_cast<unsigned char*>(p.c.k) + krow, *vc = static_cast<unsigned char*>(p.c.v) + vrow;
-            *reinterpret_cast<uint2*>(kc + ku.d0) = make_uint2(codes4(kx, kinv), codes4(kx + 4, kinv));
-            *reinterpret_cast<uint2*>(kc + ku.d1) = make_uint2(codes4(kx + 8, kinv), codes4(kx + 12, kinv));
-            *reinterpret_cast<uint4*>(vc + u * 16) = make_uint4(codes4(vx, vinv), codes4(vx + 4, vinv), codes4(vx + 8, vinv), codes4(vx + 12, vinv));
+        put_unit<F8>(p, false, job, h, i / UN, unit_of<FAST>(p, i % UN, true), kx, kinv);
+        put_unit<F8>(p, true, job, h, i / UN, {i % UN * 16, i % UN * 16 + 8, -1}, vx, vinv);
+    }
+}
+
+// A prompt's job for heads [h0, h1) and their queries, by a block
+constexpr int kJobHeads = 4;   // at most
+constexpr int kAtOnce = 4;     // queries' rows that are asked for together
+
+template <bool F8, bool FAST, bool BF>
+__device__ __forceinline__ void prompt_job(const AppendParams& p, const unsigned long long* steps, unsigned* top_s, int n, int j, int h0, int h1, int me,
+                                           int32_t* bits) {
+    Job job;
+    if (!job_of(p, n, j, job, bits)) return;
+    const int UN = p.c.D / 16, tasks = job.cnt * UN, G = p.q ? p.Hq / p.c.H : 0;
+    float inv[2 * kJobHeads];
+#pragma unroll
+    for (int e = 0; e < 2 * kJobHeads; ++e) inv[e] = 1.f;
+    Angles a;
+    float x[16];
+    // f(head of the job, whether it is the values') with the unit's keys, rotated, and values in x
+    auto rows_of = [&](int t, int u, auto f) {
+        const Unit ku = unit_of<FAST>(p, u, true), vu = {u * 16, u * 16 + 8, -1};
+        const int64_t krow = (job.tok + t) * p.ks[1], vrow = (job.tok + t) * p.vs[1];
+        if constexpr (BF) {
+#pragma unroll
+            for (int e = 0; e < kJobHeads; e += 2) {
+                Raw k[2], v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (h0 + e + i < h1) {
+                        k[i].load(p.k, krow + (h0 + e + i) * p.ks[2], ku);
+                        v[i].load(p.v, vrow + (h0 + e + i) * p.vs[2], vu);
+                    }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (h0 + e + i < h1) {
+                        k[i].widen(x);
+                        turn(p, ku, a, x);
+                        f(e + i, false);
+                        v[i].widen(x);
+                        f(e + i, true);
+                    }
+            }
         } else {
-            st8(p.c.k, krow + ku.d0, LAR_BF16, kx);
-            st8(p.c.k, krow + ku.d1, LAR_BF16, kx + 8);
-            st8(p.c.v, vrow + u * 16, LAR_BF16, vx);
-            st8(p.c.v, vrow + u * 16 + 8, LAR_BF16, vx + 8);
+#pragma unroll
+            for (int e = 0; e < kJobHeads; ++e)
+                if (h0 + e < h1) {
+                    load_unit<FAST>(p, steps, p.k, krow + (h0 + e) * p.ks[2], p.ks[3], p.k_dt, ku, a, job.place + t, true, x);
+                    f(e, false);
+                    load_unit<FAST>(p, steps, p.v, vrow + (h0 + e) * p.vs[2], p.vs[3], p.v_dt, vu, a, job.place + t, false, x);
+                    f(e, true);
+                }
+        }
+    };
+    const bool one = tasks <= kThreads;   // each thread has one token's unit, and its angles
+    if (one && me < tasks) angles_of<FAST>(p, steps, unit_of<FAST>(p, me % UN, true), job.place + me / UN, a);
+    if (F8 && job.id >= 0) {
+        float top[2 * kJobHeads];
+#pragma unroll
+        for (int e = 0; e < 2 * kJobHeads; ++e) top[e] = 0.f;
+        for (int i = me; i < tasks; i += kThreads) {
+            const int t = i / UN, u = i % UN;
+            if (!one) angles_of<FAST>(p, steps, unit_of<FAST>(p, u, true), job.place + t, a);
+            rows_of(t, u, [&](int e, bool values) { raise(top[2 * e + values], x); });
+        }
+        if (me < 2 * kJobHeads) top_s[me] = 0u;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 2 * kJobHeads; ++e) {
+            const unsigned v = __reduce_max_sync(0xffffffffu, __float_as_uint(top[e]));
+            if (me % 32 == 0 && v) atomicMax(&top_s[e], v);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kJobHeads; ++e)
+            if (h0 + e < h1) {
+                inv[2 * e] = rescale<kThreads>(p, false, job, h0 + e, __uint_as_float(top_s[2 * e]), me);
+                inv[2 * e + 1] = rescale<kThreads>(p, true, job, h0 + e, __uint_as_float(top_s[2 * e + 1]), me);
+            }
+    }
+    for (int i = me; i < tasks; i += kThreads) {
+        const int t = i / UN, u = i % UN;
+        const Unit un = unit_of<FAST>(p, u, true);
+        if (!one) angles_of<FAST>(p, steps, un, job.place + t, a);
+        if (job.id >= 0) {
+            rows_of(t, u, [&](int e, bool values) {
+                put_unit<F8>(p, values, job, h0 + e, t, values ? Unit{u * 16, u * 16 + 8, -1} : un, x, inv[2 * e + values]);
+            });
+        }
+        const int64_t qrow = (job.tok + t) * p.qs[1], orow = (job.tok + t) * p.os[1];
+        if constexpr (BF) {
+            for (int h = h0 * G; h < h1 * G; h += kAtOnce) {
+                Raw r[kAtOnce];
+#pragma unroll
+                for (int e = 0; e < kAtOnce; ++e)
+                    if (h + e < h1 * G) r[e].load(p.q, qrow + (h + e) * p.qs[2], un);
+#pragma unroll
+                for (int e = 0; e < kAtOnce; ++e)
+                    if (h + e < h1 * G) {
+                        r[e].widen(x);
+                        turn(p, un, a, x);
+                        put_query<FAST>(p, orow + (h + e) * p.os[2], un, x);
+                    }
+            }
+        } else {
+            for (int h = h0 * G; h < h1 * G; ++h) {
+                load_unit<FAST>(p, steps, p.q, qrow + h * p.qs[2], p.qs[3], p.q_dt, un, a, job.place + t, true, x);
+                put_query<FAST>(p, orow + h * p.os[2], un, x);
+            }
         }
     }
 }
 
-// Rotated queries: a thread a (token, unit), for `hpt` heads
+// A step's rotated queries: a thread a (token, unit), for `hpt` heads
 template <bool FAST>
-__device__ __forceinline__ void q_task(const AppendParams& p, const unsigned long long* steps, int64_t task, int hpt, int32_t* bits) {
+__device__ __forceinline__ void q_task(const AppendParams& p, const unsigned long long* steps, int64_t task, int hpt) {
     const int UN = p.c.D / 16, chunks = (p.Hq + hpt - 1) / hpt;
     const int u = static_cast<int>(task % UN), ch = static_cast<int>(task / UN % chunks);
     const int64_t tok = task / UN / chunks;
-    int n, t;
-    int64_t qrow, orow;
-    if (p.cu) {
-        n = last_at_most(p.n, tok, [&](int i) { return ld_idx(p.cu, i * p.cu_s, p.cu_dt); });
-        int begin, len;
-        span(p, n, &begin, &len, bits);
-        if (tok < begin || tok >= begin + len) return;
-        t = static_cast<int>(tok) - begin;
-        qrow = tok * p.qs[1];
-        orow = tok * p.os[1];
-    } else {
-        n = static_cast<int>(tok / p.T);
-        t = static_cast<int>(tok % p.T);
-        qrow = n * p.qs[0] + t * p.qs[1];
-        orow = n * p.os[0] + t * p.os[1];
-    }
+    const int n = static_cast<int>(tok / p.T), t = static_cast<int>(tok % p.T);
     const int64_t start = length_of(p, n);
     if (start < 0) return;
     const int place = static_cast<int>(start) + t;
@@ -330,70 +477,82 @@ __device__ __forceinline__ void q_task(const AppendParams& p, const unsigned lon
     const int h1 = min(p.Hq, (ch + 1) * hpt);
     for (int h = ch * hpt; h < h1; ++h) {
         float x[16];
-        load_unit<FAST>(p, steps, p.q, qrow + h * p.qs[2], p.qs[3], p.q_dt, un, a, place, true, x);
-        const int64_t row = orow + h * p.os[2];
-        if constexpr (FAST) {
-            st8(p.q_out, row + un.d0, p.o_dt, x);
-            st8(p.q_out, row + un.d1, p.o_dt, x + 8);
-        } else {
-            for (int i = 0; i < 16; ++i) st_out(p.q_out, row + (un.d0 + i) * p.os[3], p.o_dt, x[i]);
-        }
+        load_unit<FAST>(p, steps, p.q, n * p.qs[0] + t * p.qs[1] + h * p.qs[2], p.qs[3], p.q_dt, un, a, place, true, x);
+        put_query<FAST>(p, n * p.os[0] + t * p.os[1] + h * p.os[2], un, x);
     }
 }
 
-// Blocks [0, kv_blocks) are jobs, the others queries
-template <bool F8, bool FAST, int THR>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p, int kv_blocks, int pages_of, int hpt,
-                                                          int64_t q_tasks) {
+__device__ __forceinline__ void load_steps(const AppendParams& p, unsigned long long* steps) {
+    if (threadIdx.x < p.rot / 2) steps[threadIdx.x] = turn_step(__ldg(p.inv_freq + threadIdx.x * p.if_s));
+    __syncthreads();
+}
+
+// Blocks [0, kv_blocks): a warp a job (sequence, touched page, head); the others: queries
+template <bool F8, bool FAST>
+__global__ void __launch_bounds__(kThreads) append_step(const __grid_constant__ AppendParams p, int kv_blocks, int pages_of, int hpt, int64_t q_tasks) {
     __shared__ unsigned long long steps[128];
-    __shared__ unsigned top_s[2];
     const int tid = threadIdx.x;
     stream_order();
-    if (tid < p.rot / 2) steps[tid] = turn_step(__ldg(p.inv_freq + tid * p.if_s));
-    __syncthreads();
+    load_steps(p, steps);
     int32_t bits = 0;
     if (static_cast<int>(blockIdx.x) >= kv_blocks) {
         const int64_t task = static_cast<int64_t>(blockIdx.x - kv_blocks) * kThreads + tid;
-        if (task < q_tasks) q_task<FAST>(p, steps, task, hpt, &bits);
-    } else if (THR == 32) {   // a warp a job: (sequence, touched page, head)
+        if (task < q_tasks) q_task<FAST>(p, steps, task, hpt);
+    } else {
         const int64_t job = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + tid / 32;
         const int h = static_cast<int>(job % p.c.H), j = static_cast<int>(job / p.c.H % pages_of);
         const int64_t n = job / p.c.H / pages_of;
-        if (n < p.n) kv_job<F8, FAST, 32>(p, steps, nullptr, static_cast<int>(n), j, h, tid % 32, &bits);
-    } else {                  // a block a job: sequence n's pages have numbers from cu[n] / page + 2 n on
-        const int h = blockIdx.x % p.c.H;
-        const int64_t unit = blockIdx.x / p.c.H;
-        auto key = [&](int i) { return ld_idx(p.cu, i * p.cu_s, p.cu_dt) / p.c.page + 2 * static_cast<int64_t>(i); };
-        const int n = last_at_most(p.n, unit, key);
-        const int64_t j = unit - key(n);
-        if (j >= 0 && j < (1 << 30)) kv_job<F8, FAST, THR>(p, steps, top_s, n, static_cast<int>(j), h, tid, &bits);
+        if (n < p.n) step_job<F8, FAST>(p, steps, static_cast<int>(n), j, h, tid % 32, &bits);
     }
+    flag_err(p.dev_err, bits);
+}
+
+// A block a job: sequence n's pages have numbers from cu[n] / page + 2 n on
+template <bool F8, bool FAST, bool BF>
+__global__ void __launch_bounds__(kThreads, LAR_APPEND_MIN) append_prompt(const __grid_constant__ AppendParams p, int groups, int heads) {
+    __shared__ unsigned long long steps[128];
+    __shared__ unsigned top_s[2 * kJobHeads];
+    stream_order();
+    load_steps(p, steps);
+    int32_t bits = 0;
+    const int h0 = static_cast<int>(blockIdx.x % groups) * heads;
+    const int64_t unit = blockIdx.x / groups;
+    auto key = [&](int i) { return ld_idx(p.cu, i * p.cu_s, p.cu_dt) / p.c.page + 2 * static_cast<int64_t>(i); };
+    const int n = last_at_most(p.n, unit, key);
+    const int64_t j = unit - key(n);
+    if (j >= 0 && j < (1 << 30)) prompt_job<F8, FAST, BF>(p, steps, top_s, n, static_cast<int>(j), h0, min(p.c.H, h0 + heads), threadIdx.x, &bits);
     flag_err(p.dev_err, bits);
 }
 
 template <bool F8, bool FAST>
 lar_status launch(const AppendParams& p, cudaStream_t stream) {
-    const int64_t tokens = p.cu ? p.ntok : static_cast<int64_t>(p.n) * p.T;
+    const int64_t limit = (int64_t{1} << 31) - 1;
+    if (p.cu) {
+        const int64_t pages = p.ntok / p.c.page + 2 * static_cast<int64_t>(p.n);
+        // heads share their angles where there are blocks enough without
+        int heads = 1;
+        while (heads < kJobHeads && 2 * heads <= p.c.H && pages * p.c.H >= 152 * 8 * heads) heads *= 2;
+        const int64_t groups = (p.c.H + heads - 1) / heads;
+        if (pages * groups > limit) return LAR_ERR_SHAPE;
+        const dim3 grid(static_cast<unsigned>(pages * groups));
+        const bool bf = p.k_dt == LAR_BF16 && p.v_dt == LAR_BF16 && (!p.q || p.q_dt == LAR_BF16);
+        if constexpr (FAST) {
+            if (bf) return launch_ordered(append_prompt<F8, true, true>, grid, kThreads, 0, 1, stream, p, static_cast<int>(groups), heads);
+        }
+        return launch_ordered(append_prompt<F8, FAST, false>, grid, kThreads, 0, 1, stream, p, static_cast<int>(groups), heads);
+    }
+    const int64_t tokens = static_cast<int64_t>(p.n) * p.T;
     int64_t q_tasks = 0;
     int hpt = 1;
     if (p.q) {
-        // heads share their angles where there are threads enough without
         while (hpt < 8 && hpt < p.Hq && tokens * (p.c.D / 16) * p.Hq / (2 * hpt) >= 152 * 2048) hpt *= 2;
         q_tasks = tokens * (p.c.D / 16) * ((p.Hq + hpt - 1) / hpt);
     }
-    const int64_t q_blocks = (q_tasks + kThreads - 1) / kThreads;
-    int64_t kv_blocks;
-    int pages_of = 0;
-    if (p.cu) {
-        kv_blocks = (p.ntok / p.c.page + 2 * static_cast<int64_t>(p.n)) * p.c.H;
-    } else {
-        pages_of = p.T == 1 ? 1 : 2;
-        kv_blocks = (static_cast<int64_t>(p.n) * pages_of * p.c.H + kThreads / 32 - 1) / (kThreads / 32);
-    }
-    if (kv_blocks + q_blocks > (int64_t{1} << 31) - 1) return LAR_ERR_SHAPE;
-    const dim3 grid(static_cast<unsigned>(kv_blocks + q_blocks));
-    return p.cu ? launch_ordered(append_kernel<F8, FAST, kThreads>, grid, kThreads, 0, 1, stream, p, static_cast<int>(kv_blocks), pages_of, hpt, q_tasks)
-                : launch_ordered(append_kernel<F8, FAST, 32>, grid, kThreads, 0, 1, stream, p, static_cast<int>(kv_blocks), pages_of, hpt, q_tasks);
+    const int pages_of = p.T == 1 ? 1 : 2;
+    const int64_t kv_blocks = (static_cast<int64_t>(p.n) * pages_of * p.c.H + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t blocks = kv_blocks + (q_tasks + kThreads - 1) / kThreads;
+    if (blocks > limit) return LAR_ERR_SHAPE;
+    return launch_ordered(append_step<F8, FAST>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, stream, p, static_cast<int>(kv_blocks), pages_of, hpt, q_tasks);
 }
 
 }  // namespace
