@@ -13,9 +13,10 @@
 // later is rescaled without loss but for codes that leave the normal range.
 //
 // Steps of T <= 16 tokens: a warp has a job, and the queries are blocks of their own.
-// Prompts: a block has the new tokens of a page for some heads and their queries, a thread
-// a token's 16 dimensions, whose angles it works out once for all of them; the greatest
-// magnitudes come first, and the second look at keys and values finds them in L1 or L2.
+// Prompts: a block has the new tokens of a page, with their angles in a table, and a warp a
+// head (or warps share one where heads are few); after the greatest magnitudes it comes for
+// keys and values again, which L2 still has.  The queries are blocks of their own here
+// too, a thread a token's unit, whose angles it works out once for several heads.
 #include <cuda_fp8.h>
 
 #include "layer_common.cuh"
@@ -25,13 +26,8 @@ namespace lar {
 
 namespace {
 
-#ifndef LAR_APPEND_MIN
-#define LAR_APPEND_MIN 2
-#endif
-#ifndef LAR_APPEND_THREADS
-#define LAR_APPEND_THREADS 256
-#endif
-constexpr int kThreads = LAR_APPEND_THREADS;
+constexpr int kThreads = 256;
+constexpr int kAtOnce = 4;   // queries' rows that are asked for together
 constexpr int kELo = -64, kEHi = 64;   // exponents of a scale
 
 // f / 2 pi in units of 2^-64 turns, whole turns dropped: f = m 2^e, m of 24 bits, times
@@ -86,6 +82,19 @@ __device__ __forceinline__ unsigned codes4(const float* x, float inv) {
     return r;
 }
 
+// the same of values that are known to be finite, or NaN
+__device__ __forceinline__ unsigned codes4_finite(const float* x, float inv) {
+    const f32x2 m = pack2(inv, inv);
+    float a, b, c, d;
+    unpack2(mul2(pack2(x[0], x[1]), m), a, b);
+    unpack2(mul2(pack2(x[2], x[3]), m), c, d);
+    unsigned r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
 // A unit is 16 dimensions of a row.  Fast rows take them in two vectors of 8, the members
 // of 8 pairs where they are rotated; other rows dimensions 16 u to 16 u + 15.
 struct Unit {
@@ -127,10 +136,11 @@ __device__ __forceinline__ void turn(const AppendParams& p, const Unit& un, cons
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float u = x[i], v = x[i + 8];
-            x[i] = fmaf(u, a.c[i], -(v * a.s[i]));
-            x[i + 8] = fmaf(v, a.c[i], u * a.s[i]);
+        for (int i = 0; i < 8; i += 2) {   // two pairs at once
+            const f32x2 u = pack2(x[i], x[i + 1]), v = pack2(x[i + 8], x[i + 9]);
+            const f32x2 c = pack2(a.c[i], a.c[i + 1]), s = pack2(a.s[i], a.s[i + 1]), m = pack2(-a.s[i], -a.s[i + 1]);
+            unpack2(fma2(u, c, mul2(v, m)), x[i], x[i + 1]);
+            unpack2(fma2(v, c, mul2(u, s)), x[i + 8], x[i + 9]);
         }
     }
 }
@@ -146,6 +156,13 @@ struct Raw {
     __device__ __forceinline__ void widen(float* x) const {
         unpack8(a, x);
         unpack8(b, x + 8);
+    }
+    // the greatest magnitude's bits (bf16 magnitudes are ordered as whole numbers), NaN apart
+    __device__ __forceinline__ unsigned top() const {
+        const unsigned m = 0x7fff7fffu;
+        unsigned t = __vmaxu2(__vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m)),
+                              __vmaxu2(__vmaxu2(b.x & m, b.y & m), __vmaxu2(b.z & m, b.w & m)));
+        return max(t >> 16, t & 0xffffu) << 16;
     }
 };
 
@@ -260,18 +277,17 @@ __device__ __forceinline__ void raise(float& top, const float* x) {
 }
 
 // The scale of a (page, head) whose new values have the greatest magnitude `top`: no less
-// than that of `first` tokens that stand before them, whose codes follow it.  Written by
-// thread 0 of the THR threads that share the job; returned inverted.
-template <int THR>
-__device__ __forceinline__ float rescale(const AppendParams& p, bool values, const Job& job, int h, float top, int me) {
-    float* at = values ? p.c.v_scale + job.id * p.c.vss[0] + h * p.c.vss[1] : p.c.k_scale + job.id * p.c.kss[0] + h * p.c.kss[1];
+// than that of `first` tokens that stand before them, whose codes follow it, by `count`
+// threads of which this is `me`.  The caller stores it once all of them have come here.
+__device__ __forceinline__ float rescale(const AppendParams& p, bool values, const Job& job, int h, float top, int me, int count) {
+    const float* at = values ? p.c.v_scale + job.id * p.c.vss[0] + h * p.c.vss[1] : p.c.k_scale + job.id * p.c.kss[0] + h * p.c.kss[1];
     const float was = job.first ? *at : 0.f, need = pow2(scale_exponent(top)), now = was > need ? was : need;
     if (job.first && now > was) {
         const float f = was / now;
         unsigned char* pg = static_cast<unsigned char*>(values ? p.c.v : p.c.k) + job.id * (values ? p.c.vs[0] : p.c.ks[0]) + h * (values ? p.c.vs[2] : p.c.ks[2]);
         const int64_t step = values ? p.c.vs[1] : p.c.ks[1];
         const int UN = p.c.D / 16;
-        for (int i = me; i < job.first * UN; i += THR) {
+        for (int i = me; i < job.first * UN; i += count) {
             uint4* to = reinterpret_cast<uint4*>(pg + i / UN * step + i % UN * 16);
             const uint4 old = *to;
             const unsigned in[4] = {old.x, old.y, old.z, old.w};
@@ -290,20 +306,23 @@ __device__ __forceinline__ float rescale(const AppendParams& p, bool values, con
             *to = make_uint4(out[0], out[1], out[2], out[3]);
         }
     }
-    if (THR > 32) __syncthreads();   // all have read the old scale
-    else __syncwarp();
-    if (me == 0) *at = now;
-    return 1.f / now;
+    return now;
 }
 
-template <bool F8>
+__device__ __forceinline__ void store_scales(const AppendParams& p, const Job& job, int h, float k, float v) {
+    p.c.k_scale[job.id * p.c.kss[0] + h * p.c.kss[1]] = k;
+    p.c.v_scale[job.id * p.c.vss[0] + h * p.c.vss[1]] = v;
+}
+
+template <bool F8, bool FINITE = false>
 __device__ __forceinline__ void put_unit(const AppendParams& p, bool values, const Job& job, int h, int t, const Unit& un, const float* x, float inv) {
     const int64_t row = values ? job.id * p.c.vs[0] + (job.first + t) * p.c.vs[1] + h * p.c.vs[2]
                                : job.id * p.c.ks[0] + (job.first + t) * p.c.ks[1] + h * p.c.ks[2];
     void* base = values ? p.c.v : p.c.k;
     if constexpr (F8) {
         unsigned char* to = static_cast<unsigned char*>(base) + row;
-        const uint2 a = make_uint2(codes4(x, inv), codes4(x + 4, inv)), b = make_uint2(codes4(x + 8, inv), codes4(x + 12, inv));
+        auto code = [&](const float* v) { return FINITE ? codes4_finite(v, inv) : codes4(v, inv); };
+        const uint2 a = make_uint2(code(x), code(x + 4)), b = make_uint2(code(x + 8), code(x + 12));
         if (un.d1 == un.d0 + 8) {
             *reinterpret_cast<uint4*>(to + un.d0) = make_uint4(a.x, a.y, b.x, b.y);
         } else {
@@ -341,8 +360,11 @@ __device__ __forceinline__ void step_job(const AppendParams& p, const unsigned l
         }
         ktop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(ktop)));
         vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
-        kinv = rescale<32>(p, false, job, h, ktop, me);
-        vinv = rescale<32>(p, true, job, h, vtop, me);
+        const float ks = rescale(p, false, job, h, ktop, me, 32), vs = rescale(p, true, job, h, vtop, me, 32);
+        __syncwarp();   // all have read the old ones
+        if (me == 0) store_scales(p, job, h, ks, vs);
+        kinv = 1.f / ks;
+        vinv = 1.f / vs;
     }
     const bool kept = F8 && tasks <= 32;   // still in registers
     for (int i = me; i < tasks; i += 32) {
@@ -352,122 +374,202 @@ __device__ __forceinline__ void step_job(const AppendParams& p, const unsigned l
     }
 }
 
-// A prompt's job for heads [h0, h1) and their queries, by a block
-constexpr int kJobHeads = 4;   // at most
-constexpr int kAtOnce = 4;     // queries' rows that are asked for together
+// A prompt's job for heads [h0, h1), by a block
+constexpr int kTable = 4096;   // angles of a table: 64 tokens of 64 pairs
+constexpr int kBatch = 4;      // units that a thread asks for together
+constexpr int kJobWarps = kThreads / 32;
 
-template <bool F8, bool FAST, bool BF>
-__device__ __forceinline__ void prompt_job(const AppendParams& p, const unsigned long long* steps, unsigned* top_s, int n, int j, int h0, int h1, int me,
-                                           int32_t* bits) {
-    Job job;
-    if (!job_of(p, n, j, job, bits)) return;
-    const int UN = p.c.D / 16, tasks = job.cnt * UN, G = p.q ? p.Hq / p.c.H : 0;
-    float inv[2 * kJobHeads];
-#pragma unroll
-    for (int e = 0; e < 2 * kJobHeads; ++e) inv[e] = 1.f;
-    Angles a;
-    float x[16];
-    // f(head of the job, whether it is the values') with the unit's keys, rotated, and values in x
-    auto rows_of = [&](int t, int u, auto f) {
-        const Unit ku = unit_of<FAST>(p, u, true), vu = {u * 16, u * 16 + 8, -1};
-        const int64_t krow = (job.tok + t) * p.ks[1], vrow = (job.tok + t) * p.vs[1];
-        if constexpr (BF) {
-#pragma unroll
-            for (int e = 0; e < kJobHeads; e += 2) {
-                Raw k[2], v[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (h0 + e + i < h1) {
-                        k[i].load(p.k, krow + (h0 + e + i) * p.ks[2], ku);
-                        v[i].load(p.v, vrow + (h0 + e + i) * p.vs[2], vu);
-                    }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (h0 + e + i < h1) {
-                        k[i].widen(x);
-                        turn(p, ku, a, x);
-                        f(e + i, false);
-                        v[i].widen(x);
-                        f(e + i, true);
-                    }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < kJobHeads; ++e)
-                if (h0 + e < h1) {
-                    load_unit<FAST>(p, steps, p.k, krow + (h0 + e) * p.ks[2], p.ks[3], p.k_dt, ku, a, job.place + t, true, x);
-                    f(e, false);
-                    load_unit<FAST>(p, steps, p.v, vrow + (h0 + e) * p.vs[2], p.vs[3], p.v_dt, vu, a, job.place + t, false, x);
-                    f(e, true);
-                }
-        }
-    };
-    const bool one = tasks <= kThreads;   // each thread has one token's unit, and its angles
-    if (one && me < tasks) angles_of<FAST>(p, steps, unit_of<FAST>(p, me % UN, true), job.place + me / UN, a);
-    if (F8 && job.id >= 0) {
-        float top[2 * kJobHeads];
-#pragma unroll
-        for (int e = 0; e < 2 * kJobHeads; ++e) top[e] = 0.f;
-        for (int i = me; i < tasks; i += kThreads) {
-            const int t = i / UN, u = i % UN;
-            if (!one) angles_of<FAST>(p, steps, unit_of<FAST>(p, u, true), job.place + t, a);
-            rows_of(t, u, [&](int e, bool values) { raise(top[2 * e + values], x); });
-        }
-        if (me < 2 * kJobHeads) top_s[me] = 0u;
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 2 * kJobHeads; ++e) {
-            const unsigned v = __reduce_max_sync(0xffffffffu, __float_as_uint(top[e]));
-            if (me % 32 == 0 && v) atomicMax(&top_s[e], v);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < kJobHeads; ++e)
-            if (h0 + e < h1) {
-                inv[2 * e] = rescale<kThreads>(p, false, job, h0 + e, __uint_as_float(top_s[2 * e]), me);
-                inv[2 * e + 1] = rescale<kThreads>(p, true, job, h0 + e, __uint_as_float(top_s[2 * e + 1]), me);
-            }
+// Where a token's pairs 8 u + 2 i and 8 u + 2 i + 1 lie, in pairs of cosine and sine: neighbouring units side by side
+__device__ __forceinline__ int table_at(const AppendParams& p, int t, int u, int i) { return ((t * 4 + i) * (p.rot / 16) + u) * 2; }
+
+__device__ __forceinline__ void fill_table(const AppendParams& p, const unsigned long long* steps, float2* table, const Job& job, int me) {
+    const int half = p.rot / 2;
+    for (int i = me; i < job.cnt * half; i += kThreads) {
+        const int t = i / half, pair = i % half;
+        float c, s;
+        cos_sin(steps[pair] * static_cast<unsigned long long>(job.place + t), c, s);
+        table[table_at(p, t, pair / 8, pair % 8 / 2) + pair % 2] = make_float2(c * p.rope_scale, s * p.rope_scale);
     }
-    for (int i = me; i < tasks; i += kThreads) {
+    __syncthreads();
+}
+
+__device__ __forceinline__ void from_table(const AppendParams& p, const float2* table, const Unit& un, int t, Angles& a) {
+    if (un.pair < 0) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(table + table_at(p, t, un.pair / 8, i));
+        a.c[2 * i] = v.x;
+        a.s[2 * i] = v.y;
+        a.c[2 * i + 1] = v.z;
+        a.s[2 * i + 1] = v.w;
+    }
+}
+
+// Rows of any type and layout, one unit after another: f(values, t, unit, x) for `mine` of
+// `count` threads that share a head.
+template <bool FAST, typename F>
+__device__ __forceinline__ void any_rows(const AppendParams& p, const unsigned long long* steps, const Job& job, int h, int mine, int count, F f) {
+    const int UN = p.c.D / 16, tasks = job.cnt * UN;
+#pragma unroll 1
+    for (int i = mine; i < tasks; i += count) {
         const int t = i / UN, u = i % UN;
-        const Unit un = unit_of<FAST>(p, u, true);
-        if (!one) angles_of<FAST>(p, steps, un, job.place + t, a);
-        if (job.id >= 0) {
-            rows_of(t, u, [&](int e, bool values) {
-                put_unit<F8>(p, values, job, h0 + e, t, values ? Unit{u * 16, u * 16 + 8, -1} : un, x, inv[2 * e + values]);
-            });
+        const Unit ku = unit_of<FAST>(p, u, true), vu = {u * 16, u * 16 + 8, -1};
+        Angles a;
+        angles_of<FAST>(p, steps, ku, job.place + t, a);
+        float x[16];
+        load_unit<FAST>(p, steps, p.k, (job.tok + t) * p.ks[1] + h * p.ks[2], p.ks[3], p.k_dt, ku, a, job.place + t, true, x);
+        f(false, t, ku, x);
+        load_unit<FAST>(p, steps, p.v, (job.tok + t) * p.vs[1] + h * p.vs[2], p.vs[3], p.v_dt, vu, a, job.place + t, false, x);
+        f(true, t, vu, x);
+    }
+}
+
+template <bool FAST>
+__device__ __noinline__ void any_tops(const AppendParams& p, const unsigned long long* steps, const Job& job, int h, int mine, int count, float* top) {
+    any_rows<FAST>(p, steps, job, h, mine, count, [&](bool values, int, const Unit&, const float* x) { raise(top[values], x); });
+}
+
+template <bool F8, bool FAST>
+__device__ __noinline__ void any_put(const AppendParams& p, const unsigned long long* steps, const Job& job, int h, int mine, int count, float kinv, float vinv) {
+    any_rows<FAST>(p, steps, job, h, mine, count,
+                   [&](bool values, int t, const Unit& un, const float* x) { put_unit<F8>(p, values, job, h, t, un, x, values ? vinv : kinv); });
+}
+
+// bf16 rows that 16-byte loads fit, several asked for at once: f(t, unit, x) with keys rotated,
+// or g(raw) alone where RAW
+template <bool VALUES, bool RAW, typename A, typename F>
+__device__ __forceinline__ void rows(const AppendParams& p, const Job& job, int h, int mine, int count, A angles, F f) {
+    const int UN = p.c.D / 16, tasks = job.cnt * UN;
+    const unsigned short* base = static_cast<const unsigned short*>(VALUES ? p.v : p.k) + (VALUES ? job.tok * p.vs[1] + h * p.vs[2] : job.tok * p.ks[1] + h * p.ks[2]);
+    const int64_t step = VALUES ? p.vs[1] : p.ks[1];
+#pragma unroll 1
+    for (int i0 = mine; i0 < tasks; i0 += count * kBatch) {
+        Raw r[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+            const int i = min(i0 + e * count, tasks - 1);   // the last ones again, to no effect
+            r[e].load(base, i / UN * step, unit_of<true>(p, i % UN, !VALUES));
         }
-        const int64_t qrow = (job.tok + t) * p.qs[1], orow = (job.tok + t) * p.os[1];
-        if constexpr (BF) {
-            for (int h = h0 * G; h < h1 * G; h += kAtOnce) {
-                Raw r[kAtOnce];
 #pragma unroll
-                for (int e = 0; e < kAtOnce; ++e)
-                    if (h + e < h1 * G) r[e].load(p.q, qrow + (h + e) * p.qs[2], un);
-#pragma unroll
-                for (int e = 0; e < kAtOnce; ++e)
-                    if (h + e < h1 * G) {
-                        r[e].widen(x);
-                        turn(p, un, a, x);
-                        put_query<FAST>(p, orow + (h + e) * p.os[2], un, x);
-                    }
-            }
-        } else {
-            for (int h = h0 * G; h < h1 * G; ++h) {
-                load_unit<FAST>(p, steps, p.q, qrow + h * p.qs[2], p.qs[3], p.q_dt, un, a, job.place + t, true, x);
-                put_query<FAST>(p, orow + h * p.os[2], un, x);
+        for (int e = 0; e < kBatch; ++e) {
+            const int i = min(i0 + e * count, tasks - 1), t = i / UN;
+            if constexpr (RAW) {
+                f(r[e]);
+            } else {
+                const Unit un = unit_of<true>(p, i % UN, !VALUES);
+                float x[16];
+                r[e].widen(x);
+                if (!VALUES) {
+                    Angles a;
+                    angles(un, t, a);
+                    turn(p, un, a, x);
+                }
+                f(t, un, x);
             }
         }
     }
 }
 
-// A step's rotated queries: a thread a (token, unit), for `hpt` heads
-template <bool FAST>
+template <bool F8, bool FAST, bool BF>
+__device__ __forceinline__ void prompt_job(const AppendParams& p, const unsigned long long* steps, float2* table, unsigned (*top_s)[2], int n, int j, int h0,
+                                           int h1, int me, int32_t* bits) {
+    Job job;
+    if (!job_of(p, n, j, job, bits) || job.id < 0) return;   // the whole block
+    const int lane = me % 32, warp = me / 32;
+    const bool tab = BF && job.cnt * (p.rot / 2) <= kTable;
+    if (tab) fill_table(p, steps, table, job, me);
+    int side = kJobWarps;   // heads side by side
+    while (side / 2 >= h1 - h0) side /= 2;
+    const int slot = warp % side, part = warp / side, count = kJobWarps / side * 32, mine = part * 32 + lane;   // this thread's place among a head's
+    auto angles = [&](const Unit& un, int t, Angles& a) {
+        if (tab) from_table(p, table, un, t, a);
+        else angles_of<FAST>(p, steps, un, job.place + t, a);
+    };
+#pragma unroll 1
+    for (int base = h0; base < h1; base += side) {
+        const int h = base + slot;
+        const bool on = h < h1;
+        float kinv = 1.f, vinv = 1.f;
+        bool finite = true;
+        if constexpr (F8) {
+            auto share = [&](unsigned k, unsigned v) {   // the head's greatest, in top_s
+                __syncthreads();   // it is read no more
+                if (me < 2 * kJobWarps) top_s[me / 2][me % 2] = 0u;
+                __syncthreads();
+                k = __reduce_max_sync(0xffffffffu, k);
+                v = __reduce_max_sync(0xffffffffu, v);
+                if (lane == 0) {
+                    atomicMax(&top_s[slot][0], k);
+                    atomicMax(&top_s[slot][1], v);
+                }
+                __syncthreads();
+            };
+            if constexpr (BF) {
+                // infinities and NaN show as the greatest bits; where there are any, once more without them
+                float top = 0.f;
+                bool nan = false;
+                unsigned vtop = 0;
+                if (on) {
+                    rows<false, false>(p, job, h, mine, count, angles, [&](int, const Unit&, const float* x) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            top = fmaxf(top, fabsf(x[q]));
+                            nan |= x[q] != x[q];
+                        }
+                    });
+                    rows<true, true>(p, job, h, mine, count, angles, [&](const Raw& r) { vtop = max(vtop, r.top()); });
+                }
+                share(nan ? 0x7fffffffu : __float_as_uint(top), vtop);
+#pragma unroll
+                for (int e = 0; e < kJobWarps; ++e) finite &= max(top_s[e][0], top_s[e][1]) < 0x7f800000u;
+            }
+            if (!BF || !finite) {
+                float top[2] = {0.f, 0.f};
+                if (on) any_tops<FAST>(p, steps, job, h, mine, count, top);
+                share(__float_as_uint(top[0]), __float_as_uint(top[1]));
+            }
+            if (on) {
+                kinv = rescale(p, false, job, h, __uint_as_float(top_s[slot][0]), mine, count);
+                vinv = rescale(p, true, job, h, __uint_as_float(top_s[slot][1]), mine, count);
+            }
+            __syncthreads();   // all have read the old scales
+            if (on && mine == 0) store_scales(p, job, h, kinv, vinv);
+            kinv = 1.f / kinv;
+            vinv = 1.f / vinv;
+        }
+        if (!on) continue;
+        if (BF && finite) {
+            rows<false, false>(p, job, h, mine, count, angles, [&](int t, const Unit& un, const float* x) { put_unit<F8, true>(p, false, job, h, t, un, x, kinv); });
+            rows<true, false>(p, job, h, mine, count, angles, [&](int t, const Unit& un, const float* x) { put_unit<F8, true>(p, true, job, h, t, un, x, vinv); });
+        } else {
+            any_put<F8, FAST>(p, steps, job, h, mine, count, kinv, vinv);
+        }
+    }
+}
+
+// Rotated queries: a thread a (token, unit), for `hpt` heads
+template <bool FAST, bool BF>
 __device__ __forceinline__ void q_task(const AppendParams& p, const unsigned long long* steps, int64_t task, int hpt) {
     const int UN = p.c.D / 16, chunks = (p.Hq + hpt - 1) / hpt;
     const int u = static_cast<int>(task % UN), ch = static_cast<int>(task / UN % chunks);
     const int64_t tok = task / UN / chunks;
-    const int n = static_cast<int>(tok / p.T), t = static_cast<int>(tok % p.T);
+    int n, t;
+    int64_t qrow, orow;
+    if (p.cu) {
+        n = last_at_most(p.n, tok, [&](int i) { return ld_idx(p.cu, i * p.cu_s, p.cu_dt); });
+        int begin, len;
+        int32_t bits = 0;   // flagged by the jobs
+        span(p, n, &begin, &len, &bits);
+        if (tok < begin || tok >= begin + len) return;
+        t = static_cast<int>(tok) - begin;
+        qrow = tok * p.qs[1];
+        orow = tok * p.os[1];
+    } else {
+        n = static_cast<int>(tok / p.T);
+        t = static_cast<int>(tok % p.T);
+        qrow = n * p.qs[0] + t * p.qs[1];
+        orow = n * p.os[0] + t * p.os[1];
+    }
     const int64_t start = length_of(p, n);
     if (start < 0) return;
     const int place = static_cast<int>(start) + t;
@@ -475,10 +577,26 @@ __device__ __forceinline__ void q_task(const AppendParams& p, const unsigned lon
     Angles a;
     angles_of<FAST>(p, steps, un, place, a);
     const int h1 = min(p.Hq, (ch + 1) * hpt);
-    for (int h = ch * hpt; h < h1; ++h) {
-        float x[16];
-        load_unit<FAST>(p, steps, p.q, n * p.qs[0] + t * p.qs[1] + h * p.qs[2], p.qs[3], p.q_dt, un, a, place, true, x);
-        put_query<FAST>(p, n * p.os[0] + t * p.os[1] + h * p.os[2], un, x);
+    float x[16];
+    if constexpr (BF) {
+        for (int h = ch * hpt; h < h1; h += kAtOnce) {
+            Raw r[kAtOnce];
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e)
+                if (h + e < h1) r[e].load(p.q, qrow + (h + e) * p.qs[2], un);
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e)
+                if (h + e < h1) {
+                    r[e].widen(x);
+                    turn(p, un, a, x);
+                    put_query<FAST>(p, orow + (h + e) * p.os[2], un, x);
+                }
+        }
+    } else {
+        for (int h = ch * hpt; h < h1; ++h) {
+            load_unit<FAST>(p, steps, p.q, qrow + h * p.qs[2], p.qs[3], p.q_dt, un, a, place, true, x);
+            put_query<FAST>(p, orow + h * p.os[2], un, x);
+        }
     }
 }
 
@@ -497,7 +615,7 @@ __global__ void __launch_bounds__(kThreads) append_step(const __grid_constant__ 
     int32_t bits = 0;
     if (static_cast<int>(blockIdx.x) >= kv_blocks) {
         const int64_t task = static_cast<int64_t>(blockIdx.x - kv_blocks) * kThreads + tid;
-        if (task < q_tasks) q_task<FAST>(p, steps, task, hpt);
+        if (task < q_tasks) q_task<FAST, false>(p, steps, task, hpt);
     } else {
         const int64_t job = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + tid / 32;
         const int h = static_cast<int>(job % p.c.H), j = static_cast<int>(job / p.c.H % pages_of);
@@ -507,52 +625,62 @@ __global__ void __launch_bounds__(kThreads) append_step(const __grid_constant__ 
     flag_err(p.dev_err, bits);
 }
 
-// A block a job: sequence n's pages have numbers from cu[n] / page + 2 n on
+// Blocks [0, kv_blocks): jobs, where sequence n's pages have numbers from cu[n] / page + 2 n
+// on; the others: queries
 template <bool F8, bool FAST, bool BF>
-__global__ void __launch_bounds__(kThreads, LAR_APPEND_MIN) append_prompt(const __grid_constant__ AppendParams p, int groups, int heads) {
+__global__ void __launch_bounds__(kThreads, 2) append_prompt(const __grid_constant__ AppendParams p, int kv_blocks, int groups, int heads, int hpt,
+                                                                          int64_t q_tasks) {
     __shared__ unsigned long long steps[128];
-    __shared__ unsigned top_s[2 * kJobHeads];
+    __shared__ unsigned top_s[kJobWarps][2];
+    __shared__ alignas(16) float2 table[FAST ? kTable : 1];
     stream_order();
     load_steps(p, steps);
     int32_t bits = 0;
+    if (static_cast<int>(blockIdx.x) >= kv_blocks) {
+        const int64_t task = static_cast<int64_t>(blockIdx.x - kv_blocks) * kThreads + threadIdx.x;
+        if (task < q_tasks) q_task<FAST, BF>(p, steps, task, hpt);
+        return;
+    }
     const int h0 = static_cast<int>(blockIdx.x % groups) * heads;
     const int64_t unit = blockIdx.x / groups;
     auto key = [&](int i) { return ld_idx(p.cu, i * p.cu_s, p.cu_dt) / p.c.page + 2 * static_cast<int64_t>(i); };
     const int n = last_at_most(p.n, unit, key);
     const int64_t j = unit - key(n);
-    if (j >= 0 && j < (1 << 30)) prompt_job<F8, FAST, BF>(p, steps, top_s, n, static_cast<int>(j), h0, min(p.c.H, h0 + heads), threadIdx.x, &bits);
+    if (j >= 0 && j < (1 << 30)) prompt_job<F8, FAST, BF>(p, steps, table, top_s, n, static_cast<int>(j), h0, min(p.c.H, h0 + heads), threadIdx.x, &bits);
     flag_err(p.dev_err, bits);
 }
 
 template <bool F8, bool FAST>
 lar_status launch(const AppendParams& p, cudaStream_t stream) {
     const int64_t limit = (int64_t{1} << 31) - 1;
+    const int64_t tokens = p.cu ? p.ntok : static_cast<int64_t>(p.n) * p.T;
+    int64_t q_tasks = 0;
+    int hpt = 1;   // heads share their angles where there are threads enough without
+    if (p.q) {
+        const int64_t units = tokens * (p.c.D / 16) * p.Hq;
+        while (hpt < 32 && hpt < p.Hq && units / (2 * hpt) >= 152 * 1024) hpt *= 2;
+        q_tasks = tokens * (p.c.D / 16) * ((p.Hq + hpt - 1) / hpt);
+    }
+    const int64_t q_blocks = (q_tasks + kThreads - 1) / kThreads;
     if (p.cu) {
         const int64_t pages = p.ntok / p.c.page + 2 * static_cast<int64_t>(p.n);
-        // heads share their angles where there are blocks enough without
-        int heads = 1;
-        while (heads < kJobHeads && 2 * heads <= p.c.H && pages * p.c.H >= 152 * 8 * heads) heads *= 2;
+        int heads = 1;   // likewise
+        while (heads < 8 && heads < p.c.H && pages * p.c.H >= 152 * 2 * heads) heads *= 2;
         const int64_t groups = (p.c.H + heads - 1) / heads;
-        if (pages * groups > limit) return LAR_ERR_SHAPE;
-        const dim3 grid(static_cast<unsigned>(pages * groups));
+        if (pages * groups + q_blocks > limit) return LAR_ERR_SHAPE;
+        const dim3 grid(static_cast<unsigned>(pages * groups + q_blocks));
+        const int kv = static_cast<int>(pages * groups), gr = static_cast<int>(groups);
         const bool bf = p.k_dt == LAR_BF16 && p.v_dt == LAR_BF16 && (!p.q || p.q_dt == LAR_BF16);
         if constexpr (FAST) {
-            if (bf) return launch_ordered(append_prompt<F8, true, true>, grid, kThreads, 0, 1, stream, p, static_cast<int>(groups), heads);
+            if (bf) return launch_ordered(append_prompt<F8, true, true>, grid, kThreads, 0, 1, stream, p, kv, gr, heads, hpt, q_tasks);
         }
-        return launch_ordered(append_prompt<F8, FAST, false>, grid, kThreads, 0, 1, stream, p, static_cast<int>(groups), heads);
-    }
-    const int64_t tokens = static_cast<int64_t>(p.n) * p.T;
-    int64_t q_tasks = 0;
-    int hpt = 1;
-    if (p.q) {
-        while (hpt < 8 && hpt < p.Hq && tokens * (p.c.D / 16) * p.Hq / (2 * hpt) >= 152 * 2048) hpt *= 2;
-        q_tasks = tokens * (p.c.D / 16) * ((p.Hq + hpt - 1) / hpt);
+        return launch_ordered(append_prompt<F8, FAST, false>, grid, kThreads, 0, 1, stream, p, kv, gr, heads, hpt, q_tasks);
     }
     const int pages_of = p.T == 1 ? 1 : 2;
     const int64_t kv_blocks = (static_cast<int64_t>(p.n) * pages_of * p.c.H + kThreads / 32 - 1) / (kThreads / 32);
-    const int64_t blocks = kv_blocks + (q_tasks + kThreads - 1) / kThreads;
-    if (blocks > limit) return LAR_ERR_SHAPE;
-    return launch_ordered(append_step<F8, FAST>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, stream, p, static_cast<int>(kv_blocks), pages_of, hpt, q_tasks);
+    if (kv_blocks + q_blocks > limit) return LAR_ERR_SHAPE;
+    return launch_ordered(append_step<F8, FAST>, dim3(static_cast<unsigned>(kv_blocks + q_blocks)), kThreads, 0, 1, stream, p, static_cast<int>(kv_blocks), pages_of,
+                          hpt, q_tasks);
 }
 
 }  // namespace

@@ -45,32 +45,14 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxBlocks = 608;    // of a call: bounds the workspace
-#ifndef LAR_ATTN_STAGES
-#define LAR_ATTN_STAGES 2
-#endif
 
 constexpr float kLn2 = 0.6931471805599453f;
-#ifndef LAR_ATTN_START
-#define LAR_ATTN_START 16
-#endif
-constexpr int kStart = LAR_ATTN_START;   // tiles that a pair's beginning and end count as
+constexpr int kStart = 16;   // tiles that a pair's beginning and end count as
 constexpr float kSlack = 8.f;      // a weight may grow to 2^8 before the sums are scaled down
 
-#ifndef LAR_ATTN_QREG
-#define LAR_ATTN_QREG 256
-#endif
-#ifndef LAR_ATTN_BLOCKS2
-#define LAR_ATTN_BLOCKS2 2
-#endif
-#ifndef LAR_ATTN_TILE
-#define LAR_ATTN_TILE 8192
-#endif
-#ifndef LAR_ATTN_BLOCKS
-#define LAR_ATTN_BLOCKS 3
-#endif
-// Tokens of a warp's tile: 8 KB of keys and values, at least a granule of 16.
+// Tokens of a warp's tile: 4 KB of keys and values, at least a granule of 16.
 constexpr int tile_tokens(int D, bool f8) {
-    const int t = LAR_ATTN_TILE / (2 * D * (f8 ? 1 : 2));
+    const int t = 4096 / (2 * D * (f8 ? 1 : 2));
     return t > 32 ? 32 : t < 16 ? 16 : t;
 }
 
@@ -84,7 +66,7 @@ struct Shape {
     static constexpr int ROW = D * ES;                 // bytes of a token's row
     static constexpr int CH = ROW / 16;                // its 16-byte chunks
     static constexpr int TILE = WT * ROW;              // bytes of a tile's keys
-    static constexpr int STAGES = LAR_ATTN_STAGES;
+    static constexpr int STAGES = 2;
     static constexpr int RING = STAGES * 2 * TILE;     // a warp's
     static constexpr int KS = D / 16;                  // steps of the first product
     static constexpr int MT = D / 16;                  // row tiles of the second
@@ -94,8 +76,8 @@ struct Shape {
     static constexpr int JOIN = kWarps * PART * 4;
     static constexpr int BODY = kWarps * RING > JOIN ? kWarps * RING : JOIN;
     static constexpr int SMEM = BODY + QF + ROWS * 4;
-    static constexpr bool QREG = D * NR <= LAR_ATTN_QREG;        // fragments stay in registers
-    static constexpr int BLOCKS = D * NR <= 128 ? LAR_ATTN_BLOCKS : D * NR <= 256 ? LAR_ATTN_BLOCKS2 : 2;   // an SM, by registers
+    static constexpr bool QREG = D * NR <= 128 || (D == 256 && NR == 1);        // fragments stay in registers
+    static constexpr int BLOCKS = D < 256 && D * NR <= 256 ? 3 : 2;   // an SM, by registers
 };
 
 __device__ __forceinline__ void cp16_zfill(unsigned dst, const void* src, bool take) {

@@ -34,10 +34,7 @@ namespace {
 
 using u64 = unsigned long long;
 
-#ifndef LAR_SAMPLE_THREADS
-#define LAR_SAMPLE_THREADS 512
-#endif
-constexpr int kThreads = LAR_SAMPLE_THREADS;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kStep = 256;       // tokens of a warp's step, 8 a lane
