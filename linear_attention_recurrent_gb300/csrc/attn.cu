@@ -47,7 +47,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxBlocks = 608;    // of a call: bounds the workspace
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kStart = 16;   // tiles that a pair's beginning and end count as
+constexpr int kStart = 20;   // tiles that a pair's beginning and end count as
 constexpr float kSlack = 8.f;      // a weight may grow to 2^8 before the sums are scaled down
 
 // Tokens of a warp's tile: 4 KB of keys and values, at least a granule of 16.
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) top = max(top, max(xq[e][i] & 0x7fffu, xq[e][i] >> 16 & 0x7fffu));
                 const int x = static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7);   // biased exponent
-                if (x > 15 && x < 240) {
+                if (x > 15 && x < 255) {
                     mul = __uint_as_float(static_cast<unsigned>(254 + 14 - x) << 23);
                     back = __uint_as_float(static_cast<unsigned>(x - 14) << 23);
                 }

@@ -122,6 +122,19 @@ def test_sharp_and_flat_rows(cuda_device):
     check(s)
 
 
+@pytest.mark.parametrize("cache", [F8, BF16])
+def test_range_of_queries(cache, cuda_device):
+    """Queries near both ends of what bf16 holds, with a scale that brings the scores back: powers
+    of two change nothing."""
+    s = make(cuda_device, 33, [70, 9], 1, 4, 2, 64, 16, cache)
+    want, _ = check(s)
+    q = s["q"].clone()
+    for e in (-100, 60, 120):
+        s["q"] = (q.float() * 2.0 ** e).to(BF16)
+        out = call(s, scale=64 ** -0.5 * 2.0 ** -e)
+        assert torch.equal(out, want), e
+
+
 def test_scales_of_pages(cuda_device):
     """Pages of one sequence whose scales differ by 2^20, and scales that are no powers of two."""
     for kind in ("far", "odd"):
