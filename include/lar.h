@@ -13,8 +13,10 @@
  * kda_decode_varlen, la_decode_varlen) and the chunked form of the latter for
  * long spans (gdn_prefill, kda_prefill, la_prefill).  Around them stand the short
  * causal convolution in front of such a layer (conv_*), a further recurrent form,
- * the selective state space scan (ssm_*), and the verification of drafted tokens
- * that makes the accepted counts (spec_verify).  The chunked calls also set their
+ * the selective state space scan (ssm_*), the verification of drafted tokens
+ * that makes the accepted counts (spec_verify), the draw of the tokens themselves
+ * (sample_tokens), and, for the softmax-attention layers of hybrid models, a paged
+ * key/value cache (kv_append) and the attention over it (attn_decode).  The chunked calls also set their
  * kernel's shared-memory limit (a function attribute) on every call; capturing
  * them into a CUDA graph has not been tested (the other calls' capture and
  * replay are).
@@ -500,9 +502,9 @@ lar_status spec_verify(const lar_tensor* draft_tokens, const lar_tensor* draft_p
  *            or of no sequence, are left as they were.
  *   inv_freq fp32 [rot / 2], rot to D: pair i of dimensions (x, y) of a token at place t
  *            becomes rope_scale (x cos a - y sin a, y cos a + x sin a), a = t inv_freq[i]
- *            (its whole turns dropped before it is rounded, so far places are as exact as near ones;
- *            frequencies to 2^60).  Dimensions
- *            from rot on are copied.  NULL: no rotation (then no flags, rope_scale 1).
+ *            (its whole turns are dropped before it is rounded, so far places are as exact
+ *            as near ones; frequencies to 2^60).  Dimensions from rot on are copied.  NULL:
+ *            no rotation (then no flags, rope_scale 1).
  * e4m3: the scale is a power of two, 2^-64 to 2^64: the least with |x| <= 448 scale for the
  * values that enter a (page, head) in this call, and no less than that of the tokens that
  * stand before them in the page; if those have a smaller one, their codes are rounded to the
@@ -567,8 +569,10 @@ lar_status attn_decode(const lar_tensor* q, const lar_tensor* k_cache, const lar
  *   tokens   out, int32 or int64 [B, T] (rank 1 for T = 1).
  *   probs    out, fp32 [B, T, V] (rank 2) or NULL.
  * Any strides (outputs: no two elements at one address).  Weights are held to 2^-30 of
- * themselves or 2^-40 of the greatest, sums exactly: the token is the one that exact
- * arithmetic gives unless u or a threshold is as near as that to a border.
+ * themselves or V 2^-62 of the greatest, sums exactly: the token is the one that exact
+ * arithmetic gives unless u or a threshold is as near as that to a border.  Fastest are
+ * top_k up to a thousand or so, and temperatures alone; top_p without top_k takes about
+ * twice as long, and rows of few different logits several times.
  */
 lar_status sample_tokens(const lar_tensor* logits, const lar_tensor* u, const lar_tensor* temperature,
                          const lar_tensor* top_k, const lar_tensor* top_p, const lar_tensor* min_p,

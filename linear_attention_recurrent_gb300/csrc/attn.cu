@@ -322,12 +322,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
                             kp += k_step;
                             vp += v_step;
                         }
-                    } else {   // zeros where there is nothing to see
+                    } else {   // zeros where there is nothing to see (there may be no page at all: any address will do)
+                        const char* const nowhere = reinterpret_cast<const char*>(p.ws);
                         for (int j = 0; j < CH / 2; ++j) {
                             const int row = gr * 16 + row_l + j * RS, at = pos + row;
                             const bool take = ka >= 0 && at >= seen.lo && at < seen.hi;
-                            cp16_zfill(dst + place<CH, true>(row, c_l), take ? kp : static_cast<const char*>(p.c.k), take);
-                            cp16_zfill(dst + S::TILE + place<CH, false>(row, c_l), take ? vp : static_cast<const char*>(p.c.v), take);
+                            cp16_zfill(dst + place<CH, true>(row, c_l), take ? kp : nowhere, take);
+                            cp16_zfill(dst + S::TILE + place<CH, false>(row, c_l), take ? vp : nowhere, take);
                             kp += k_step;
                             vp += v_step;
                         }

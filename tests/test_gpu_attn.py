@@ -200,6 +200,21 @@ def test_no_sequence_no_page(cache, cuda_device):
     assert int(err) & lar.LAR_DEVERR_SEQLEN
 
 
+@pytest.mark.parametrize("cache", [F8, BF16])
+def test_no_pages_at_all(cache, cuda_device):
+    """An empty pool, and a table without columns: nothing is seen."""
+    dev = cuda_device
+    s = make(dev, 34, [40, 3], 2, 4, 2, 64, 16, cache)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    none = {n: s[n][:0] for n in ("k_cache", "v_cache", "k_scale", "v_scale") if n in s}
+    lse = torch.zeros(2, 2, 4, device=dev)
+    out = call(dict(s, **none), k_scale=none.get("k_scale"), v_scale=none.get("v_scale"), lse=lse, dev_err=err)
+    assert bool((out == 0).all() and (lse == -float("inf")).all()) and int(err) == lar.LAR_DEVERR_PAGE
+    err.zero_()
+    out = call(dict(s, table=s["table"][:, :0]), lse=lse, dev_err=err)
+    assert bool((out == 0).all() and (lse == -float("inf")).all()) and int(err) == lar.LAR_DEVERR_SEQLEN
+
+
 def test_layouts_and_types(cuda_device):
     """Strided queries and outputs, heads-first pages, halves of one buffer, 64-bit indices,
     fp32 outputs, a workspace of the caller's: the same numbers."""
