@@ -739,7 +739,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
             bound = static_cast<unsigned>(s.found[0]);
         }
         n_list = kList + 1;
-        if (bound > kLeast || row.V <= kList) {
+        if (k <= groups || row.V <= kList) {
+            // fewer maxima than k above -infinity, as a mask leaves: all logits above it
+            if (k <= groups) bound = max(bound, kLeast + 1);
             const float least_x = of_key(bound);
             for (int st = s0; st < s1; ++st) {
                 float x[8], high = -INFINITY;
@@ -757,7 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         list_low = bound;
         if (n_list <= kList) {
             if (c.rank == 0) {
-                cut_list(static_cast<u64>(k), one);
+                if (n_list > static_cast<u64>(k)) cut_list(static_cast<u64>(k), one);
+                else cut = {bound, row.V};
                 if (top_p < 1.f) {
                     u64 w = 0;
                     of_list([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });

@@ -148,6 +148,22 @@ def test_edges_of_logits(cuda_device):
     check(dev, x, u, temperature=torch.zeros(10))
 
 
+def test_masked_vocabularies(cuda_device):
+    """A grammar's few tokens among many: fewer logits above -infinity than top_k, as many, more;
+    side by side and spread."""
+    for V in (5000, 40000):
+        x, u, g = rows(48, 9, 1, V)
+        for b, n in enumerate((1, 2, 49, 50, 51, 400, 1999, 2100, V)):
+            keep = torch.randperm(V, generator=g)[:n] if b % 2 else torch.arange(V // 3, min(V, V // 3 + n))
+            y = torch.full((V,), -float("inf"))
+            y[keep] = x[b, 0, keep]
+            x[b, 0] = y
+        for k in (50, 1000):
+            check(cuda_device, x, u, top_k=torch.full((9,), k))
+            check(cuda_device, x, u, top_k=torch.full((9,), k), top_p=torch.full((9,), 0.8), min_p=torch.full((9,), 0.01))
+        check(cuda_device, x, u, top_p=torch.full((9,), 0.95))
+
+
 def test_wide_spread(cuda_device):
     """Logits over many orders of magnitude, where bins of keys and of weights differ most."""
     g = torch.Generator().manual_seed(42)
