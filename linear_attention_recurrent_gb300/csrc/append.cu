@@ -244,10 +244,9 @@ struct Job {
 };
 
 // false: no tokens there
-__device__ __forceinline__ bool job_of(const AppendParams& p, int n, int j, Job& job, int32_t* bits) {
+__device__ __forceinline__ bool job_of(const AppendParams& p, int n, int j, int64_t start, Job& job, int32_t* bits) {
     int begin, len;
     span(p, n, &begin, &len, bits);
-    const int64_t start = length_of(p, n);
     if (start < 0 || len == 0) return false;
     const int page = p.c.page;
     const int64_t pg = start / page + j;                                // page of the sequence
@@ -335,11 +334,78 @@ __device__ __forceinline__ void put_unit(const AppendParams& p, bool values, con
     }
 }
 
+// A step's job for one head, by a warp, where its lanes can hold all of the step's tokens: the
+// rows are asked for before the sequence's length and the page are known
+constexpr int kStepUnits = 2;   // of a lane
+
+struct StepRows {
+    Raw k[kStepUnits], v[kStepUnits];
+    int64_t start;   // the sequence's length
+
+    __device__ __forceinline__ void load(const AppendParams& p, int n, int h, int me) {
+        const int UN = p.c.D / 16, tasks = p.T * UN;
+        start = length_of(p, n);
+#pragma unroll
+        for (int e = 0; e < kStepUnits; ++e) {
+            const int i = me + e * 32, t = i / UN, u = i % UN;
+            if (i >= tasks) continue;
+            k[e].load(p.k, n * p.ks[0] + t * p.ks[1] + h * p.ks[2], unit_of<true>(p, u, true));
+            v[e].load(p.v, n * p.vs[0] + t * p.vs[1] + h * p.vs[2], {u * 16, u * 16 + 8, -1});
+        }
+    }
+};
+
+template <bool F8>
+__device__ __forceinline__ void step_job_bf16(const AppendParams& p, const unsigned long long* steps, const StepRows& rows, int n, int j, int h, int me,
+                                              int32_t* bits) {
+    const int UN = p.c.D / 16, tasks = p.T * UN;
+    const Raw (&k)[kStepUnits] = rows.k, (&v)[kStepUnits] = rows.v;
+    Job job;
+    if (!job_of(p, n, j, rows.start, job, bits) || job.id < 0) return;
+    float x[kStepUnits][16];
+    float ktop = 0.f, vtop = 0.f;
+#pragma unroll
+    for (int e = 0; e < kStepUnits; ++e) {
+        const int i = me + e * 32, t = i / UN - job.tok;   // among the page's tokens
+        if (i >= tasks || t < 0 || t >= job.cnt) continue;
+        const Unit un = unit_of<true>(p, i % UN, true);
+        Angles a;
+        angles_of<true>(p, steps, un, job.place + t, a);
+        k[e].widen(x[e]);
+        turn(p, un, a, x[e]);
+        if (F8) {
+            raise(ktop, x[e]);
+            float y[16];
+            v[e].widen(y);
+            raise(vtop, y);
+        }
+    }
+    float kinv = 1.f, vinv = 1.f;
+    if constexpr (F8) {
+        ktop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(ktop)));
+        vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vtop)));
+        const float ks = rescale(p, false, job, h, ktop, me, 32), vs = rescale(p, true, job, h, vtop, me, 32);
+        __syncwarp();   // all have read the old ones
+        if (me == 0) store_scales(p, job, h, ks, vs);
+        kinv = 1.f / ks;
+        vinv = 1.f / vs;
+    }
+#pragma unroll
+    for (int e = 0; e < kStepUnits; ++e) {
+        const int i = me + e * 32, t = i / UN - job.tok, u = i % UN;
+        if (i >= tasks || t < 0 || t >= job.cnt) continue;
+        put_unit<F8>(p, false, job, h, t, unit_of<true>(p, u, true), x[e], kinv);
+        float y[16];
+        v[e].widen(y);
+        put_unit<F8>(p, true, job, h, t, {u * 16, u * 16 + 8, -1}, y, vinv);
+    }
+}
+
 // A step's job for one head, by a warp
 template <bool F8, bool FAST>
 __device__ __forceinline__ void step_job(const AppendParams& p, const unsigned long long* steps, int n, int j, int h, int me, int32_t* bits) {
     Job job;
-    if (!job_of(p, n, j, job, bits) || job.id < 0) return;
+    if (!job_of(p, n, j, length_of(p, n), job, bits) || job.id < 0) return;
     const int UN = p.c.D / 16, tasks = job.cnt * UN;
     float kx[16], vx[16];
     auto take = [&](int i) {
@@ -474,7 +540,7 @@ template <bool F8, bool FAST, bool BF>
 __device__ __forceinline__ void prompt_job(const AppendParams& p, const unsigned long long* steps, float2* table, unsigned (*top_s)[2], int n, int j, int h0,
                                            int h1, int me, int32_t* bits) {
     Job job;
-    if (!job_of(p, n, j, job, bits) || job.id < 0) return;   // the whole block
+    if (!job_of(p, n, j, length_of(p, n), job, bits) || job.id < 0) return;   // the whole block
     const int lane = me % 32, warp = me / 32;
     const bool tab = BF && job.cnt * (p.rot / 2) <= kTable;
     if (tab) fill_table(p, steps, table, job, me);
@@ -570,20 +636,27 @@ __device__ __forceinline__ void q_task(const AppendParams& p, const unsigned lon
         qrow = n * p.qs[0] + t * p.qs[1];
         orow = n * p.os[0] + t * p.os[1];
     }
+    const Unit un = unit_of<FAST>(p, u, true);
+    const int h1 = min(p.Hq, (ch + 1) * hpt);
+    Raw r[BF ? kAtOnce : 1];
+    if constexpr (BF) {   // the first rows are asked for before the length is known
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e)
+            if (ch * hpt + e < h1) r[e].load(p.q, qrow + (ch * hpt + e) * p.qs[2], un);
+    }
     const int64_t start = length_of(p, n);
     if (start < 0) return;
     const int place = static_cast<int>(start) + t;
-    const Unit un = unit_of<FAST>(p, u, true);
     Angles a;
     angles_of<FAST>(p, steps, un, place, a);
-    const int h1 = min(p.Hq, (ch + 1) * hpt);
     float x[16];
     if constexpr (BF) {
         for (int h = ch * hpt; h < h1; h += kAtOnce) {
-            Raw r[kAtOnce];
+            if (h > ch * hpt) {
 #pragma unroll
-            for (int e = 0; e < kAtOnce; ++e)
-                if (h + e < h1) r[e].load(p.q, qrow + (h + e) * p.qs[2], un);
+                for (int e = 0; e < kAtOnce; ++e)
+                    if (h + e < h1) r[e].load(p.q, qrow + (h + e) * p.qs[2], un);
+            }
 #pragma unroll
             for (int e = 0; e < kAtOnce; ++e)
                 if (h + e < h1) {
@@ -606,21 +679,30 @@ __device__ __forceinline__ void load_steps(const AppendParams& p, unsigned long 
 }
 
 // Blocks [0, kv_blocks): a warp a job (sequence, touched page, head); the others: queries
-template <bool F8, bool FAST>
-__global__ void __launch_bounds__(kThreads) append_step(const __grid_constant__ AppendParams p, int kv_blocks, int pages_of, int hpt, int64_t q_tasks) {
+template <bool F8, bool FAST, bool BF>
+__global__ void __launch_bounds__(kThreads, 2) append_step(const __grid_constant__ AppendParams p, int kv_blocks, int pages_of, int hpt, int64_t q_tasks) {
     __shared__ unsigned long long steps[128];
     const int tid = threadIdx.x;
     stream_order();
-    load_steps(p, steps);
     int32_t bits = 0;
     if (static_cast<int>(blockIdx.x) >= kv_blocks) {
         const int64_t task = static_cast<int64_t>(blockIdx.x - kv_blocks) * kThreads + tid;
-        if (task < q_tasks) q_task<FAST, false>(p, steps, task, hpt);
+        load_steps(p, steps);
+        if (task < q_tasks) q_task<FAST, BF>(p, steps, task, hpt);
     } else {
         const int64_t job = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + tid / 32;
         const int h = static_cast<int>(job % p.c.H), j = static_cast<int>(job / p.c.H % pages_of);
         const int64_t n = job / p.c.H / pages_of;
-        if (n < p.n) step_job<F8, FAST>(p, steps, static_cast<int>(n), j, h, tid % 32, &bits);
+        const bool held = BF && p.T * (p.c.D / 16) <= 32 * kStepUnits;
+        StepRows rows;
+        if (held && n < p.n) rows.load(p, static_cast<int>(n), h, tid % 32);
+        load_steps(p, steps);
+        if (n < p.n) {
+            if constexpr (BF) {
+                if (held) step_job_bf16<F8>(p, steps, rows, static_cast<int>(n), j, h, tid % 32, &bits);
+            }
+            if (!held) step_job<F8, FAST>(p, steps, static_cast<int>(n), j, h, tid % 32, &bits);
+        }
     }
     flag_err(p.dev_err, bits);
 }
@@ -653,11 +735,13 @@ __global__ void __launch_bounds__(kThreads, 2) append_prompt(const __grid_consta
 template <bool F8, bool FAST>
 lar_status launch(const AppendParams& p, cudaStream_t stream) {
     const int64_t limit = (int64_t{1} << 31) - 1;
+    const bool bf = p.k_dt == LAR_BF16 && p.v_dt == LAR_BF16 && (!p.q || p.q_dt == LAR_BF16);
     const int64_t tokens = p.cu ? p.ntok : static_cast<int64_t>(p.n) * p.T;
     int64_t q_tasks = 0;
     int hpt = 1;   // heads share their angles where there are threads enough without
     if (p.q) {
         const int64_t units = tokens * (p.c.D / 16) * p.Hq;
+        if (FAST && bf) hpt = kAtOnce;   // rows that are asked for together take no longer than one
         while (hpt < 32 && hpt < p.Hq && units / (2 * hpt) >= 152 * 1024) hpt *= 2;
         q_tasks = tokens * (p.c.D / 16) * ((p.Hq + hpt - 1) / hpt);
     }
@@ -670,7 +754,6 @@ lar_status launch(const AppendParams& p, cudaStream_t stream) {
         if (pages * groups + q_blocks > limit) return LAR_ERR_SHAPE;
         const dim3 grid(static_cast<unsigned>(pages * groups + q_blocks));
         const int kv = static_cast<int>(pages * groups), gr = static_cast<int>(groups);
-        const bool bf = p.k_dt == LAR_BF16 && p.v_dt == LAR_BF16 && (!p.q || p.q_dt == LAR_BF16);
         if constexpr (FAST) {
             if (bf) return launch_ordered(append_prompt<F8, true, true>, grid, kThreads, 0, 1, stream, p, kv, gr, heads, hpt, q_tasks);
         }
@@ -679,8 +762,12 @@ lar_status launch(const AppendParams& p, cudaStream_t stream) {
     const int pages_of = p.T == 1 ? 1 : 2;
     const int64_t kv_blocks = (static_cast<int64_t>(p.n) * pages_of * p.c.H + kThreads / 32 - 1) / (kThreads / 32);
     if (kv_blocks + q_blocks > limit) return LAR_ERR_SHAPE;
-    return launch_ordered(append_step<F8, FAST>, dim3(static_cast<unsigned>(kv_blocks + q_blocks)), kThreads, 0, 1, stream, p, static_cast<int>(kv_blocks), pages_of,
-                          hpt, q_tasks);
+    const dim3 grid(static_cast<unsigned>(kv_blocks + q_blocks));
+    const int kv = static_cast<int>(kv_blocks);
+    if constexpr (FAST) {
+        if (bf) return launch_ordered(append_step<F8, true, true>, grid, kThreads, 0, 1, stream, p, kv, pages_of, hpt, q_tasks);
+    }
+    return launch_ordered(append_step<F8, FAST, false>, grid, kThreads, 0, 1, stream, p, kv, pages_of, hpt, q_tasks);
 }
 
 }  // namespace
