@@ -17,6 +17,12 @@
 // head (or warps share one where heads are few); after the greatest magnitudes it comes for
 // keys and values again, which L2 still has.  The queries are blocks of their own here
 // too, a thread a token's unit, whose angles it works out once for several heads.
+//
+// Bound: bytes for prompts (16384 tokens, 32 + 8 heads of 128, e4m3: 80 us where the copy rate
+// admits 54; the keys and values alone 43 of 15, the queries beside them 37 of 40), latency for
+// steps (256 tokens 6.6 us, one 4.2: a launch, frequencies, length, page, old scale).  Angles
+// worked out by every thread instead of a table: 138 us; keys and values kept in registers
+// instead of asked for again: 88 to 120 (they spill).
 #include <cuda_fp8.h>
 
 #include "layer_common.cuh"

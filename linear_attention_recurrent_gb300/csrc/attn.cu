@@ -29,6 +29,11 @@
 // that no other warp waits for, its own running maximum, sum and output, joined
 // once a pair.  A pair that several blocks share leaves its parts in the workspace, and
 // attn_join adds them.
+//
+// Bound: the bytes of the visible codes.  64 sequences of 0 to 8192 places, 8 heads of 128,
+// e4m3: 100 us where the copy rate admits 80; 1 x 131000, 2 heads of 256: 35 of 20; 32 x 4
+// tokens x 0 to 4096: 42 of 21 (twice the instructions of one token).  What is lost: a block's
+// beginning and end (3 and 4 us), and issue: 37 to 47 % of the cycles at 8 to 12 warps an SM.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -47,10 +52,13 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxBlocks = 608;    // of a call: bounds the workspace
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kStart = 20;   // tiles that a pair's beginning and end count as
+// Tiles that a pair's beginning and end count as: 64 sequences and 32 x 4 tokens take 125 and
+// 110 us at 4 tiles of 8 KB, 101 and 46 at 16 of 4 KB, 104 and 42 at 24, 105 and 45 at 48.
+constexpr int kStart = 20;
 constexpr float kSlack = 8.f;      // a weight may grow to 2^8 before the sums are scaled down
 
-// Tokens of a warp's tile: 4 KB of keys and values, at least a granule of 16.
+// Tokens of a warp's tile: 4 KB of keys and values, at least a granule of 16.  Of 8 KB, one
+// sequence takes 10.2 us instead of 9.5 and 32 x 4 tokens 56 instead of 46; 64 sequences the same.
 constexpr int tile_tokens(int D, bool f8) {
     const int t = 4096 / (2 * D * (f8 ? 1 : 2));
     return t > 32 ? 32 : t < 16 ? 16 : t;
@@ -66,7 +74,7 @@ struct Shape {
     static constexpr int ROW = D * ES;                 // bytes of a token's row
     static constexpr int CH = ROW / 16;                // its 16-byte chunks
     static constexpr int TILE = WT * ROW;              // bytes of a tile's keys
-    static constexpr int STAGES = 2;
+    static constexpr int STAGES = 2;                   // three and four: 64 sequences 113 and 110 us instead of 102
     static constexpr int RING = STAGES * 2 * TILE;     // a warp's
     static constexpr int KS = D / 16;                  // steps of the first product
     static constexpr int MT = D / 16;                  // row tiles of the second
@@ -76,7 +84,8 @@ struct Shape {
     static constexpr int JOIN = kWarps * PART * 4;
     static constexpr int BODY = kWarps * RING > JOIN ? kWarps * RING : JOIN;
     static constexpr int SMEM = BODY + QF + ROWS * 4;
-    static constexpr bool QREG = D * NR <= 128 || (D == 256 && NR == 1);        // fragments stay in registers
+    // fragments stay in registers, unless a third block fits an SM without them (32 x 4 tokens 52 -> 46 us)
+    static constexpr bool QREG = D * NR <= 128 || (D == 256 && NR == 1);
     static constexpr int BLOCKS = D < 256 && D * NR <= 256 ? 3 : 2;   // an SM, by registers
 };
 

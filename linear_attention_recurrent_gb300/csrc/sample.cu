@@ -23,6 +23,12 @@
 // that grow past their room (equal logits, sorted ones) are replaced by passes over the
 // row that narrow the key down 11 bits at a time.  Ties at a cut are kept from the lowest
 // index on.
+//
+// Measured, 64 x 131072 fp32 (the bytes: 5 us): the greatest alone 14 us, temperature 24,
+// top-k 50 21, 1000 28, top-p 56, equal logits with top-p 268; one such row 6.4, 11, 14, 17
+// and 25.  144 x 50257 bf16 with probabilities 33 (the bytes: 6.4).  Bound: instructions (26 a
+// weight, in each pass that needs them), and the exchanges over a cluster, 1 to 2 us each,
+// three with a temperature alone and nine with top-p.
 #include "layer_common.cuh"
 #include "serve_params.h"
 
@@ -34,6 +40,7 @@ namespace {
 
 using u64 = unsigned long long;
 
+// 256: 64 rows of top-k 1000 46 us instead of 36, one row 28 instead of 23; 1024: no better, and one row slower
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
