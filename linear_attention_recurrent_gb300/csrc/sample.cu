@@ -25,7 +25,7 @@
 // index on.
 //
 // Measured, 64 x 131072 fp32 (the bytes: 5 us): the greatest alone 14 us, temperature 24,
-// top-k 50 21, 1000 28, top-p 56, equal logits with top-p 268; one such row 6.4, 11, 14, 17
+// top-k 50 21, 1000 29, top-p 57, equal logits with top-p 268; one such row 6.3, 11, 12, 17
 // and 25.  144 x 50257 bf16 with probabilities 33 (the bytes: 6.4).  Bound: instructions (26 a
 // weight, in each pass that needs them), and the exchanges over a cluster, 1 to 2 us each,
 // three with a temperature alone and nine with top-p.
@@ -620,9 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         const u64 w = sc.weight(x, s.pow);
         return w >= least ? w : u64{0};
     };
-    // f(i, x, w): all of the warp's logits with their weights; i may lie outside the row, where
-    // the weight is 0
-    auto each_weight2 = [&](auto f) {   // f(i, x, x', w, w') of neighbours
+    // f(i, x, x', w, w'): all of the warp's logits and their neighbours with their weights; i may
+    // lie outside the row, where the weight is 0
+    auto each_weight2 = [&](auto f) {
         for (int st = s0; st < s1; ++st) {
             float x[8];
             row.eight_of(st * kStep + lane * 8, x);
@@ -635,21 +635,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
             }
         }
     };
-    auto each_weight = [&](auto f) {
-        each_weight2([&](int i, float x0, float x1, u64 w0, u64 w1) {
-            f(i, x0, w0);
-            f(i + 1, x1, w1);
-        });
-    };
     auto of_row = [&](auto g) {
         each([&](int i, float x) {
             const unsigned key = key_of(x);
             if (kept(i, key)) g(key, i, x);
         });
     };
-    const auto one = [](unsigned, int, float) { return u64{1}; };
-    const auto by_weight = [&](unsigned, int, float x) { return sc.weight(x, s.pow); };
-
     auto to_list = [&](unsigned key, int i) {
         const unsigned at = atomicAdd(&s.count, 1u);
         if (at < kList) s.list[at] = entry_of(key, i);
@@ -675,14 +666,43 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
             if (kept(at, key)) g(key, at, of_key(key));
         }
     };
-    // The cut behind the first logits whose sum of f reaches `target`: among block 0's list, and
-    // among the whole row
-    auto cut_list = [&](u64 target, auto f) {
-        const u64 at = c.find_place(entry_of(list_low, 0x7fffffff), entry_of(list_high, 0), target,
-                                    [&](auto g) { of_list([&](unsigned key, int i, float x) { g(entry_of(key, i), f(key, i, x)); }); });
-        __syncthreads();
-        cut = {entry_key(at), entry_index(at) + 1};
+    u64 total = 0;
+    bool drawn = false;
+    // Block 0's list: 0 the cut of top-k, 1 that of top-p, 2 the token; from stage `begin` on, whose
+    // sum is `target` where that is known.  One loop for all: the code of a kernel has to fit
+    // the instruction cache.
+    auto work_list = [&](int begin, u64 target, bool to_draw) {
+#pragma unroll 1
+        for (int stage = begin; stage < 3; ++stage) {
+            if (stage == 1 && !(top_p < 1.f)) continue;
+            if (stage == 2 && !to_draw) break;
+            auto each_of = [&](auto g) {
+                of_list([&](unsigned key, int i, float x) {
+                    const u64 w = stage == 0 ? 1ull : sc.weight(x, s.pow);
+                    g(stage == 2 ? 0xffffffffull - static_cast<unsigned>(i) : entry_of(key, i), stage == 2 && w < least ? 0ull : w);
+                });
+            };
+            if (target == 0) {
+                u64 w = 0;
+                each_of([&](u64, u64 v) { w += v; });
+                const u64 all = c.own_sum(w);
+                if (stage == 1) {
+                    target = part_of<true>(top_p, all);
+                } else {
+                    total = all;
+                    target = part_of<false>(u, all) + 1;
+                    if (target > all) target = all;
+                }
+            }
+            const u64 low = stage == 2 ? 0xffffffffull - static_cast<unsigned>(row.V) : entry_of(list_low, 0x7fffffff);
+            const u64 at = c.find_place(low, stage == 2 ? 0xffffffffull : entry_of(list_high, 0), target, each_of);
+            __syncthreads();
+            if (stage < 2) cut = {entry_key(at), entry_index(at) + 1};
+            else if (tid == 0) put(static_cast<int64_t>(0xffffffffull - at));
+            target = 0;
+        }
     };
+    // The cut behind the first logits of the row whose sum of f reaches `target`
     auto cut_row = [&](u64 target, auto f) {
         const unsigned key = c.template find_key<true>(cut.key, top_key, target, of_row, f);
         const u64 above = s.found[2], at = s.found[3], w1 = f(key, 0, of_key(key));
@@ -692,26 +712,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         if (n * w1 < at) {
             const unsigned last = c.template find_key<true>(
                 0xffffffffu - static_cast<unsigned>(row.V), 0xffffffffu, n,
-                [&](auto g) { of_row([&](unsigned q, int i, float x) { if (q == key) g(0xffffffffu - static_cast<unsigned>(i), i, x); }); }, one);
+                [&](auto g) { of_row([&](unsigned q, int i, float x) { if (q == key) g(0xffffffffu - static_cast<unsigned>(i), i, x); }); },
+                [](unsigned, int, float) { return u64{1}; });
             limit = static_cast<int>(0xffffffffu - last) + 1;
         }
         cut = {key, limit};
     };
 
-    u64 total = 0;
-    bool drawn = false;
-    // The token, among block 0's list
-    auto draw_of_list = [&] {
-        u64 w = 0;
-        of_list([&](unsigned, int i, float x) { w += weight(i, x); });
-        total = c.own_sum(w);
-        u64 target = part_of<false>(u, total);
-        if (target >= total) target = total - 1;
-        const u64 most_i = 0xffffffffull, least_i = most_i - static_cast<unsigned>(row.V);
-        const u64 at = c.find_place(least_i, most_i, target + 1,
-                                    [&](auto g) { of_list([&](unsigned, int i, float x) { g(most_i - static_cast<unsigned>(i), weight(i, x)); }); });
-        if (tid == 0) put(static_cast<int64_t>(most_i - at));
-    };
     // Block 0's cut and sum, to all blocks
     auto tell_all = [&] {
         if (tid < static_cast<int>(c.size)) {
@@ -727,6 +734,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     };
     bool summed = false;   // the warps' sums of what the draw is among
     u64 mine = 0;
+    bool listed = false;   // block 0's list has the cuts: work_list's arguments
+    int list_begin = 0;
+    u64 list_target = 0;
     if (by_k) {
         unsigned bound = kLeast;
         if (k <= groups) {
@@ -766,117 +776,119 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         list_low = bound;
         if (n_list <= kList) {
             if (c.rank == 0) {
-                if (n_list > static_cast<u64>(k)) cut_list(static_cast<u64>(k), one);
-                else cut = {bound, row.V};
-                if (top_p < 1.f) {
-                    u64 w = 0;
-                    of_list([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });
-                    cut_list(part_of<true>(top_p, c.own_sum(w)), by_weight);
-                }
-                draw_of_list();
-                if (p.probs) tell_all();
+                const bool all = n_list <= static_cast<u64>(k);
+                if (all) cut = {bound, row.V};
+                list_begin = all ? 1 : 0;
+                list_target = all ? 0 : static_cast<u64>(k);
             }
-            drawn = true;
-            if (p.probs) hear();   // else the other blocks may be gone: nothing is sent to them
-        } else {
-            cut_row(static_cast<u64>(k), one);
+            drawn = listed = true;
         }
     }
-    if (!drawn && top_p < 1.f) {
-        bool done = false;
-        if (!by_k) {
-            // bins of equal widths over the logits that weigh anything
-            const float low = fmaxf(greatest - 0.6931472f * (sc.up + 1) * temp, -3e38f), to_bin = (kBins - 1) / (greatest - low);
-            auto bin_of = [&](float x) { return min(kBins - 1, max(0, static_cast<int>((x - low) * to_bin))); };
-            c.clear_bins();
+    bool p_done = false;
+    if (!by_k && top_p < 1.f) {
+        // bins of equal widths over the logits that weigh anything
+        const float low = fmaxf(greatest - 0.6931472f * (sc.up + 1) * temp, -3e38f), to_bin = (kBins - 1) / (greatest - low);
+        auto bin_of = [&](float x) { return min(kBins - 1, max(0, static_cast<int>((x - low) * to_bin))); };
+        c.clear_bins();
 #pragma unroll 2
-            for (int st = s0; st < s1; ++st) {
-                float x[8];
-                row.eight_of(st * kStep + lane * 8, x);
+        for (int st = s0; st < s1; ++st) {
+            float x[8];
+            row.eight_of(st * kStep + lane * 8, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (x[e] >= low) atomicAdd(&s.lo[bin_of(x[e])], 1u);
-            }
-            const float width = 1.f / to_bin;
-            c.template find_bin<true>([&](int q, u64 n) { return n ? n * sc.weight(fminf(greatest, low + (q + 0.5f) * width), s.pow) : 0ull; },
-                                      [&](u64 all) { return max(u64{1}, part_of<true>(top_p, all)); });
-            const int bin = static_cast<int>(s.found[1]);
-            // How many lie in and above it, and in the 3, 7 and 17 bins around it: a bin's middle is up
-            // to 0.8 % off, so the cut may lie in a neighbour.  The list takes all of them or, where
-            // they are too many, the widest of these windows that fits.
-            u64 n[4] = {0, 0, 0, 0};
-            for (int q = max(0, bin - 8) + tid; q < kBins; q += kThreads) {
-                const unsigned v = s.lo[q];
-                if (q >= bin - 3) n[0] += v;
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-                    if (abs(q - bin) <= (e == 0 ? 1 : e == 1 ? 3 : 8)) n[e + 1] += v;
-            }
-            c.sums(n);
-            const bool few = n[0] <= kList;
-            const int around = n[3] <= kList ? 8 : n[2] <= kList ? 3 : n[1] <= kList ? 1 : 0;
-            const float from = low + (few ? bin - 3 : bin - around) * width, to = few ? INFINITY : low + (bin + around + 1) * width;
-            // exact sums: of all, of what lies above the list's, of those
-            u64 got[4] = {0, 0, 0, 0};
-            each_weight2([&](int i, float x0, float x1, u64 w0, u64 w1) {
-                got[0] += w0 + w1;
-                if (!(fmaxf(x0, x1) >= from)) return;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float x = e ? x1 : x0;
-                    const u64 w = e ? w1 : w0;
-                    if (!(x >= from) || w == 0) continue;
-                    if (x > to) {
-                        got[1] += w;
-                        mine += w >= least ? w : 0ull;
-                    } else {
-                        got[2] += w;
-                        to_list(key_of(clean(x)), i + e);
-                    }
-                }
-            });
-            c.sums(got);
-            const u64 all = got[0], above = got[1], own = got[2];
-            n_list = gather();
-            list_low = key_of(clean(from));
-            if (!few) list_high = key_of(clean(to));
-            const u64 target = part_of<true>(top_p, all);
-            if (n_list <= kList && above < target && target <= above + own) {
-                if (c.rank == 0) {
-                    cut_list(target - above, by_weight);
-                    if (few) draw_of_list();
-                    if (!few || p.probs) tell_all();
-                }
-                done = true;
-                drawn = few;
-                if (!few || p.probs) hear();
-                if (!few) {
-                    // each warp its own of the lists'
-                    for (unsigned i = lane; i < s.count; i += 32) {
-                        const int at = entry_index(s.list[i]), st = (at + row.off) / kStep;
-                        if (st >= s0 && st < s1) mine += weight(at, of_key(entry_key(s.list[i])));
-                    }
-                    summed = true;
-                }
-            }
+            for (int e = 0; e < 8; ++e)
+                if (x[e] >= low) atomicAdd(&s.lo[bin_of(x[e])], 1u);
         }
-        if (!done) {
-            u64 w = 0;
-            of_row([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });
-            const u64 all = c.sum(w, nullptr);
-            cut_row(part_of<true>(top_p, all), by_weight);
+        const float width = 1.f / to_bin;
+        c.template find_bin<true>([&](int q, u64 n) { return n ? n * sc.weight(fminf(greatest, low + (q + 0.5f) * width), s.pow) : 0ull; },
+                                  [&](u64 all) { return max(u64{1}, part_of<true>(top_p, all)); });
+        const int bin = static_cast<int>(s.found[1]);
+        // How many lie in and above it, and in the 3, 7 and 17 bins around it: a bin's middle is up
+        // to 0.8 % off, so the cut may lie in a neighbour.  The list takes all of them or, where
+        // they are too many, the widest of these windows that fits.
+        u64 n[4] = {0, 0, 0, 0};
+        for (int q = max(0, bin - 8) + tid; q < kBins; q += kThreads) {
+            const unsigned v = s.lo[q];
+            if (q >= bin - 3) n[0] += v;
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (abs(q - bin) <= (e == 0 ? 1 : e == 1 ? 3 : 8)) n[e + 1] += v;
+        }
+        c.sums(n);
+        const bool few = n[0] <= kList;
+        const int around = n[3] <= kList ? 8 : n[2] <= kList ? 3 : n[1] <= kList ? 1 : 0;
+        const float from = low + (few ? bin - 3 : bin - around) * width, to = few ? INFINITY : low + (bin + around + 1) * width;
+        // exact sums: of all, of what lies above the list's, of those
+        u64 got[4] = {0, 0, 0, 0};
+        each_weight2([&](int i, float x0, float x1, u64 w0, u64 w1) {
+            got[0] += w0 + w1;
+            if (!(fmaxf(x0, x1) >= from)) return;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x = e ? x1 : x0;
+                const u64 w = e ? w1 : w0;
+                if (!(x >= from) || w == 0) continue;
+                if (x > to) {
+                    got[1] += w;
+                    mine += w >= least ? w : 0ull;
+                } else {
+                    got[2] += w;
+                    to_list(key_of(clean(x)), i + e);
+                }
+            }
+        });
+        c.sums(got);
+        const u64 all = got[0], above = got[1], own = got[2];
+        n_list = gather();
+        list_low = key_of(clean(from));
+        if (!few) list_high = key_of(clean(to));
+        const u64 target = part_of<true>(top_p, all);
+        if (n_list <= kList && above < target && target <= above + own) {
+            list_begin = 1;
+            list_target = target - above;
+            p_done = listed = true;
+            drawn = few;
+        }
+    }
+    if (listed) {
+        const bool tell = !drawn || p.probs != nullptr;   // else the other blocks may be gone: nothing is sent to them
+        if (c.rank == 0) {
+            work_list(list_begin, list_target, drawn);
+            if (tell) tell_all();
+        }
+        if (tell) hear();
+        if (!drawn) {
+            // each warp its own of the lists'
+            for (unsigned i = lane; i < s.count; i += 32) {
+                const int at = entry_index(s.list[i]), st = (at + row.off) / kStep;
+                if (st >= s0 && st < s1) mine += weight(at, of_key(entry_key(s.list[i])));
+            }
+            summed = true;
+        }
+    } else {
+#pragma unroll 1
+        for (int stage = 0; stage < 2; ++stage) {   // passes over the row instead: top-k, top-p
+            if (stage == 0 ? !by_k : !(top_p < 1.f) || p_done) continue;
+            auto f = [&](unsigned, int, float x) { return stage == 0 ? u64{1} : sc.weight(x, s.pow); };
+            u64 target = static_cast<u64>(k);
+            if (stage == 1) {
+                u64 w = 0;
+                of_row([&](unsigned, int, float x) { w += sc.weight(x, s.pow); });
+                target = part_of<true>(top_p, c.sum(w, nullptr));
+            }
+            cut_row(target, f);
         }
     }
     if (!drawn) {
         u64 start;
         if (!summed) {
             mine = 0;
-            if (cut.key == kLeast) {
-                if (least) each_weight([&](int, float, u64 w) { mine += w >= least ? w : 0ull; });
-                else each_weight([&](int, float, u64 w) { mine += w; });
-            } else {
-                each_weight([&](int i, float x, u64 w) { mine += w >= least && kept(i, key_of(clean(x))) ? w : 0ull; });
-            }
+            if (cut.key == kLeast && !least)   // the same with a test in the loop is 4 % slower
+                each_weight2([&](int, float, float, u64 w0, u64 w1) { mine += w0 + w1; });
+            else
+                each_weight2([&](int i, float x0, float x1, u64 w0, u64 w1) {
+                    mine += w0 >= least && kept(i, key_of(clean(x0))) ? w0 : 0ull;
+                    mine += w1 >= least && kept(i + 1, key_of(clean(x1))) ? w1 : 0ull;
+                });
         }
         total = c.sum(mine, &start);
         u64 target = part_of<false>(u, total);
