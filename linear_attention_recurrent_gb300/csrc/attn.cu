@@ -64,7 +64,7 @@ constexpr int tile_tokens(int D, bool f8) {
     return t > 32 ? 32 : t < 16 ? 16 : t;
 }
 
-constexpr float kNone = -1e30f;    // the maximum of a row that has seen nothing
+constexpr float kNone = -3e38f;    // the maximum of a row that has seen nothing: below any score
 
 template <int D, bool F8, int NR>
 struct Shape {

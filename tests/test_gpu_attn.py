@@ -135,6 +135,25 @@ def test_range_of_queries(cache, cuda_device):
         assert torch.equal(out, want), e
 
 
+def test_far_scores(cuda_device):
+    """Scores near the lowest that fp32 holds, as keys of a type's lowest values leave them: a row
+    of nothing else is their softmax still."""
+    s = make(cuda_device, 35, [50, 200], 1, 4, 2, 64, 16, BF16)
+    s["q"].zero_()
+    s["q"][..., 0] = 1.0
+    for e in (100, 120, 126):
+        s["k_cache"].zero_()
+        s["k_cache"][..., 0] = -2.0 ** e
+        lse = torch.zeros(2, 1, 4, device=cuda_device)
+        out = call(s, scale=1.0, lse=lse, out_dtype=F32)
+        for b, n in enumerate((51, 201)):
+            v = held(s, "v", b)[0][:n]
+            for h in range(4):
+                want = v[:, h // 2].mean(0)
+                assert np.abs(out[b, 0, h].cpu().double().numpy() - want).max() <= (2.0 ** -15 + n * 2 * R.U) * np.abs(v).max()
+        assert bool(((lse / -2.0 ** e - 1).abs() < 1e-6).all())
+
+
 def test_scales_of_pages(cuda_device):
     """Pages of one sequence whose scales differ by 2^20, and scales that are no powers of two."""
     for kind in ("far", "odd"):
