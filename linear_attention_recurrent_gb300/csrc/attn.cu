@@ -148,19 +148,24 @@ __device__ __forceinline__ void mma(float* d, const unsigned* a, unsigned b0, un
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The places that any of sequence b's rows see: [lo, hi); own: the first token's place.
+// The places that any of sequence b's rows see: [lo, hi), none where they are equal; own: the
+// first token's place, which may lie past the table and its window still reach back into it.
+// Up to 2^30 places and windows below 2^31: from 3 2^30 + 64 on no window does, and what is
+// reckoned with `own`, modulo 2^32, comes out right where there is anything to see.
 struct Seen {
-    int lo, hi, own;
+    int lo, hi;
+    unsigned own;
 };
 
 __device__ __forceinline__ Seen seen_of(const AttnParams& p, int b, int32_t* bits) {
     const int64_t len = ld_idx(p.c.lens, b * p.c.len_s, p.c.len_dt);
     const int cap = p.c.M * p.c.page;
-    if (len < 0) return {0, 0, 0};   // no sequence here
-    if (len + p.T > cap) *bits |= LAR_DEVERR_SEQLEN;
-    const int own = static_cast<int>(len < cap ? len : cap);
-    const int hi = min(own + p.T, cap), lo = p.window ? max(0, own - p.window + 1) : 0;
-    return {lo, max(hi, lo), own};
+    if (len < 0) return {0, 0, 0u};   // no sequence here
+    if (len > cap - p.T) *bits |= LAR_DEVERR_SEQLEN;
+    const int64_t own = min(len, (int64_t{3} << 30) + 64);
+    const int hi = static_cast<int>(min(own + p.T, static_cast<int64_t>(cap)));
+    const int64_t lo = p.window ? max(int64_t{0}, own - p.window + 1) : 0;
+    return {static_cast<int>(min(lo, static_cast<int64_t>(hi))), hi, static_cast<unsigned>(own)};
 }
 
 // Tiles of a pair, and what it counts as where the work is dealt out: kStart in front of them
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
         }
         // this lane's rows: n 8 + t4 2 + {0, 1}
         float cf[NR][2], mx[NR][2], l[NR][2];
-        int end[NR][2];   // one past the last place that the row sees
+        unsigned end[NR][2];   // one past the row's own place
         float o[NR][S::MT][4];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
             }
 
             // scores in base 2 with the values' scale, against the maximum so far
-            const bool inner = pos >= (p.window ? seen.own + p.T - p.window : 0) && pos + S::WT <= seen.own + 1;   // all rows see all of it
+            const bool inner = pos >= (p.window ? static_cast<int>(seen.own + p.T - p.window) : 0) && pos + S::WT <= seen.own + 1;   // all rows see all of it
             float gk[GR], gv[GR], gi[GR];
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
@@ -485,8 +490,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
             auto against = [&](int gr, int n, int k, float top) {
                 const float x = fmaf(s[gr][n][k], cf[n][k & 1] * gk[gr], gv[gr] - top);
                 if (inner) return x;
-                const int at = pos + gr * 16 + g + (k >> 1) * 8, e = end[n][k & 1];
-                return at >= min(e, seen.hi) || (p.window && at < e - p.window) || gv[gr] == -INFINITY ? -INFINITY : x;
+                const int at = pos + gr * 16 + g + (k >> 1) * 8;
+                const unsigned e = end[n][k & 1];
+                return at >= min(e, static_cast<unsigned>(seen.hi)) || (p.window && at < static_cast<int>(e - p.window)) || gv[gr] == -INFINITY ? -INFINITY : x;
             };
             float w[GR][NR][4];
             float high = -INFINITY;
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
                             }
                         } else {
                             for (int tk = 0; tk < p.T; ++tk) {
-                                const int last = min(seen.own + tk + 1, seen.hi), first = p.window ? seen.own + tk + 1 - p.window : 0;
+                                const int last = min(seen.own + tk + 1, static_cast<unsigned>(seen.hi)), first = p.window ? static_cast<int>(seen.own + tk + 1 - p.window) : 0;
                                 unsigned keep[2];
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {

@@ -333,3 +333,28 @@ def test_append_then_attend_in_steps(cuda_device):
             want, bd, _, _ = R.attend(qr[h], kk[:, h // 2], vv[:, h // 2], D ** -0.5, 0, t + 1, eight=False)
             flip = 2.0 ** -7 * np.abs(qr[h]).max() * np.abs(kk).max() * D ** -0.5
             assert (np.abs(o[h] - want) <= bd + R.U * np.abs(want) + 2 * flip * np.abs(vv).max()).all(), (t, h)
+
+
+@pytest.mark.parametrize("cache", [F8, BF16])
+@pytest.mark.parametrize("T", [1, 5])
+def test_windows_past_the_table(cache, T, cuda_device):
+    """Lengths that reach past the table by less than the window, just as far, and any further: a
+    row's window lies where its place is, and what of it the table has no page for is not seen."""
+    dev = cuda_device
+    s = make(dev, 36, [90] * 8, T, 4, 2, 64, 16, cache)
+    cap = s["table"].shape[1] * 16
+    assert cap == 96
+    lens = [cap - T, cap - 1, cap, cap + 3, cap + 19, cap + 20, 40, 2 ** 31 - 1]
+    for far in (2 ** 31 - 1, 2 ** 40, 2 ** 62):
+        s["lens"] = lens[:-1] + [far]
+        s["seq_lens"] = torch.tensor(s["lens"], dtype=torch.int32 if far < 2 ** 31 else torch.int64, device=dev)
+        for window in (0, 1, 20, 24, 200, 2 ** 31 - 1):
+            err = torch.zeros(1, dtype=torch.int32, device=dev)
+            out, lse = check(s, window, dev_err=err)
+            assert int(err) == lar.LAR_DEVERR_SEQLEN
+            if window == 20:
+                assert bool((out[5] == 0).all() and (lse[5] == -float("inf")).all())
+    err.zero_()
+    s["seq_lens"] = torch.tensor([40] * 7 + [2 ** 63 - 1], device=dev)
+    out = call(s, window=20, dev_err=err)
+    assert int(err) == lar.LAR_DEVERR_SEQLEN and bool((out[7] == 0).all())
