@@ -477,7 +477,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
             }
 
             // scores in base 2 with the values' scale, against the maximum so far
-            const bool inner = pos >= (p.window ? static_cast<int>(seen.own + p.T - p.window) : 0) && pos + S::WT <= seen.own + 1;   // all rows see all of it
             float gk[GR], gv[GR], gi[GR];
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
@@ -486,6 +485,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
                 gv[gr] = __shfl_sync(0xffffffffu, gv_l, src);
                 gi[gr] = __shfl_sync(0xffffffffu, gi_l, src);
             }
+            // all rows see all of it (a granule that no page has is not seen: a query that is no number
+            // would make one of it)
+            bool inner = pos >= (p.window ? static_cast<int>(seen.own + p.T - p.window) : 0) && pos + S::WT <= seen.own + 1;
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) inner &= gv[gr] != -INFINITY;
             // element k of granule gr, row tile n: token g + 8 (k / 2), row k % 2 of the lane's
             auto against = [&](int gr, int n, int k, float top) {
                 const float x = fmaf(s[gr][n][k], cf[n][k & 1] * gk[gr], gv[gr] - top);

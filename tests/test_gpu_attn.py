@@ -358,3 +358,23 @@ def test_windows_past_the_table(cache, T, cuda_device):
     s["seq_lens"] = torch.tensor([40] * 7 + [2 ** 63 - 1], device=dev)
     out = call(s, window=20, dev_err=err)
     assert int(err) == lar.LAR_DEVERR_SEQLEN and bool((out[7] == 0).all())
+
+
+@pytest.mark.parametrize("cache", [F8, BF16])
+@pytest.mark.parametrize("T", [1, 3])
+def test_queries_that_are_no_numbers(cache, T, cuda_device):
+    """NaN and infinite queries: a row that sees nothing is 0 all the same, and rows beside it are as
+    they were."""
+    dev = cuda_device
+    s = make(dev, 38, [200, 130, 7], T, 4, 2, 128, 16, cache)
+    s["table"][0, :] = -1
+    want, want_lse = check(s)
+    for bad in (float("nan"), float("inf")):
+        t = dict(s, q=s["q"].clone())
+        t["q"][0], t["q"][1, 0, 1] = bad, bad
+        lse = torch.zeros_like(want_lse)
+        out = call(t, lse=lse)
+        assert bool((out[0] == 0).all() and (lse[0] == -float("inf")).all())
+        assert not bool(torch.isfinite(out[1, 0, 1]).any())
+        out[1, 0, 1], lse[1, 0, 1] = want[1, 0, 1], want_lse[1, 0, 1]
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
