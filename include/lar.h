@@ -539,7 +539,9 @@ lar_status kv_append(const lar_tensor* q, const lar_tensor* k, const lar_tensor*
  *            at the same time need one each.
  * What stands at places that a row does not see has no say in it, whatever it is.  Scores,
  * maxima and sums are fp32; the weights of the second product are rounded to 11 bits (e4m3
- * pages: fp16) or 16 bits (bf16 pages).  How the work is split depends on the lengths and
+ * pages: fp16) or 16 bits (bf16 pages).  16-bit values may be as large as their type goes: where
+ * a sum passes 2^115 it is taken once more (in about twice the time), with weights 2^-60 of what
+ * they were, and values below 2^-66 beside such ones may count as 0.  How the work is split depends on the lengths and
  * sizes alone, so a repeated call gives the same bits.  Scales are positive and finite.
  * Two kernels on `stream`.
  */

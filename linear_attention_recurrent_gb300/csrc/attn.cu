@@ -21,6 +21,11 @@
 // A weight is taken against a maximum that is moved only when a score passes it by 2^8
 // (fp16 reaches 2^16): no maximum is looked for, only that none is too large.
 //
+// The sums are not divided before the end, and those of 16-bit values near the end of their
+// range pass fp32's: a warp with a sum past 2^115 takes its tiles once more, against references
+// 2^60 higher, where 2^30 values sum up to less than 2^107.  The joins add up 2432 such sums at
+// most.
+//
 // Work.  A tile is WT tokens of one pair (sequence, key/value head, 8 NR query rows).
 // The tiles of all pairs in a row, each pair with kStart more for what its beginning and
 // end cost, are dealt out to the blocks in equal shares, a multiple of four, whatever the
@@ -55,7 +60,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Tiles that a pair's beginning and end count as: 64 sequences and 32 x 4 tokens take 125 and
 // 110 us at 4 tiles of 8 KB, 101 and 46 at 16 of 4 KB, 104 and 42 at 24, 105 and 45 at 48.
 constexpr int kStart = 20;
-constexpr float kSlack = 8.f;      // a weight may grow to 2^8 before the sums are scaled down
+constexpr float kSlack = 8.f;      // a weight may grow to 2^8 of its first before the sums are scaled down
+constexpr float kMost = 4.1538374868278621e34f;   // 2^115: sums that the joins have room for
+constexpr float kLow = -60.f;      // log2 of first weights where there are greater ones
 
 // Tokens of a warp's tile: 4 KB of keys and values, at least a granule of 16.  Of 8 KB, one
 // sequence takes 10.2 us instead of 9.5 and 32 x 4 tokens 56 instead of 46; 64 sequences the same.
@@ -424,8 +431,51 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
                 for (int k = 0; k < 4; ++k) o[n][m][k] = 0.f;
         }
         float gk_l = 1.f, gv_l = 0.f, gi_l = 1.f;   // of this lane's granule: the keys' scale, log2 and inverse of the values'
+        float fresh = 0.f;   // log2 of the greatest weight where a maximum is moved
 
-        for (int i = 0; i < mine; ++i) {
+        for (int i = 0;; ++i) {
+            if (i >= mine) {
+                if (F8 || fresh != 0.f) break;
+                unsigned over = 0;   // rows with sums that are too large, or no numbers
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int m = 0; m < S::MT; ++m)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) over |= !(fabsf(o[n][m][k]) <= kMost) ? 1u << (n * 2 + (k & 1)) : 0u;
+                if (!__any_sync(0xffffffffu, over != 0)) break;
+                // rows whose scores are no numbers are not helped, and leave the others as they are
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float all = l[n][r];
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+                        if (!(all < INFINITY)) over &= ~(1u << (n * 2 + r));
+                    }
+                if (!__any_sync(0xffffffffu, over != 0)) break;
+                // once more from the beginning, with room
+                fresh = kLow;
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        mx[n][k] = kNone;
+                        l[n][k] = 0.f;
+                    }
+#pragma unroll
+                    for (int m = 0; m < S::MT; ++m)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[n][m][k] = 0.f;
+                }
+                id_next = page_of(0);
+                load_batch(0);
+                __syncwarp();   // the ring is read no more
+#pragma unroll
+                for (int j = 0; j < S::STAGES - 1; ++j) load(j);
+                i = 0;
+            }
             if (i % BT == 0) {   // the loads are at this batch already, and not at the next one
                 gk_l = ks_raw;
                 gv_l = !there ? -INFINITY : F8 ? log2f(vs_raw) : 0.f;
@@ -509,14 +559,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
                         w[gr][n][k] = against(gr, n, k, mx[n][k & 1]);
                         high = fmaxf(high, w[gr][n][k]);
                     }
-            if (__any_sync(0xffffffffu, high > kSlack)) {
+            if (__any_sync(0xffffffffu, high > kSlack + fresh)) {
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float top = mx[n][r];
 #pragma unroll
-                        for (int gr = 0; gr < GR; ++gr) top = fmaxf(top, fmaxf(against(gr, n, r, 0.f), against(gr, n, r + 2, 0.f)));
+                        for (int gr = 0; gr < GR; ++gr) top = fmaxf(top, fmaxf(against(gr, n, r, fresh), against(gr, n, r + 2, fresh)));
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                         const float f = exp2_f(mx[n][r] - top);

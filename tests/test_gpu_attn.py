@@ -378,3 +378,51 @@ def test_queries_that_are_no_numbers(cache, T, cuda_device):
         assert not bool(torch.isfinite(out[1, 0, 1]).any())
         out[1, 0, 1], lse[1, 0, 1] = want[1, 0, 1], want_lse[1, 0, 1]
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_range_of_values(D, cuda_device):
+    """16-bit values to the end of their range, where their weighted sum passes fp32's and their
+    average does not; and small ones."""
+    most = float(torch.finfo(BF16).max)
+    for lens, T in (([1, 0, 14, 15, 600, 33], 2), ([9000], 1), ([60] * 40, 1)):
+        s = make(cuda_device, 40, lens, T, 4, 2, D, 16, BF16)
+        base, top = s["v_cache"], {}
+        for kind in (-100, 100, 125, "most", "signs"):
+            if kind == "most":
+                s["v_cache"] = torch.full_like(base, most)
+            elif kind == "signs":
+                s["v_cache"] = torch.where(base > 0, most, -most).to(BF16)
+            else:
+                s["v_cache"] = (base.float() * 2.0 ** kind).clamp(-most, most).to(BF16)
+            check(s)
+            top[kind] = check(s, window=21, out_dtype=F32)[0]
+        assert float((top["most"] / most - 1).abs().max()) <= 2.0 ** -13
+    # two tokens; and a maximum that creeps up, so that weights are above 1
+    s = make(cuda_device, 41, [1], 1, 2, 1, D, 16, BF16)
+    s["v_cache"] = torch.full_like(s["v_cache"], 2.0 ** 127)
+    check(s)
+    s = make(cuda_device, 42, [600], 1, 2, 1, D, 16, BF16)
+    up = torch.linspace(-30, 30, 16 * s["P"], device=cuda_device).view(s["P"], 16)
+    order = s["table"][0].long()
+    k = torch.zeros(s["P"], 16, 1, D, device=cuda_device)
+    k[order.to(cuda_device), :, 0, 0] = up[:len(order)]
+    s["k_cache"] = k.to(BF16)
+    s["q"].zero_()
+    s["q"][..., 0] = 8.0 * (D / 64) ** 0.5
+    for e in (0, 118, 122, 125):
+        s["v_cache"] = (torch.randn(s["v_cache"].shape, generator=torch.Generator().manual_seed(e)) * 2.0 ** e).clamp(-most, most).to(BF16).to(cuda_device)
+        check(s)
+
+
+def test_large_values_beside_unseen_ones(cuda_device):
+    """The same among a step's tokens, of which the later ones are not finite."""
+    most = float(torch.finfo(BF16).max)
+    s = make(cuda_device, 43, [37, 200], 4, 4, 2, 128, 16, BF16)
+    s["v_cache"] = torch.where(s["v_cache"] > 0, most, -most / 2).to(BF16)
+    want, _ = check(s)
+    pg = int(s["table"][1, 203 // 16])
+    s["v_cache"][pg, 203 % 16] = float("inf")
+    out = call(s)
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1, :3], want[1, :3])
+    assert not bool(torch.isfinite(out[1, 3]).all())
