@@ -538,11 +538,13 @@ lar_status kv_append(const lar_tensor* q, const lar_tensor* k, const lar_tensor*
  *            or more; what it holds need not be kept between calls, and calls that may run
  *            at the same time need one each.
  * What stands at places that a row does not see has no say in it, whatever it is.  Scores,
- * maxima and sums are fp32; the weights of the second product are rounded to 11 bits (e4m3
- * pages: fp16) or 16 bits (bf16 pages).  16-bit values may be as large as their type goes: where
- * a sum passes 2^115 it is taken once more (in about twice the time), with weights 2^-60 of what
- * they were, and values below 2^-66 beside such ones may count as 0.  How the work is split depends on the lengths and
- * sizes alone, so a repeated call gives the same bits.  Scales are positive and finite.
+ * maxima and sums are fp32.  The weights of the second product are rounded to 11 bits with e4m3
+ * pages (fp16; below 2^-21 of the greatest, each times its values' scale, to 2^-32 of that), to 16
+ * bits with bf16 pages.  16-bit values may be as large as their type goes: where a sum passes
+ * 2^115 it is taken once more (in about twice the time), with weights 2^-60 of what they were,
+ * and values below 2^-66 beside such ones may count as 0.  How the work is split depends on the
+ * lengths and sizes alone, so a repeated call gives the same bits.  Scales are positive normal numbers,
+ * those of one sequence's values within 2^100 of one another.
  * Two kernels on `stream`.
  */
 int64_t attn_workspace(int32_t T, int32_t Hq, int32_t H, int32_t D);

@@ -7,7 +7,7 @@
 //     e_j = scale log2(e) q.K_j + log2 r_j,   M = max e_j
 // the output is sum 2^(e_j - M) c_j / sum 2^(e_j - M) / r_j, so that the products take
 // codes as they lie (an e4m3 number is exact in fp16, and so is a bf16 query once its
-// row is scaled by a power of two), and what fp16 rounds is a weight in [0, 2^8].
+// row is scaled by a power of two), and what fp16 rounds is a weight in [0, 2^15].
 // Both products run on the tensor cores with fp32 sums.  bf16 pages take weights split
 // into two bf16 terms (16 bits of each weight).
 //
@@ -18,8 +18,11 @@
 // order that the queries are laid out to match; a value's 16 bytes are the same dimensions
 // of eight steps.
 //
-// A weight is taken against a maximum that is moved only when a score passes it by 2^8
-// (fp16 reaches 2^16): no maximum is looked for, only that none is too large.
+// A weight is taken against a reference that is moved only when a weight passes 2^8 of what
+// the greatest was then: no maximum is looked for, only that none is too large.  The greatest
+// is 2^7 then in fp16, which reaches 2^16, and so keeps 11 bits of weights down to 2^-21 of it and
+// 2^-32 of it below (a long tail of those may be all that a row has, beside values near 0); 1 in
+// bf16, whose range is fp32's.
 //
 // The sums are not divided before the end, and those of 16-bit values near the end of their
 // range pass fp32's: a warp with a sum past 2^115 takes its tiles once more, against references
@@ -62,6 +65,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kStart = 20;
 constexpr float kSlack = 8.f;      // a weight may grow to 2^8 of its first before the sums are scaled down
 constexpr float kMost = 4.1538374868278621e34f;   // 2^115: sums that the joins have room for
+constexpr float kFresh16 = 7.f;    // log2 of the greatest weight where a reference is moved, in fp16
 constexpr float kLow = -60.f;      // log2 of first weights where there are greater ones
 
 // Tokens of a warp's tile: 4 KB of keys and values, at least a granule of 16.  Of 8 KB, one
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, F8, NR>::BLOCKS)) attn_ker
                 for (int k = 0; k < 4; ++k) o[n][m][k] = 0.f;
         }
         float gk_l = 1.f, gv_l = 0.f, gi_l = 1.f;   // of this lane's granule: the keys' scale, log2 and inverse of the values'
-        float fresh = 0.f;   // log2 of the greatest weight where a maximum is moved
+        float fresh = F8 ? kFresh16 : 0.f;   // log2 of the greatest weight where a reference is moved
 
         for (int i = 0;; ++i) {
             if (i >= mine) {

@@ -426,3 +426,41 @@ def test_large_values_beside_unseen_ones(cuda_device):
     out = call(s)
     assert torch.equal(out[0], want[0]) and torch.equal(out[1, :3], want[1, :3])
     assert not bool(torch.isfinite(out[1, 3]).all())
+
+
+def test_small_weights(cuda_device):
+    """Tokens that take nearly all the weight and whose values are 0, one in each of the first tiles,
+    in front of a long tail: fp16 weights are good to 2^-11 of themselves or 2^-32 of the
+    greatest, so a row that is all tail is as good as that.
+
+    Bound: (2 ew + 2^-11 + n 2 u) S as for every row (the head of the reference's file), and
+    n 2^-32 max |V| over the weights' sum, in units of the greatest."""
+    dev, n, D, B = cuda_device, 2048, 64, 600
+    drop = [10.5, 17.5, 21.5, 22.0, 23.5, 24.5, 25.5, 26.5]
+    s = make(dev, 39, [n - 1], 1, len(drop), 1, D, 64, F8)
+    s["k_scale"].fill_(1.0)
+    s["v_scale"].fill_(1.0)
+    kb, vb = s["k_cache"].view(torch.uint8), s["v_cache"].view(torch.uint8)
+    kb.zero_()
+    heavy = list(range(0, 256, 8))
+    for i in heavy:
+        kb[int(s["table"][0, i // 64]), i % 64, 0, 0] = 0x38   # 1
+        vb[int(s["table"][0, i // 64]), i % 64] = 0
+    vb &= 0x7f                                                 # of one sign: sums do not cancel
+    s["q"].zero_()
+    s["q"][0, 0, :, 0] = torch.tensor(drop)
+    scale = float(np.float32(np.log(2)))                       # a weight is 2^-drop
+    (k, _), (v, _) = held(s, "k", 0), held(s, "v", 0)
+    k, v, q = k[:n, 0], v[:n, 0], R.f64(s["q"])
+    s["table"], s["q"], s["seq_lens"] = s["table"].expand(B, -1).contiguous(), s["q"].expand(B, -1, -1, -1).contiguous(), s["seq_lens"].expand(B).contiguous()
+    lse = torch.zeros(B, 1, len(drop), device=dev)
+    got = call(s, scale=scale, out_dtype=F32, lse=lse).cpu().double().numpy()
+    for h in range(len(drop)):
+        x = k @ q[0, 0, h] * scale
+        w = np.exp(x - x.max())
+        want = w @ v / w.sum()
+        es = (2 * D + 8) * R.U * drop[h] * scale * 1.4427 + 8 * R.U * (drop[h] + 64)
+        ew = es * 0.6932 + 2.0 ** -22
+        tol = (2 * ew + 2.0 ** -11 + n * 2 * R.U) * want + n * 2.0 ** -32 * v.max() / w.sum() + R.U * want
+        assert (np.abs(got[:, 0, h] - want) <= tol).all(), (drop[h], (np.abs(got[:, 0, h] - want) / want).max(), (tol / want).max())
+        assert (np.abs(lse[:, 0, h].cpu().double().numpy() - x.max() - np.log(w.sum())) <= ew + n * 2 * R.U + 4 * R.U * x.max()).all()
