@@ -516,8 +516,8 @@ lar_status spec_verify(const lar_tensor* draft_tokens, const lar_tensor* draft_p
  * Aliasing: caches and scales are in and out; they and q_out overlap nothing else of the call
  * (keys' and values' views may lie between one another).  No page is named by two sequences,
  * or twice, where tokens are appended; pages in front of those are not touched, and may be
- * shared.  Offsets that do not ascend are flagged (LAR_DEVERR_SEQLEN); which of the spans
- * behind them are taken is not defined.
+ * shared.  Offsets that do not ascend are flagged (LAR_DEVERR_SEQLEN; with no tokens at all nothing
+ * is looked at); which of the spans around them are taken is not defined.
  */
 lar_status kv_append(const lar_tensor* q, const lar_tensor* k, const lar_tensor* v, const lar_tensor* q_out,
                      const lar_tensor* k_cache, const lar_tensor* v_cache, const lar_tensor* k_scale,

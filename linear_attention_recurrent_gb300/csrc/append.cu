@@ -732,6 +732,12 @@ __global__ void __launch_bounds__(kThreads, 2) append_prompt(const __grid_consta
     const int h0 = static_cast<int>(blockIdx.x % groups) * heads;
     const int64_t unit = blockIdx.x / groups;
     auto key = [&](int i) { return ld_idx(p.cu, i * p.cu_s, p.cu_dt) / p.c.page + 2 * static_cast<int64_t>(i); };
+    // The search finds no span that offsets fall back behind: each is looked at once besides, by
+    // the block of its number (blocks are two a span at least).
+    if (static_cast<int>(blockIdx.x) < p.n && threadIdx.x == 0) {
+        int begin, len;
+        span(p, static_cast<int>(blockIdx.x), &begin, &len, &bits);
+    }
     const int n = last_at_most(p.n, unit, key);
     const int64_t j = unit - key(n);
     if (j >= 0 && j < (1 << 30)) prompt_job<F8, FAST, BF>(p, steps, table, top_s, n, static_cast<int>(j), h0, min(p.c.H, h0 + heads), threadIdx.x, &bits);

@@ -329,3 +329,26 @@ def test_prepared_captured_streams(cuda_device):
     for n in ("k_cache", "v_cache"):
         assert np.array_equal(raw(s[n]), raw(t[n]))
     assert torch.equal(s["k_scale"], t["k_scale"]) and torch.equal(s["v_scale"], t["v_scale"])
+
+
+@pytest.mark.parametrize("cu", [[0, 1000, 0, 1000], [0, 600, 300, 1000], [0, 1000, 999, 1000], [0, 40, 20, 1000],
+                                [0, 1000, -5, 1000], [700, 300, 600, 1000]])
+def test_offsets_that_do_not_ascend(cu, cuda_device):
+    """Flagged however far they fall back; pages of no sequence stay as they are."""
+    dev = cuda_device
+    s = make(dev, 19, [0, 3, 7], [1000] * 3, 2, 1, 64, 16, F8, packed=True)
+    s.update({n: s[n][:1000] for n in ("q", "k", "v")})
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    mine = s["table"][s["table"] >= 0].tolist()
+    before = raw(s["k_cache"]), raw(s["v_cache"])
+    for dt in (torch.int32, torch.int64):
+        err.zero_()
+        s["cu"] = torch.tensor(cu, dtype=dt, device=dev)
+        call(s, dev_err=err)
+        assert int(err) == lar.LAR_DEVERR_SEQLEN
+    spare = [i for i in range(s["P"]) if i not in mine]
+    assert spare and all(np.array_equal(a[spare], raw(s[n])[spare]) for a, n in zip(before, ("k_cache", "v_cache")))
+    err.zero_()
+    s["cu"] = torch.tensor([0, 0, 1000, 1000], dtype=torch.int32, device=dev)
+    call(s, dev_err=err)
+    assert int(err) == 0
