@@ -6,8 +6,9 @@
 // exp((x - max) / temperature) is a whole number of 2^-(63 - log2 V): a token has to be the
 // one that exact sums give, and whole numbers add up exactly in any order, at the rate of
 // 32-bit adds, where fp64 is slow on this part.  Its argument is kept in two floats, 2^n
-// comes from a table of 32 steps, and the rest, at most 1/64, from a polynomial: good to
-// 2^-30 of the weight.
+// comes from a table of 256 steps, and the rest, f of at most 1/512, from a polynomial: good to
+// 2^-30 of the weight (the table and the product with it 2^-32 each, its rounding 2^-33, f and the
+// polynomial's steps 2^-34 each; with 32 steps the last four are 8 times as much and more).
 //
 // Work.  A row is a cluster's, every warp owning a contiguous stretch of the vocabulary.
 // One pass finds the greatest logit.  Then
@@ -50,12 +51,41 @@ constexpr int kList = 2048;      // room for logits around a cut
 constexpr int kBins = 1 << kBits;
 constexpr int kSmall = 256;      // entries that are compared with one another
 
-// 2^(31 + j / 32), to the nearest whole number
-__constant__ unsigned kPow[32] = {
-    2147483648u, 2194507417u, 2242560872u, 2291666561u, 2341847524u, 2393127307u, 2445529972u, 2499080105u,
-    2553802834u, 2609723834u, 2666869345u, 2725266179u, 2784941738u, 2845924021u, 2908241642u, 2971923842u,
-    3037000500u, 3103502151u, 3171459999u, 3240905930u, 3311872529u, 3384393094u, 3458501653u, 3534232978u,
-    3611622603u, 3690706840u, 3771522796u, 3854108391u, 3938502376u, 4024744348u, 4112874773u, 4202935003u};
+// 2^(31 + j / 256), to the nearest whole number
+constexpr int kPowBits = 8, kPows = 1 << kPowBits;
+__constant__ unsigned kPow[kPows] = {
+    2147483648u, 2153306067u, 2159144272u, 2164998306u, 2170868212u, 2176754033u, 2182655811u, 2188573592u,
+    2194507417u, 2200457330u, 2206423375u, 2212405596u, 2218404036u, 2224418739u, 2230449750u, 2236497113u,
+    2242560872u, 2248641071u, 2254737756u, 2260850970u, 2266980759u, 2273127167u, 2279290240u, 2285470023u,
+    2291666561u, 2297879899u, 2304110083u, 2310357160u, 2316621173u, 2322902170u, 2329200197u, 2335515300u,
+    2341847524u, 2348196917u, 2354563524u, 2360947394u, 2367348571u, 2373767105u, 2380203040u, 2386656425u,
+    2393127307u, 2399615734u, 2406121752u, 2412645410u, 2419186755u, 2425745836u, 2432322700u, 2438917396u,
+    2445529972u, 2452160476u, 2458808958u, 2465475465u, 2472160047u, 2478862753u, 2485583632u, 2492322733u,
+    2499080105u, 2505855799u, 2512649863u, 2519462348u, 2526293303u, 2533142779u, 2540010826u, 2546897494u,
+    2553802834u, 2560726895u, 2567669730u, 2574631389u, 2581611923u, 2588611383u, 2595629821u, 2602667287u,
+    2609723834u, 2616799513u, 2623894376u, 2631008476u, 2638141863u, 2645294591u, 2652466713u, 2659658279u,
+    2666869345u, 2674099961u, 2681350181u, 2688620059u, 2695909648u, 2703219000u, 2710548171u, 2717897212u,
+    2725266179u, 2732655125u, 2740064105u, 2747493172u, 2754942382u, 2762411789u, 2769901447u, 2777411411u,
+    2784941738u, 2792492481u, 2800063696u, 2807655439u, 2815267765u, 2822900730u, 2830554390u, 2838228802u,
+    2845924021u, 2853640104u, 2861377107u, 2869135087u, 2876914102u, 2884714207u, 2892535461u, 2900377920u,
+    2908241642u, 2916126685u, 2924033107u, 2931960965u, 2939910317u, 2947881223u, 2955873740u, 2963887926u,
+    2971923842u, 2979981545u, 2988061094u, 2996162550u, 3004285971u, 3012431416u, 3020598946u, 3028788621u,
+    3037000500u, 3045234644u, 3053491112u, 3061769967u, 3070071267u, 3078395075u, 3086741451u, 3095110456u,
+    3103502151u, 3111916599u, 3120353861u, 3128813999u, 3137297074u, 3145803149u, 3154332287u, 3162884549u,
+    3171459999u, 3180058700u, 3188680714u, 3197326104u, 3205994934u, 3214687269u, 3223403170u, 3232142703u,
+    3240905930u, 3249692918u, 3258503729u, 3267338429u, 3276197082u, 3285079754u, 3293986508u, 3302917412u,
+    3311872529u, 3320851927u, 3329855670u, 3338883824u, 3347936457u, 3357013633u, 3366115421u, 3375241885u,
+    3384393094u, 3393569115u, 3402770014u, 3411995860u, 3421246719u, 3430522660u, 3439823750u, 3449150059u,
+    3458501653u, 3467878602u, 3477280975u, 3486708840u, 3496162267u, 3505641324u, 3515146082u, 3524676610u,
+    3534232978u, 3543815256u, 3553423514u, 3563057822u, 3572718252u, 3582404874u, 3592117759u, 3601856978u,
+    3611622603u, 3621414705u, 3631233356u, 3641078629u, 3650950594u, 3660849326u, 3670774895u, 3680727376u,
+    3690706840u, 3700713361u, 3710747013u, 3720807869u, 3730896002u, 3741011488u, 3751154399u, 3761324810u,
+    3771522796u, 3781748432u, 3792001792u, 3802282952u, 3812591987u, 3822928972u, 3833293984u, 3843687099u,
+    3854108391u, 3864557939u, 3875035819u, 3885542107u, 3896076880u, 3906640216u, 3917232192u, 3927852886u,
+    3938502376u, 3949180739u, 3959888054u, 3970624400u, 3981389855u, 3992184498u, 4003008408u, 4013861665u,
+    4024744348u, 4035656537u, 4046598312u, 4057569753u, 4068570940u, 4079601955u, 4090662878u, 4101753790u,
+    4112874773u, 4124025908u, 4135207276u, 4146418961u, 4157661043u, 4168933606u, 4180236731u, 4191570503u,
+    4202935003u, 4214330316u, 4225756525u, 4237213713u, 4248701965u, 4260221365u, 4271771996u, 4283353945u};
 
 // A logit as it is ordered: NaN is -infinity, and -0 is 0.
 __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
@@ -91,7 +121,7 @@ struct Scale {
         e = fma2(d, pack2(lo, lo), fma2(de, h, fma2(d, h, mul2(y, minus))));
     }
 
-    // Weights of two logits (NaN and -infinity weigh nothing): 2^y by whole number, 32nd and
+    // Weights of two logits (NaN and -infinity weigh nothing): 2^y by whole number, 256th and
     // the rest
     __device__ __forceinline__ void weights(float x0, float x1, const uint2* pow, u64& w0, u64& w1) const {
         if (infinite) {
@@ -106,11 +136,10 @@ struct Scale {
         const float least = static_cast<float>(-2 - up);   // from there on a weight is 0
         y = pack2(fmaxf(y0, least), fmaxf(y1, least));
         const f32x2 big = pack2(kRound, kRound), minus = pack2(-1.f, -1.f);
-        const f32x2 r = fma2(y, pack2(32.f, 32.f), big);
-        const f32x2 f = add2(fma2(add2(r, mul2(big, minus)), pack2(-1.f / 32, -1.f / 32), y), e);
-        // 2^f - 1: ln 2, its powers over the factorials
-        f32x2 g = fma2(f, pack2(9.618129e-3f, 9.618129e-3f), pack2(5.550411e-2f, 5.550411e-2f));
-        g = fma2(f, g, pack2(0.24022651f, 0.24022651f));
+        const f32x2 r = fma2(y, pack2(1.f * kPows, 1.f * kPows), big);
+        const f32x2 f = add2(fma2(add2(r, mul2(big, minus)), pack2(-1.f / kPows, -1.f / kPows), y), e);
+        // 2^f - 1: ln 2, its powers over the factorials (the next one is below 2^-42)
+        f32x2 g = fma2(f, pack2(5.550411e-2f, 5.550411e-2f), pack2(0.24022651f, 0.24022651f));
         g = fma2(f, g, pack2(0.69314718f, 0.69314718f));
         g = mul2(f, g);
         unpack2(r, r0, r1);
@@ -119,12 +148,12 @@ struct Scale {
         w1 = scaled(r1, g1, pow);
     }
 
-    // r has the 32nds in its low bits, as a whole number
+    // r has the 256ths in its low bits, as a whole number
     __device__ __forceinline__ u64 scaled(float r, float g, const uint2* pow) const {
         const int j = static_cast<int>(__float_as_uint(r));   // kRound's own low 22 bits are 0
-        const uint2 t = pow[j & 31];
+        const uint2 t = pow[j & (kPows - 1)];
         const unsigned m = t.x + static_cast<unsigned>(__float2int_rn(g * __uint_as_float(t.y)));
-        const int down = 63 - up + (static_cast<int>(__float_as_uint(kRound)) >> 5) - (j >> 5);
+        const int down = 63 - up + (static_cast<int>(__float_as_uint(kRound)) >> kPowBits) - (j >> kPowBits);
         u64 w;
         asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(static_cast<u64>(m) << 32), "r"(down));   // by 64 and more: 0
         return w;
@@ -209,7 +238,7 @@ __device__ __forceinline__ unsigned entry_key(u64 e) { return static_cast<unsign
 __device__ __forceinline__ int entry_index(u64 e) { return static_cast<int>(0xffffffffu - static_cast<unsigned>(e)); }
 
 struct Shared {
-    uint2 pow[32];                 // a whole number, and as a float
+    uint2 pow[kPows];              // a whole number, and as a float
     u64 warp[kWarps];
     u64 peer[2][kMaxCluster];      // exchanges in turn
     u64 warp4[4][kWarps], peer4[2][4][kMaxCluster];
@@ -507,7 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Block c{s, cluster_rank(), cluster_size(), tid, lane, warp};
     cluster_arrive();
-    if (tid < 32) s.pow[tid] = make_uint2(kPow[tid], __float_as_uint(static_cast<float>(kPow[tid])));
+    static_assert(kPows <= kThreads, "");
+    if (tid < kPows) s.pow[tid] = make_uint2(kPow[tid], __float_as_uint(static_cast<float>(kPow[tid])));
     if (tid == 0) s.count = 0;
     stream_order();
     const int b = blockIdx.y / p.T, t = blockIdx.y % p.T;

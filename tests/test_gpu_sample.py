@@ -254,3 +254,30 @@ def test_prepared_captured_streams(cuda_device):
         torch.cuda.synchronize()
         a, b = run(dev, y, v, top_p=p)
         assert np.array_equal(tok.cpu(), a) and np.array_equal(pr.cpu().double(), b)
+
+
+def test_borders_of_weights(cuda_device):
+    """Random numbers that lie no further from a border than twice what weights are held to, 2^-30 of
+    themselves: the token on their side of it, all the same.
+
+    Of two tokens the first weighs a = exp((x - max) / temperature), the second 1: the border is p =
+    a / (1 + a), and an error of d in a is one of (1 - p) d in p."""
+    rng = np.random.default_rng(7)
+    x, u, temp, want = [], [], [], []
+    for t in (1.0, 0.3, 0.71, 1.7, 0.05):
+        t = np.float32(t)
+        a = (-12 * rng.random(200000) * float(t)).astype(np.float32)
+        w = np.exp(a.astype(np.longdouble) / np.longdouble(t))
+        p = w / (1 + w)
+        v = p.astype(np.float32)
+        far = (v.astype(np.longdouble) - p) / p / (1 - p) * 2.0 ** 30
+        near = (np.abs(far) > 1) & (np.abs(far) < 2) & (v < 1)
+        x.append(a[near])
+        u.append(v[near])
+        temp.append(np.full(near.sum(), t))
+        want.append((far[near] > 0).astype(np.int64))          # the second where u is past the border
+    x, u, temp, want = (np.concatenate(i)[:65535] for i in (x, u, temp, want))
+    assert len(x) > 20000
+    rows2 = torch.stack([torch.from_numpy(x), torch.zeros(len(x))], -1)
+    tok, _ = run(cuda_device, rows2, torch.from_numpy(u), False, temperature=torch.from_numpy(temp))
+    assert int((tok != want).sum()) == 0
