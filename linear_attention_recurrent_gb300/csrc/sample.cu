@@ -580,11 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     most0 += 0.f;   // -0 is 0
     most1 += 0.f;
     const float most = fmaxf(most0, most1);
-    // maxima of as many groups of logits as there is room for: two a thread, one, or one of two threads
+    // maxima of as many groups of logits as there is room for: two a thread, or one
+    static_assert(kMaxCluster * kThreads <= 2 * kList, "");
     const int groups = min(2 * static_cast<int>(c.size) * kThreads, 2 * kList);
     if (by_k) {
         const int id = static_cast<int>(c.rank) * kThreads + tid;
-        const float both = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         auto push = [&](int at, float x) {
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(&s.maxima[at], 0)), "r"(key_of(x)) : "memory");
         };
@@ -592,10 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         if (2 * all <= groups) {
             push(id, most0);
             push(id + all, most1);
-        } else if (all <= groups) {
+        } else {
             push(id, most);
-        } else if (tid % 2 == 0) {
-            push(id / 2, both);
         }
     }
     const unsigned top_key = static_cast<unsigned>(c.greatest(key_of(most)));
