@@ -510,7 +510,7 @@ lar_status spec_verify(const lar_tensor* draft_tokens, const lar_tensor* draft_p
  * stand before them in the page; if those have a smaller one, their codes are rounded to the
  * new one (exact unless a code falls below the least normal one).  A code is value / scale
  * rounded to nearest even (a rotated key from fp32: next to a tie, to either neighbour);
- * magnitudes past 448 2^64 are held there.  What is not finite
+ * magnitudes past 448 2^64 are held there.  What is not finite (in fp32, once it is rotated)
  * becomes a NaN and has no say in the scale.
  * Tokens behind the appended ones in a page count as not there.
  * Aliasing: caches and scales are in and out; they and q_out overlap nothing else of the call

@@ -352,3 +352,58 @@ def test_offsets_that_do_not_ascend(cu, cuda_device):
     s["cu"] = torch.tensor([0, 0, 1000, 1000], dtype=torch.int32, device=dev)
     call(s, dev_err=err)
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("cache", [F8, BF16])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Hq,H,news,lens,D,page,rot,interleaved", [
+    (4, 2, [33, 0, 1, 100], [0, 5, 15, 37], 128, 16, None, False), (6, 3, [200, 65], [63, 0], 128, 64, 32, True),
+    (16, 16, [129, 3, 260], [1, 0, 100], 64, 128, None, False), (5, 5, [70, 30], [9, 31], 256, 64, 64, True),
+    (9, 9, [150], [20], 128, 1024, None, False), (9, 9, [25] * 60, list(range(60)), 64, 16, None, False),
+    (6, 3, [40] * 150, list(range(150)), 64, 32, 32, True)])
+def test_prompts_of_both_types(cache, dtype, Hq, H, news, lens, D, page, rot, interleaved, cuda_device):
+    """Packed prompts of aligned rows, fp32 and bf16; heads from one to more than a block takes at once,
+    pages whose angles fit a table and pages whose do not."""
+    check(make(cuda_device, D + page + H, lens, news, Hq, H, D, page, cache, dtype, packed=True, rot=rot), interleaved, 0.75)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,many", [(1, 0), (3, 0), (9, 0), (9, 60), (3, 150)])
+@pytest.mark.parametrize("rot", [0, None])
+def test_prompts_that_are_not_finite(dtype, H, many, rot, cuda_device):
+    """Infinities and NaN in keys of some heads and values of others, in pages that hold earlier
+    tokens and in whole ones: they become NaN, and every other code and scale is what it
+    would be without them."""
+    dev, inf, nan = cuda_device, float("inf"), float("nan")
+    lens, news = [5, 0, 40], [40, 17, 33]
+    if many:   # pages enough for a block to have several heads, side by side
+        lens, news = lens + list(range(many)), news + [25] * many
+    s = make(dev, 51 + H, lens, news, H, H, 64, 16, F8, dtype, packed=True, rot=rot)
+    for n in ("k_scale", "v_scale"):   # far below the new ones: what stands there is rescaled
+        s[n].fill_(2.0 ** -12)
+    s["k"][3, 0, 5], s["k"][12, H - 1, 40], s["k"][41, 0, 0] = inf, nan, -inf
+    s["v"][0, H - 1, 63], s["v"][60, 0, 7], s["v"][89, H // 2, 31] = nan, -inf, inf
+    s["v"][44, 0] = nan
+    check(s)
+    assert float(s["k_scale"][int(s["table"][0, 0]), 0]) > 2.0 ** -12
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rotations_past_fp32(dtype, cuda_device):
+    """Keys that fp32 holds and their rotations do not are as infinite ones, in a prompt and in a
+    step; other tokens and heads do not see them."""
+    dev = cuda_device
+    for packed in (True, False):
+        new = [40, 20] if packed else 8
+        s = make(dev, 61, [3, 0], new, 3, 3, 64, 16, F8, dtype, packed=packed)
+        t = {m: (v.clone() if torch.is_tensor(v) else v) for m, v in s.items()}
+        for d, x in ((s, 1e38), (t, float("inf"))):
+            k = d["k"] if packed else d["k"][0]
+            k[2, 0, 5], k[2, 0, 37], k[7, 2, 10], k[7, 2, 42] = x, x, -x, x
+            call(d, rope_scale=1e5)
+        for n in ("k_cache", "v_cache"):
+            assert np.array_equal(raw(s[n]), raw(t[n])), n
+        assert torch.equal(s["k_scale"], t["k_scale"]) and torch.equal(s["v_scale"], t["v_scale"])
+        pg = int(s["table"][0, 0])
+        assert all((raw(s["k_cache"])[pg, 5, 0, d] & 0x7f) == 0x7f for d in (5, 37))
+        assert bool((s["k_scale"] < 2.0 ** 20).all())
