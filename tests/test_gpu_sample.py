@@ -281,3 +281,15 @@ def test_borders_of_weights(cuda_device):
     rows2 = torch.stack([torch.from_numpy(x), torch.zeros(len(x))], -1)
     tok, _ = run(cuda_device, rows2, torch.from_numpy(u), False, temperature=torch.from_numpy(temp))
     assert int((tok != want).sum()) == 0
+
+
+def test_random_numbers_past_their_range(cuda_device):
+    """Below 0 and NaN as 0; 1 and above: the last token that weighs anything."""
+    x, _, _ = rows(40, 12, 1, 3001)
+    inf, nan = float("inf"), float("nan")
+    u = torch.tensor([[-1.0], [nan], [1.0], [2.0], [inf], [-inf]] * 2)
+    tok, _ = run(cuda_device, x, u)
+    assert tok[:, 0].tolist() == [0, 0, 3000, 3000, 3000, 0] * 2
+    x[:, 0, 0] = x[:, 0, 2990:] = -inf
+    for kw in ({}, dict(top_k=torch.full((12,), 3001)), dict(top_p=torch.full((12,), 1 - 2.0 ** -24)), dict(min_p=torch.full((12,), 1e-12))):
+        check(cuda_device, x, u, **kw)
