@@ -30,6 +30,8 @@
 
 namespace lar {
 
+int cached_occupancy(const void* kern, int threads, size_t smem, size_t smem_max, int* sms_out);
+
 namespace {
 
 constexpr int kThreads = 256;
@@ -749,19 +751,24 @@ lar_status launch(const AppendParams& p, cudaStream_t stream) {
     const int64_t limit = (int64_t{1} << 31) - 1;
     const bool bf = p.k_dt == LAR_BF16 && p.v_dt == LAR_BF16 && (!p.q || p.q_dt == LAR_BF16);
     const int64_t tokens = p.cu ? p.ntok : static_cast<int64_t>(p.n) * p.T;
+    // asked for where it decides anything: the smallest steps are as long as their launch takes
+    int sms = 1;
+    if ((p.cu || tokens * (p.c.D / 16) * p.Hq >= 2048) &&
+        cached_occupancy(reinterpret_cast<const void*>(append_prompt<F8, FAST, false>), kThreads, 0, 0, &sms) < 1)
+        return LAR_ERR_LAUNCH;
     int64_t q_tasks = 0;
     int hpt = 1;   // heads share their angles where there are threads enough without
     if (p.q) {
         const int64_t units = tokens * (p.c.D / 16) * p.Hq;
         if (FAST && bf) hpt = kAtOnce;   // rows that are asked for together take no longer than one
-        while (hpt < 32 && hpt < p.Hq && units / (2 * hpt) >= 152 * 1024) hpt *= 2;
+        while (hpt < 32 && hpt < p.Hq && units / (2 * hpt) >= static_cast<int64_t>(sms) * 1024) hpt *= 2;
         q_tasks = tokens * (p.c.D / 16) * ((p.Hq + hpt - 1) / hpt);
     }
     const int64_t q_blocks = (q_tasks + kThreads - 1) / kThreads;
     if (p.cu) {
         const int64_t pages = p.ntok / p.c.page + 2 * static_cast<int64_t>(p.n);
         int heads = 1;   // likewise
-        while (heads < 8 && heads < p.c.H && pages * p.c.H >= 152 * 2 * heads) heads *= 2;
+        while (heads < 8 && heads < p.c.H && pages * p.c.H >= static_cast<int64_t>(sms) * 2 * heads) heads *= 2;
         const int64_t groups = (p.c.H + heads - 1) / heads;
         if (pages * groups + q_blocks > limit) return LAR_ERR_SHAPE;
         const dim3 grid(static_cast<unsigned>(pages * groups + q_blocks));
