@@ -170,13 +170,12 @@ struct Seen {
 
 __device__ __forceinline__ Seen seen_of(const AttnParams& p, int b, int32_t* bits) {
     const int64_t len = ld_idx(p.c.lens, b * p.c.len_s, p.c.len_dt);
-    const int cap = p.c.M * p.c.page;
+    const unsigned cap = static_cast<unsigned>(p.c.M) * p.c.page, far = (3u << 30) + 64u, window = p.window;
     if (len < 0) return {0, 0, 0u};   // no sequence here
-    if (len > cap - p.T) *bits |= LAR_DEVERR_SEQLEN;
-    const int64_t own = min(len, (int64_t{3} << 30) + 64);
-    const int hi = static_cast<int>(min(own + p.T, static_cast<int64_t>(cap)));
-    const int64_t lo = p.window ? max(int64_t{0}, own - p.window + 1) : 0;
-    return {static_cast<int>(min(lo, static_cast<int64_t>(hi))), hi, static_cast<unsigned>(own)};
+    const unsigned own = len < far ? static_cast<unsigned>(len) : far;
+    if (own + p.T > cap) *bits |= LAR_DEVERR_SEQLEN;
+    const unsigned hi = min(own + p.T, cap), lo = window && own >= window ? own + 1 - window : 0u;
+    return {static_cast<int>(min(lo, hi)), static_cast<int>(hi), own};
 }
 
 // Tiles of a pair, and what it counts as where the work is dealt out: kStart in front of them
