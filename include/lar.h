@@ -535,8 +535,8 @@ lar_status kv_append(const lar_tensor* q, const lar_tensor* k, const lar_tensor*
  *            Query head i reads key/value head i / (Hq / H).
  *   lse      fp32 [B, T, Hq] or NULL.  A row that sees nothing has out 0 and lse -infinity.
  *   workspace   fp32, contiguous, 16-byte aligned, of attn_workspace(T, Hq, H, D) elements
- *            or more; what it holds need not be kept between calls, and calls that may run
- *            at the same time need one each.
+ *            or more (-1: the call does not take such sizes); what it holds need not be kept
+ *            between calls, and calls that may run at the same time need one each.
  * What stands at places that a row does not see has no say in it, whatever it is.  Scores,
  * maxima and sums are fp32.  The weights of the second product are rounded to 11 bits with e4m3
  * pages (fp16; below 2^-21 of the greatest, each times its values' scale, to 2^-32 of that), to 16

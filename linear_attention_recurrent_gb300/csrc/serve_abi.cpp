@@ -195,7 +195,7 @@ lar_status kv_append(const lar_tensor* q, const lar_tensor* k, const lar_tensor*
 }
 
 int64_t attn_workspace(int32_t T, int32_t Hq, int32_t H, int32_t D) {
-    if (T < 1 || T > 16 || H < 1 || Hq < H || Hq % H || (D != 64 && D != 128 && D != 256)) return -1;
+    if (T < 1 || T > 16 || H < 1 || H > 1024 || Hq < H || Hq % H || Hq / H > 256 || (D != 64 && D != 128 && D != 256)) return -1;
     return attn_workspace_floats(T, Hq / H, D);
 }
 

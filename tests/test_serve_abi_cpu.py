@@ -86,6 +86,13 @@ def test_workspace(lib):
         assert lib.attn_workspace(T, Hq, H, D) == -1
 
 
+def test_workspace_of_sizes_that_are_refused(lib):
+    """More heads than attn_decode takes, to the ends of what the arguments hold."""
+    assert lib.attn_workspace(16, 256 * 1024, 1024, 256) > 0
+    for T, Hq, H, D in ((1, 257, 1, 64), (16, 2 ** 31 - 1, 1, 64), (1, 1025, 1025, 64), (16, 2 ** 31 - 1, 2 ** 31 - 1, 256)):
+        assert lib.attn_workspace(T, Hq, H, D) == -1
+
+
 @pytest.mark.parametrize("change,want", [
     (dict(k_cache=None), NULL), (dict(v_cache=None), NULL), (dict(block_table=None), NULL), (dict(seq_lens=None), NULL),
     (dict(k_scale=None), NULL), (dict(v_scale=None), NULL),
