@@ -490,7 +490,7 @@ lar_status spec_verify(const lar_tensor* draft_tokens, const lar_tensor* draft_p
  *   seq_lens int32/int64 [B]: tokens that sequence b has BEFORE the step: the step's token t
  *            is at place seq_lens[b] + t, in both calls.  Negative: no sequence here.
  *            Places from M page on are not written, not seen, and flagged
- *            (LAR_DEVERR_SEQLEN).
+ *            (LAR_DEVERR_SEQLEN; queries are rotated there too, past 2^30 as at 2^30).
  *
  * kv_append: the keys and values of a step's (or a prompt's) tokens enter the cache, the
  * keys rotated by their place; with q, the queries are rotated into q_out.
@@ -516,7 +516,9 @@ lar_status spec_verify(const lar_tensor* draft_tokens, const lar_tensor* draft_p
  * Aliasing: caches and scales are in and out; they and q_out overlap nothing else of the call
  * (keys' and values' views may lie between one another).  No page is named by two sequences,
  * or twice, where tokens are appended; pages in front of those are not touched, and may be
- * shared.  Offsets that do not ascend are flagged (LAR_DEVERR_SEQLEN; with no tokens at all nothing
+ * shared.  Fastest are bf16 rows that 16-byte loads fit and, for prompts, pages of 4096 angles or
+ * fewer (tokens times rot / 2): prompts take 1.4 times as long in larger ones, and fp32 rows
+ * twice.  Offsets that do not ascend are flagged (LAR_DEVERR_SEQLEN; with no tokens at all nothing
  * is looked at); which of the spans around them are taken is not defined.
  */
 lar_status kv_append(const lar_tensor* q, const lar_tensor* k, const lar_tensor* v, const lar_tensor* q_out,
@@ -545,6 +547,7 @@ lar_status kv_append(const lar_tensor* q, const lar_tensor* k, const lar_tensor*
  * and values below 2^-66 beside such ones may count as 0.  How the work is split depends on the
  * lengths and sizes alone, so a repeated call gives the same bits.  Scales are positive normal numbers,
  * those of one sequence's values within 2^100 of one another.
+ * The pages of a key/value head are walked once for every 32 of its T Hq / H rows (16 at D = 256).
  * Two kernels on `stream`.
  */
 int64_t attn_workspace(int32_t T, int32_t Hq, int32_t H, int32_t D);
@@ -573,11 +576,12 @@ lar_status attn_decode(const lar_tensor* q, const lar_tensor* k_cache, const lar
  *   min_p    fp32 [B] or NULL; 0 or less (or NaN): all.
  *   tokens   out, int32 or int64 [B, T] (rank 1 for T = 1).
  *   probs    out, fp32 [B, T, V] (rank 2) or NULL.
- * Any strides (outputs: no two elements at one address).  Weights are held to 2^-30 of
- * themselves or V 2^-62 of the greatest, sums exactly: the token is the one that exact
- * arithmetic gives unless u or a threshold is as near as that to a border.  Fastest are
- * top_k up to a thousand or so, and temperatures alone; top_p without top_k takes about
- * twice as long, and rows of few different logits several times.
+ * Any strides (outputs: no two elements at one address; rows whose logits lie side by side are
+ * read in half the time).  Weights are held to 2^-30 of themselves (temperatures from 2^-100 on)
+ * or V 2^-62 of the greatest, sums exactly: the token is the one that exact arithmetic gives
+ * unless u or a threshold is as near as that to a border.  Fastest are top_k up to a thousand or
+ * so, and temperatures alone; top_p without top_k takes about twice as long, and rows of few
+ * different logits several times.
  */
 lar_status sample_tokens(const lar_tensor* logits, const lar_tensor* u, const lar_tensor* temperature,
                          const lar_tensor* top_k, const lar_tensor* top_p, const lar_tensor* min_p,

@@ -12,17 +12,20 @@
 // magnitude is taken first.  Scales are powers of two, so that a page whose scale grows
 // later is rescaled without loss but for codes that leave the normal range.
 //
-// Steps of T <= 16 tokens: a warp has a job, and the queries are blocks of their own.
+// Steps of T <= 16 tokens: a warp has a job, and the queries are blocks of their own.  Steps whose
+// rows a warp's lanes can hold (T D / 16 up to 64, bf16) ask for them before length and page are known;
+// the queries' do in any case.
 // Prompts: a block has the new tokens of a page, with their angles in a table, and a warp a
 // head (or warps share one where heads are few); after the greatest magnitudes it comes for
 // keys and values again, which L2 still has.  The queries are blocks of their own here
 // too, a thread a token's unit, whose angles it works out once for several heads.
 //
 // Bound: bytes for prompts (16384 tokens, 32 + 8 heads of 128, e4m3: 80 us where the copy rate
-// admits 54; the keys and values alone 43 of 15, the queries beside them 37 of 40), latency for
-// steps (256 tokens 6.6 us, one 4.2: a launch, frequencies, length, page, old scale).  Angles
-// worked out by every thread instead of a table: 138 us; keys and values kept in registers
-// instead of asked for again: 88 to 120 (they spill).
+// admits 54; the keys and values alone 43 of 15, the queries beside them 37 of 40; into bf16 pages 70
+// of 59; from fp32 rows, angles worked out for each, 174 of 104), latency for steps (256 tokens 6.6
+// us, one 4.2: a launch, frequencies, length, page, old scale; 256 of fp32 8.3).  The table holds
+// 4096 angles, 32 KB: pages of 128 tokens, whose angles every thread works out, take 113 us.  Keys
+// and values kept in registers instead of asked for again: 88 to 120 (they spill).
 #include <cuda_fp8.h>
 
 #include "layer_common.cuh"

@@ -39,9 +39,12 @@
 // attn_join adds them.
 //
 // Bound: the bytes of the visible codes.  64 sequences of 0 to 8192 places, 8 heads of 128,
-// e4m3: 100 us where the copy rate admits 80; 1 x 131000, 2 heads of 256: 35 of 20; 32 x 4
-// tokens x 0 to 4096: 42 of 21 (twice the instructions of one token).  What is lost: a block's
-// beginning and end (3 and 4 us), and issue: 37 to 47 % of the cycles at 8 to 12 warps an SM.
+// e4m3: 97 to 112 us by the lengths drawn where the copy rate admits 81; bf16 163 to 170 of 161; 1 x
+// 131000, 2 heads of 256: 35 of 20; 32 x 4 tokens x 0 to 4096: 42 to 47 of 21 (twice the
+// instructions of one token).  What is lost: a block's beginning and end (3 and 4 us), and issue: 37
+// to 47 % of the cycles at 8 to 12 warps an SM.  Of 8 NR rows a pair, as many as registers hold, more
+// rows walk the pages again: 16 sequences of 0 to 4096, groups of 8 heads of 128, 48 us for 4 tokens
+// (32 rows), 73 for 5, 81 for 8, 145 for 16; of 256, 25 for 2 (16 rows), 31 for 4.
 #include <cuda_fp16.h>
 
 #include <type_traits>

@@ -26,8 +26,9 @@
 // index on.
 //
 // Measured, 64 x 131072 fp32 (the bytes: 5 us): the greatest alone 14 us, temperature 24,
-// top-k 50 21, 1000 29, top-p 57, equal logits with top-p 268; one such row 6.3, 11, 12, 17
-// and 25.  144 x 50257 bf16 with probabilities 33 (the bytes: 6.4).  Bound: instructions (26 a
+// top-k 50 21, 1000 29, top-p 52 to 57, equal logits with top-p 271; one such row 6.3, 11, 12, 18,
+// 26 and 98.  144 x 50257 bf16 with probabilities 33 (the bytes: 6.4).  64 x 131072 with filters as they
+// come 54, of logits that lie two apart 93.  Bound: instructions (26 a
 // weight, in each pass that needs them), and the exchanges over a cluster, 1 to 2 us each,
 // three with a temperature alone and nine with top-p.
 #include "layer_common.cuh"
